@@ -255,6 +255,108 @@ MOE_API int moe_forward_w8(const moe_dims* d, const moe_weights_w8* w, const voi
                            size_t ws_bytes, cudaStream_t stream, cudaStream_t side, cudaEvent_t ev_fork,
                            cudaEvent_t ev_join);
 
+/* ---------------------------------------------------------------------------
+ * KV cache in 8 bits: the attention beside the layer.
+ *
+ * Pools hold pages of `page` tokens; each page holds, per kv head, the e4m3
+ * codes of K and of V (row-major [page][D]) and one fp32 scale for each:
+ *   K[t] = k_scale[id][h] * e4m3(k[id][h][t % page]),  id = page_table[b][t / page]
+ * and V likewise.  Scales are finite and not negative; the codes 0x7f and 0xff
+ * (NaN) are never stored by these calls and read as +-480 (as elsewhere in
+ * this library).  Slots at or beyond a sequence's length may hold anything.
+ * Supported: D 64 or 128; page 16, 32, 64 or 128. */
+typedef struct {
+  int Hkv, D, page;
+} moe_kv_dims;
+
+/*  k, v             e4m3 [num_pages][Hkv][page][D], 16-byte aligned
+ *  k_scale, v_scale fp32 [num_pages][Hkv] */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int num_pages;
+} moe_kv_pool;
+
+/* B sequences.
+ *  page_table int32 [B][width]: the page ids of each sequence, in token order
+ *             (entries beyond a sequence's length are not read)
+ *  seq_lens   int32 [B] on the device (never read by the host)
+ *  max_len    host upper bound on seq_lens
+ * A length outside [0, max_len] or beyond width * page, packed boundaries that
+ * are not ascending or exceed the stated total, and page ids outside the pool
+ * are device-checked: a sequence that fails is skipped, a page that fails is
+ * taken as masked. */
+typedef struct {
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  int B, width, max_len;
+} moe_kv_seqs;
+
+/* Append: stores the K and V rows of new tokens.  seq_lens already counts
+ * them: sequence b's new tokens are rows cu_new[b] .. cu_new[b+1] - 1 of k and
+ * v and take the positions that end at seq_lens[b] - 1.
+ *  k, v      bf16, token rows kv_stride elements apart, [Hkv][D] within a row
+ *  cu_new    int32 [B+1] on the device, ascending from 0; cu_new[B] <= T_new
+ * Per touched (page, head), K and V apart: need = the least power of two with
+ * max|new row values| <= 448 need (2^-126 at least).  A page that already
+ * holds tokens of the sequence takes scale' = max(scale, need) and, where that
+ * grew, its older codes become e4m3(code * (scale / scale')); any other page
+ * takes scale' = need.  New codes are e4m3(x / scale'), to nearest even; products
+ * and quotients are rounded to fp32 first (they are exact for powers of two).
+ * An infinity is stored as +-448 scale', a NaN as 0, neither counts for
+ * `need`, and either records MOE_ERR_DEVICE_CHECK.  No page may be in use by
+ * two sequences of the call at the positions written. */
+MOE_API int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_seqs* s, const void* k,
+                          const void* v, int64_t kv_stride, const int32_t* cu_new, int T_new, cudaStream_t stream);
+
+/* Attention of the last tokens of each sequence over its cache.  Sequence b's
+ * queries are rows cu_q[b] .. cu_q[b+1] - 1 of q and stand at the positions
+ * that end at seq_lens[b] - 1 (append first); a query sees the tokens up to its
+ * own position.  Head h reads kv head h / (Hq / Hkv).
+ *   out = sum_t p_t V[t],  p = softmax_t(scale * q . K[t])
+ *  q       bf16, token rows q_stride elements apart, [Hq][D] within a row
+ *  cu_q    int32 [B+1] on the device; cu_q[B] <= T_q; at most max_q queries each
+ *  out     bf16 [T_q][Hq][D]
+ *  lse     fp32 [T_q][Hq] or NULL: ln sum_t exp(scale * q . K[t])
+ *  weights fp32 [B][Hkv][w_stride] or NULL, w_stride >= max_len: token t of
+ *          (sequence, kv head) gains sum p_t over the call's queries and the
+ *          heads of that kv head; other entries keep their values
+ *  ws      scratch of moe_kv_attention_workspace_bytes(...) bytes (256-byte
+ *          aligned, any content); calls that share it must not overlap on the GPU
+ * A query that sees nothing (an empty sequence, or more queries than tokens)
+ * gives out 0 and lse -inf; a query row that holds a NaN or an infinity gives
+ * NaN.  Rows of q outside every sequence are neither read nor written.
+ * Sums, maxima and outputs are held in fp32; the products' operands are exact
+ * (q, K, V) or keep 16 bits (the softmax weights, at any size).  Results do not
+ * depend on scheduling. */
+MOE_API size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int B, int T_q, int max_q, int max_len);
+MOE_API int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_seqs* s, const void* q,
+                             int64_t q_stride, int Hq, const int32_t* cu_q, int T_q, int max_q, float scale, void* out,
+                             float* lse, float* weights, int64_t w_stride, void* ws, size_t ws_bytes,
+                             cudaStream_t stream);
+
+/* Eviction by accumulated attention weight: copies the tokens that stay into
+ * the pages of dst_table, per kv head.  A sequence of at most `budget` tokens
+ * keeps all.  A longer one keeps, per head, its first `sink` and last `recent`
+ * tokens and the budget - sink - recent heaviest between them (equal weights:
+ * the lower position; a NaN counts as heaviest), in their order.
+ *  weights     fp32 [B][Hkv][w_stride], w_stride >= max_len
+ *  dst         the destination pools (may be the source's); no page that the
+ *              call reads may be among those of dst_table
+ *  dst_table   int32 [B][dst_width], dst_width * page >= min(max_len, budget)
+ *  dst_lens    int32 [B] (out): min(seq_lens[b], budget)
+ *  dst_weights fp32 [B][Hkv][budget] (out): the kept tokens' weights, then 0
+ *  kept        int32 [B][Hkv][budget] (out): their positions, then -1
+ * A destination page's scale is the largest of its rows' scales; a row from a
+ * page of another scale becomes e4m3(code * (scale / scale')).  Slots beyond
+ * dst_lens are not written. */
+MOE_API int moe_kv_evict(const moe_kv_dims* d, const moe_kv_pool* src, const moe_kv_seqs* s, const float* weights,
+                         int64_t w_stride, int budget, int sink, int recent, const moe_kv_pool* dst,
+                         const int32_t* dst_table, int dst_width, int32_t* dst_lens, float* dst_weights, int32_t* kept,
+                         cudaStream_t stream);
+
 /* Reads and clears the current device's status word (first device-side error
  * since the last read, MOE_OK if none).  Synchronises `stream`. */
 MOE_API int moe_last_device_error(cudaStream_t stream);

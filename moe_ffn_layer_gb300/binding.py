@@ -45,7 +45,22 @@ class moe_weights(ctypes.Structure):
                 ("w_down", ctypes.c_void_p), ("ws_gate_up", ctypes.c_void_p), ("ws_down", ctypes.c_void_p)]
 
 
+class moe_kv_dims(ctypes.Structure):
+    _fields_ = [("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("page", ctypes.c_int)]
+
+
+class moe_kv_pool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int)]
+
+
+class moe_kv_seqs(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("width", ctypes.c_int), ("max_len", ctypes.c_int)]
+
+
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F, _R = ctypes.c_int64, ctypes.c_float, ctypes.POINTER
 _SIGS = {
     "moe_route_workspace_bytes": (_Z, [_I, _I, _I]),
     "moe_route": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P]),
@@ -61,6 +76,12 @@ _SIGS = {
                          _P]),
     "moe_forward_w8": (_I, [ctypes.POINTER(moe_dims), ctypes.POINTER(moe_weights_w8), _P, _I, _P, _P, _Z, _P, _P,
                             _P, _P]),
+    "moe_kv_append": (_I, [_R(moe_kv_dims), _R(moe_kv_pool), _R(moe_kv_seqs), _P, _P, _L, _P, _I, _P]),
+    "moe_kv_attention_workspace_bytes": (_Z, [_R(moe_kv_dims), _I, _I, _I, _I, _I]),
+    "moe_kv_attention": (_I, [_R(moe_kv_dims), _R(moe_kv_pool), _R(moe_kv_seqs), _P, _L, _I, _P, _I, _I, _F, _P, _P,
+                              _P, _L, _P, _Z, _P]),
+    "moe_kv_evict": (_I, [_R(moe_kv_dims), _R(moe_kv_pool), _R(moe_kv_seqs), _P, _L, _I, _I, _I, _R(moe_kv_pool), _P,
+                          _I, _P, _P, _P, _P]),
     "moe_last_device_error": (_I, [_P]),
     "moe_last_launch_count": (_I, []),
     "moe_workspace_layout": (_I, [ctypes.POINTER(moe_dims), _I, ctypes.POINTER(moe_workspace_offsets)]),
@@ -181,6 +202,33 @@ def moe_forward_w8(dims: moe_dims, weights: moe_weights_w8, x, T, out, ws, ws_by
     return _check("moe_forward_w8", lib().moe_forward_w8(ctypes.byref(dims), ctypes.byref(weights), ptr(x), T,
                                                          ptr(out), ptr(ws), ws_bytes, handle(stream), handle(side),
                                                          handle(ev_fork), handle(ev_join)))
+
+
+def moe_kv_append(dims: moe_kv_dims, pool: moe_kv_pool, seqs: moe_kv_seqs, k, v, kv_stride, cu_new, T_new,
+                  stream) -> int:
+    return _check("moe_kv_append", lib().moe_kv_append(ctypes.byref(dims), ctypes.byref(pool), ctypes.byref(seqs),
+                                                       ptr(k), ptr(v), kv_stride, ptr(cu_new), T_new,
+                                                       handle(stream)))
+
+
+def moe_kv_attention_workspace_bytes(dims: moe_kv_dims, Hq: int, B: int, T_q: int, max_q: int, max_len: int) -> int:
+    return lib().moe_kv_attention_workspace_bytes(ctypes.byref(dims), Hq, B, T_q, max_q, max_len)
+
+
+def moe_kv_attention(dims: moe_kv_dims, pool: moe_kv_pool, seqs: moe_kv_seqs, q, q_stride, Hq, cu_q, T_q, max_q,
+                     scale, out, lse, weights, w_stride, ws, ws_bytes, stream) -> int:
+    return _check("moe_kv_attention", lib().moe_kv_attention(ctypes.byref(dims), ctypes.byref(pool),
+                                                             ctypes.byref(seqs), ptr(q), q_stride, Hq, ptr(cu_q),
+                                                             T_q, max_q, scale, ptr(out), ptr(lse), ptr(weights),
+                                                             w_stride, ptr(ws), ws_bytes, handle(stream)))
+
+
+def moe_kv_evict(dims: moe_kv_dims, src: moe_kv_pool, seqs: moe_kv_seqs, weights, w_stride, budget, sink, recent,
+                 dst: moe_kv_pool, dst_table, dst_width, dst_lens, dst_weights, kept, stream) -> int:
+    return _check("moe_kv_evict", lib().moe_kv_evict(ctypes.byref(dims), ctypes.byref(src), ctypes.byref(seqs),
+                                                     ptr(weights), w_stride, budget, sink, recent,
+                                                     ctypes.byref(dst), ptr(dst_table), dst_width, ptr(dst_lens),
+                                                     ptr(dst_weights), ptr(kept), handle(stream)))
 
 
 def moe_last_device_error(stream) -> int:

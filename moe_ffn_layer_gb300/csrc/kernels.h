@@ -113,6 +113,54 @@ int router_gemm_launch(const void* x, const void* wr3, int T, int H, int E, floa
 int combine_launch(const void* y, const int32_t* inv_perm, const float* topk_w, const void* shared, int T, int H,
                    int k, long long rows_max, void* out, cudaStream_t stream, int* launches);
 
+// ---------------------------------------------------------------- KV cache in 8 bits
+// moe_kv_dims, moe_kv_pool and moe_kv_seqs as kernels take them (see moe_ffn.h).
+struct KvPool {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int num_pages;
+};
+struct KvSeqs {
+  const int32_t* table;
+  const int32_t* seq_lens;
+  int B, width, max_len;
+};
+struct KvDims {
+  int Hkv, D, page;
+};
+int kv_append_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const void* k, const void* v,
+                     long long kv_stride, const int32_t* cu_new, int T_new, int* status, cudaStream_t stream,
+                     int* launches);
+struct KvAttention {
+  const void* q;
+  long long q_stride;
+  int Hq;
+  const int32_t* cu_q;
+  int T_q, max_q;
+  float scale;
+  void* out;
+  float* lse;
+  float* weights;
+  long long w_stride;
+};
+size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len);
+int kv_attention_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, void* ws,
+                        int* status, cudaStream_t stream, int* launches);
+struct KvEvict {
+  const float* weights;
+  long long w_stride;
+  int budget, sink, recent;
+  const int32_t* dst_table;
+  int dst_width;
+  int32_t* dst_lens;
+  float* dst_weights;
+  int32_t* kept;
+};
+int kv_evict_launch(const KvDims& d, const KvPool& src, const KvSeqs& s, const KvPool& dst, const KvEvict& e,
+                    int* status, cudaStream_t stream, int* launches);
+
 // Status word and SM count of the current device (first use looks them up).
 int current_device_info(int** status, int* num_sms);
 

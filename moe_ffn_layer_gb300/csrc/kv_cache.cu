@@ -1,0 +1,373 @@
+// Writing into and evicting from the 8-bit paged KV cache.
+//
+// Append: of each page that new tokens reach, one CTA per (page, head, K or V)
+// takes the largest magnitude of the page's new rows, grows the page's scale
+// where they need it (requantising the page's older rows), and stores the new
+// rows' codes.
+//
+// Evict: one CTA per (sequence, head) finds the tokens to keep by their
+// accumulated attention weight; then one CTA per destination (page, head)
+// gathers the kept rows.
+#include "kv_cache.cuh"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------- append
+constexpr int kAppendThreads = 128;
+
+// A sequence's touched pages are numbered from floor(cu[b] / page) + 2 b on: a
+// run of n > 0 tokens touches at most floor((n - 1) / page) + 2 pages, and the
+// next sequence's first number lies at least floor(n / page) + 2 further, so
+// the numbers never meet and need no prefix sum.
+__device__ __forceinline__ long long first_item(const int32_t* cu, int b, int page) {
+  return cu[b] / page + 2ll * b;
+}
+
+__device__ __forceinline__ uint32_t absmax_bits(const uint4& v) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t a = __vmaxu2(v.x & m, v.y & m), b = __vmaxu2(v.z & m, v.w & m), c = __vmaxu2(a, b);
+  return max(c & 0xFFFFu, c >> 16);
+}
+
+// The largest finite magnitude of eight bf16 (their bits), for a vector that holds a NaN or an infinity.
+__device__ __forceinline__ uint32_t absmax_finite_bits(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+    m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+  }
+  return m;
+}
+
+// x / s rounded once, a NaN as 0.  inv is 1 / s where that product is exact.
+__device__ __forceinline__ float quotient(float x, float s, float inv, bool exact) {
+  const float y = exact ? x * inv : __fdiv_rn(x, s);
+  return y == y ? y : 0.f;
+}
+
+// Bound: the bf16 rows read once and their codes written once (3 bytes a
+// value); a decode step's single rows are launch latency.  The rows stay in
+// registers between the maximum and the rounding (up to 16 vectors a thread:
+// a whole page of 128 rows of 128).
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvPool pool, KvSeqs s,
+                                                                   const __nv_bfloat16* __restrict__ kn,
+                                                                   const __nv_bfloat16* __restrict__ vn,
+                                                                   long long kv_stride, const int32_t* __restrict__ cu,
+                                                                   int T, int* status) {
+  chain_wait();
+  ChainReleaseAtExit release;
+  const long long item = blockIdx.x;
+  const int h = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  // the sequence whose numbers hold this item
+  int lo = 0, hi = s.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first_item(cu, mid, d.page) <= item) lo = mid; else hi = mid - 1;
+  }
+  const int b = lo;
+  int first, n, len;
+  if (!kv_sequence(s, cu, T, b, d.page, status, &first, &n, &len)) return;
+  const int start = len - n;
+  if (start < 0) {
+    set_status(status, MOE_ERR_DEVICE_CHECK);
+    return;
+  }
+  const long long p = start / d.page + (item - first_item(cu, b, d.page));   // page of the sequence
+  if (n == 0 || item < first_item(cu, b, d.page) || p * d.page >= len) return;
+  const int page_id = s.table[static_cast<size_t>(b) * s.width + p];
+  if (page_id < 0 || page_id >= pool.num_pages) {
+    set_status(status, MOE_ERR_DEVICE_CHECK);
+    return;
+  }
+  const int t0 = static_cast<int>(p) * d.page;
+  const int s0 = max(start - t0, 0), s1 = min(len - t0, d.page);   // slots of the new rows
+  const __nv_bfloat16* src = (is_v ? vn : kn) + static_cast<long long>(first + t0 + s0 - start) * kv_stride +
+                             static_cast<long long>(h) * d.D;
+  uint8_t* codes = (is_v ? pool.v : pool.k) + kv_row(page_id, d.Hkv, h, d.page, 0, d.D);
+  float* scale = (is_v ? pool.v_scale : pool.k_scale) + static_cast<size_t>(page_id) * d.Hkv + h;
+  const int per_row = d.D / 8, vecs = (s1 - s0) * per_row;
+  uint4 x[16];
+  uint32_t m = 0;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int j = threadIdx.x + i * kAppendThreads;
+    if (j >= vecs) break;
+    x[i] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(j / per_row) * kv_stride + j % per_row * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (threadIdx.x + i * kAppendThreads >= vecs) break;
+    uint32_t a = absmax_bits(x[i]);
+    if (a >= 0x7F80u) {
+      odd = true;
+      a = absmax_finite_bits(x[i]);
+    }
+    m = max(m, a);
+  }
+  if (odd) set_status(status, MOE_ERR_DEVICE_CHECK);
+  __shared__ uint32_t warp_max[kAppendThreads / 32];
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+  const float before = *scale;
+  __syncthreads();   // (also: every thread has read the scale before it is written)
+#pragma unroll
+  for (int i = 0; i < kAppendThreads / 32; ++i) m = max(m, warp_max[i]);
+  const float need = kv_pow2_scale(__uint_as_float(m << 16));
+  const float now = s0 > 0 ? fmaxf(before, need) : need;
+  if (threadIdx.x == 0) *scale = now;
+  if (s0 > 0 && now != before) {
+    const float ratio = __fdiv_rn(before, now);
+    for (int j = threadIdx.x; j < s0 * d.D / 16; j += kAppendThreads) {
+      uint4* at = reinterpret_cast<uint4*>(codes) + j;
+      *at = e4m3x16_scaled(*at, ratio);
+    }
+  }
+  const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0;
+  const float inv = __fdiv_rn(1.f, now);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int j = threadIdx.x + i * kAppendThreads;
+    if (j >= vecs) break;
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      c[e] = e4m3x2_of(quotient(bf16_lo(w[e]), now, inv, exact), quotient(bf16_hi(w[e]), now, inv, exact));
+    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(s0) * d.D + j * 8) =
+        make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  }
+}
+
+// ---------------------------------------------------------------- evict
+constexpr int kSelectThreads = 1024;
+
+// Order-preserving integer of a weight: larger weight, larger key; -0 as +0,
+// a NaN above everything (a token whose weight is not a number stays).
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0xFFFFFFFFu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Exclusive sum over the block of two counts packed in 16 bits each per warp
+// (a block counts at most 1024), and their totals.
+__device__ __forceinline__ void block_scan2(bool a, bool b, int* before_a, int* before_b, int* all_a, int* all_b,
+                                            int* shared) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t ba = __ballot_sync(0xFFFFFFFFu, a), bb = __ballot_sync(0xFFFFFFFFu, b);
+  const uint32_t below = (1u << lane) - 1;
+  if (lane == 0) {
+    shared[warp] = __popc(ba);
+    shared[32 + warp] = __popc(bb);
+  }
+  __syncthreads();
+  int ca = shared[lane], cb = shared[32 + lane];
+  const int all0 = __reduce_add_sync(0xFFFFFFFFu, ca), all1 = __reduce_add_sync(0xFFFFFFFFu, cb);
+  const int w0 = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? ca : 0);
+  const int w1 = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? cb : 0);
+  *before_a = w0 + __popc(ba & below);
+  *before_b = w1 + __popc(bb & below);
+  *all_a = all0;
+  *all_b = all1;
+  __syncthreads();
+}
+
+// Which tokens of (sequence b, head h) stay: all of a sequence within the
+// budget; else the first `sink`, the last `recent`, and of those between the
+// budget - sink - recent heaviest, the lower index first among equal ones.
+// Radix selection of the threshold key (11, 11 and 10 bits), then one pass in
+// index order writes the kept indices, so the result does not depend on
+// scheduling.
+__global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvSeqs s, KvEvict e, int* status) {
+  chain_wait();
+  ChainReleaseAtExit release;
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  int len = s.seq_lens[b];
+  if (len < 0 || len > s.max_len) {
+    if (tid == 0) set_status(status, MOE_ERR_DEVICE_CHECK);
+    len = 0;   // skipped: nothing is kept
+  }
+  const float* w = e.weights + (static_cast<long long>(b) * d.Hkv + h) * e.w_stride;
+  const size_t row = (static_cast<size_t>(b) * d.Hkv + h) * static_cast<size_t>(e.budget);
+  int32_t* kept = e.kept + row;
+  float* wout = e.dst_weights + row;
+  const int keep = min(len, e.budget);
+  if (h == 0 && tid == 0) e.dst_lens[b] = keep;
+  for (int j = keep + tid; j < e.budget; j += kSelectThreads) {
+    kept[j] = -1;
+    wout[j] = 0.f;
+  }
+  if (len <= e.budget) {
+    for (int j = tid; j < keep; j += kSelectThreads) {
+      kept[j] = j;
+      wout[j] = w[j];
+    }
+    return;
+  }
+  __shared__ int hist[2048];
+  __shared__ int scan[64];
+  __shared__ int pick[2];
+  const int m0 = e.sink, m1 = len - e.recent;
+  int want = e.budget - e.sink - e.recent;   // heaviest of [m0, m1) still to place
+  uint32_t prefix = 0;
+  int bits_done = 0;
+  const int widths[3] = {11, 11, 10};
+  if (want > 0) {
+    for (int pass = 0; pass < 3; ++pass) {
+      const int width = widths[pass], shift = 32 - bits_done - width, bins = 1 << width;
+      for (int i = tid; i < bins; i += kSelectThreads) hist[i] = 0;
+      __syncthreads();
+      for (int t = m0 + tid; t < m1; t += kSelectThreads) {
+        const uint32_t key = weight_key(w[t]);
+        if (bits_done == 0 || key >> (32 - bits_done) == prefix) atomicAdd(&hist[key >> shift & (bins - 1)], 1);
+      }
+      __syncthreads();
+      // from the top bin down: the bin in which the want-th largest key lies
+      const int per = bins / kSelectThreads;   // 2 or 1
+      const int top = bins - 1 - tid * per;
+      int mine = 0;
+      for (int i = 0; i < per; ++i) mine += hist[top - i];
+      int before = mine;   // inclusive sum over threads 0..tid
+      const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += up;
+      }
+      if (lane == 31) scan[warp] = before;
+      __syncthreads();
+      before += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scan[lane] : 0) - mine;
+      if (before < want && before + mine >= want) {
+        int i = 0, above = before;
+        while (above + hist[top - i] < want) above += hist[top - i++];
+        pick[0] = top - i;
+        pick[1] = want - above;
+      }
+      __syncthreads();
+      prefix = prefix << width | static_cast<uint32_t>(pick[0]);
+      want = pick[1];
+      bits_done += width;
+      __syncthreads();
+    }
+  }
+  // `prefix` is the smallest key kept, `want` how many of the equal ones
+  int done = 0, equal = 0;
+  const bool any = e.budget - e.sink - e.recent > 0;
+  for (int t0 = 0; t0 < len; t0 += kSelectThreads) {
+    const int t = t0 + tid;
+    const float x = t < len ? w[t] : 0.f;
+    const uint32_t key = weight_key(x);
+    const bool ends = t < m0 || t >= m1;
+    const bool eq = t < len && !ends && any && key == prefix;
+    int at, eq_at, n, n_eq;
+    block_scan2(eq, false, &eq_at, &at, &n_eq, &n, scan);
+    const bool stay = t < len && (ends || (any && (key > prefix || (eq && equal + eq_at < want))));
+    int unused, none;
+    block_scan2(stay, false, &at, &unused, &n, &none, scan);
+    if (stay) {
+      kept[done + at] = t;
+      wout[done + at] = x;
+    }
+    done += n;
+    equal += n_eq;
+  }
+}
+
+constexpr int kGatherThreads = 128;
+
+// One destination (page, head): its kept rows, K then V.  The page's scale is
+// the largest of its rows' scales; a row from a page of another scale has its
+// codes rescaled (exact for powers of two, except into the subnormals).
+// Bound: the kept codes read and written once.
+__global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvPool src, KvSeqs s, KvPool dst,
+                                                                   KvEvict e, int* status) {
+  chain_wait();
+  ChainReleaseAtExit release;
+  const int p = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int n = min(e.dst_lens[b] - p * d.page, d.page);   // rows of this page
+  if (n <= 0) return;
+  const int to_id = e.dst_table[static_cast<size_t>(b) * e.dst_width + p];
+  if (to_id < 0 || to_id >= dst.num_pages) {
+    if (tid == 0) set_status(status, MOE_ERR_DEVICE_CHECK);
+    return;
+  }
+  const int32_t* kept = e.kept + (static_cast<size_t>(b) * d.Hkv + h) * static_cast<size_t>(e.budget) +
+                        static_cast<size_t>(p) * d.page;
+  __shared__ size_t from[128];        // byte offset of each row in the source pools
+  __shared__ float scale[2][128];
+  __shared__ uint32_t top[2];
+  if (tid < 2) top[tid] = 0;
+  __syncthreads();
+  if (tid < n) {
+    const int t = kept[tid];
+    const int q = t / d.page;
+    int id = q < s.width ? s.table[static_cast<size_t>(b) * s.width + q] : -1;
+    if (id < 0 || id >= src.num_pages) {
+      set_status(status, MOE_ERR_DEVICE_CHECK);
+      from[tid] = ~static_cast<size_t>(0);
+      scale[0][tid] = scale[1][tid] = 0.f;
+    } else {
+      from[tid] = kv_row(id, d.Hkv, h, d.page, t % d.page, d.D);
+      const float a = src.k_scale[static_cast<size_t>(id) * d.Hkv + h], c = src.v_scale[static_cast<size_t>(id) * d.Hkv + h];
+      scale[0][tid] = a;
+      scale[1][tid] = c;
+      // scales are not negative: their bits order as they do
+      atomicMax(&top[0], __float_as_uint(a));
+      atomicMax(&top[1], __float_as_uint(c));
+    }
+  }
+  __syncthreads();
+  const int per_row = d.D / 16;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint8_t* in = kv ? src.v : src.k;
+    uint8_t* out = (kv ? dst.v : dst.k) + kv_row(to_id, d.Hkv, h, d.page, 0, d.D);
+    const float big = __uint_as_float(top[kv]);
+    if (tid == 0) (kv ? dst.v_scale : dst.k_scale)[static_cast<size_t>(to_id) * d.Hkv + h] = big;
+#pragma unroll 8
+    for (int j = tid; j < n * per_row; j += kGatherThreads) {
+      const int r = j / per_row;
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (from[r] != ~static_cast<size_t>(0)) c = *reinterpret_cast<const uint4*>(in + from[r] + j % per_row * 16);
+      if (scale[kv][r] != big) c = e4m3x16_scaled(c, __fdiv_rn(scale[kv][r], big));
+      *reinterpret_cast<uint4*>(out + static_cast<size_t>(j) * 16) = c;
+    }
+  }
+}
+
+}  // namespace
+
+int kv_append_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const void* k, const void* v,
+                     long long kv_stride, const int32_t* cu_new, int T_new, int* status, cudaStream_t stream,
+                     int* launches) {
+  const dim3 grid(static_cast<unsigned>(T_new / d.page + 2ll * s.B), 2u * d.Hkv);
+  if (launch_chained(kv_append_kernel, grid, dim3(kAppendThreads), 0, stream, d, pool, s,
+                     static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), kv_stride, cu_new,
+                     T_new, status) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  ++*launches;
+  return MOE_OK;
+}
+
+int kv_evict_launch(const KvDims& d, const KvPool& src, const KvSeqs& s, const KvPool& dst, const KvEvict& e,
+                    int* status, cudaStream_t stream, int* launches) {
+  if (launch_chained(kv_select_kernel, dim3(d.Hkv, s.B), dim3(kSelectThreads), 0, stream, d, s, e, status) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  ++*launches;
+  const int most = s.max_len < e.budget ? s.max_len : e.budget;
+  const int pages = (most + d.page - 1) / d.page;
+  if (pages == 0) return MOE_OK;
+  if (launch_chained(kv_gather_kernel, dim3(pages, d.Hkv, s.B), dim3(kGatherThreads), 0, stream, d, src, s, dst, e,
+                     status) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  ++*launches;
+  return MOE_OK;
+}
+
+}  // namespace moe

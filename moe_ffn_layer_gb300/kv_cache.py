@@ -1,0 +1,142 @@
+"""The 8-bit paged KV cache of one attention layer, held on one CUDA device: code
+pools, scales and the attention's workspace.  PyTorch provides the memory and
+the streams; each method is one call of a C entry point (``moe_kv_append``,
+``moe_kv_attention``, ``moe_kv_evict``; their meaning, layouts and device-side
+checks are documented in ``include/moe_ffn.h``).  Which pages belong to which
+sequence is the caller's: ``page_table`` int32 [B, width] and ``seq_lens`` int32
+[B], both on the device.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+
+class KVCache8:
+    """k, v: uint8 [num_pages, Hkv, page, D] e4m3 codes; k_scale, v_scale: fp32
+    [num_pages, Hkv].  D is 64 or 128, page 16, 32, 64 or 128 tokens."""
+
+    def __init__(self, num_pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda"):
+        shape = (num_pages, kv_heads, page, head_dim)
+        self._hold(torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.zeros(shape, dtype=torch.uint8, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+    @classmethod
+    def from_tensors(cls, k, v, k_scale, v_scale) -> "KVCache8":
+        """Over existing pools (not copied)."""
+        self = cls.__new__(cls)
+        self._hold(k, v, k_scale, v_scale)
+        return self
+
+    def _hold(self, k, v, k_scale, v_scale):
+        self.device = k.device
+        _want("k", k, torch.uint8, 4, self.device)
+        _want("v", v, torch.uint8, 4, self.device, k.shape)
+        _want("k_scale", k_scale, torch.float32, 2, self.device, k.shape[:2])
+        _want("v_scale", v_scale, torch.float32, 2, self.device, k.shape[:2])
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page, self.head_dim = k.shape
+        self.dims = B.moe_kv_dims(self.kv_heads, self.head_dim, self.page)
+        self.pool = B.moe_kv_pool(*(B.ptr(t) for t in (k, v, k_scale, v_scale)), self.num_pages)
+        self._ws = {}   # by stream: calls of different streams may overlap
+
+    def _seqs(self, page_table, seq_lens, max_len):
+        _want("page_table", page_table, torch.int32, 2, self.device)
+        _want("seq_lens", seq_lens, torch.int32, 1, self.device, page_table.shape[:1])
+        n, width = page_table.shape
+        return B.moe_kv_seqs(B.ptr(page_table), B.ptr(seq_lens), n, width, max_len)
+
+    def _stream(self, stream):
+        return stream if stream is not None else torch.cuda.current_stream(self.device)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+               cu_new: torch.Tensor, stream=None) -> None:
+        """Stores the new tokens' k and v (bf16 [T, Hkv, D], rows any equal
+        stride apart); seq_lens already counts them, cu_new int32 [B+1] says
+        whose they are."""
+        T = k.shape[0]
+        for name, t in (("k", k), ("v", v)):
+            _want(name, t, torch.bfloat16, 3, self.device, (T, self.kv_heads, self.head_dim), rows=True)
+        if T > 1 and k.stride(0) != v.stride(0):
+            raise ValueError(f"k and v rows lie {k.stride(0)} and {v.stride(0)} elements apart")
+        _want("cu_new", cu_new, torch.int32, 1, self.device, (page_table.shape[0] + 1,))
+        seqs = self._seqs(page_table, seq_lens, page_table.shape[1] * self.page)
+        stride = k.stride(0) if T > 1 else self.kv_heads * self.head_dim
+        B.moe_kv_append(self.dims, self.pool, seqs, k, v, stride, cu_new, T, self._stream(stream))
+
+    def workspace(self, need: int, stream) -> torch.Tensor:
+        """The stream's workspace, of at least `need` bytes."""
+        key = B.handle(stream)
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < need:
+            with torch.cuda.stream(stream):
+                ws = self._ws[key] = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        return ws
+
+    def attend(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor, max_q: int,
+               max_len: int, scale: float | None = None, weights: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """out bf16 [T, Hq, D]: attention of the queries q (bf16 [T, Hq, D], rows
+        any stride apart), the last tokens of their sequences, over the cache.
+        max_q and max_len bound the queries and the length of a sequence; scale
+        defaults to D ** -0.5.  lse fp32 [T, Hq], where given, takes the
+        log-sum-exps; weights fp32 [B, Hkv, >= max_len], where given, gains the
+        softmax weights."""
+        T, Hq = q.shape[0], q.shape[1]
+        _want("q", q, torch.bfloat16, 3, self.device, (T, Hq, self.head_dim), rows=True)
+        _want("cu_q", cu_q, torch.int32, 1, self.device, (page_table.shape[0] + 1,))
+        seqs = self._seqs(page_table, seq_lens, max_len)
+        stream = self._stream(stream)
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty((T, Hq, self.head_dim), dtype=torch.bfloat16, device=self.device)
+        _want("out", out, torch.bfloat16, 3, self.device, (T, Hq, self.head_dim))
+        if lse is not None:
+            _want("lse", lse, torch.float32, 2, self.device, (T, Hq))
+        if weights is not None:
+            _want("weights", weights, torch.float32, 3, self.device, (seqs.B, self.kv_heads, weights.shape[2]))
+        need = B.moe_kv_attention_workspace_bytes(self.dims, Hq, seqs.B, T, max_q, max_len)
+        ws = self.workspace(need, stream)
+        B.moe_kv_attention(self.dims, self.pool, seqs, q, q.stride(0) if T > 1 else Hq * self.head_dim, Hq, cu_q, T,
+                           max_q, self.head_dim ** -0.5 if scale is None else scale, out, lse, weights,
+                           0 if weights is None else weights.shape[2], ws, ws.numel(), stream)
+        return out
+
+    def evict(self, weights: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int, budget: int,
+              sink: int, recent: int, dst_table: torch.Tensor, dst: "KVCache8 | None" = None, stream=None):
+        """Keeps at most `budget` tokens of each sequence and kv head (its first
+        `sink`, its last `recent`, the heaviest between by `weights` fp32 [B,
+        Hkv, >= max_len]), copied into the pages of dst_table int32 [B, width]
+        of `dst` (default: this cache; none of them a page that is read).
+        Returns (lengths int32 [B], the kept weights fp32 [B, Hkv, budget], the
+        kept positions int32 [B, Hkv, budget])."""
+        dst = self if dst is None else dst
+        if dst.k.shape[1:] != self.k.shape[1:]:
+            raise ValueError(f"dst holds pages of {tuple(dst.k.shape[1:])}, not {tuple(self.k.shape[1:])}")
+        seqs = self._seqs(page_table, seq_lens, max_len)
+        _want("weights", weights, torch.float32, 3, self.device, (seqs.B, self.kv_heads, weights.shape[2]))
+        _want("dst_table", dst_table, torch.int32, 2, self.device, (seqs.B, dst_table.shape[1]))
+        stream = self._stream(stream)
+        shape = (seqs.B, self.kv_heads, max(budget, 0))
+        with torch.cuda.stream(stream):
+            lens = torch.empty(seqs.B, dtype=torch.int32, device=self.device)
+            kept_w = torch.empty(shape, dtype=torch.float32, device=self.device)
+            kept = torch.empty(shape, dtype=torch.int32, device=self.device)
+        B.moe_kv_evict(self.dims, self.pool, seqs, weights, weights.shape[2], budget, sink, recent, dst.pool,
+                       dst_table, dst_table.shape[1], lens, kept_w, kept, stream)
+        return lens, kept_w, kept
+
+
+def _want(name, t, dtype, ndim, device, shape=None, rows=False):
+    """Raises ValueError unless t is a tensor of that type, shape and device,
+    contiguous (rows: within each row of its first axis)."""
+    if t.dtype != dtype or t.dim() != ndim or t.device != device:
+        raise ValueError(f"{name}: want {ndim}-d {dtype} on {device}, got {t.dim()}-d {t.dtype} on {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: want shape {tuple(shape)}, got {tuple(t.shape)}")
+    flat = t[0] if rows and t.shape[0] > 0 else t
+    if not flat.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
