@@ -129,6 +129,7 @@ struct KvSeqs {
 };
 struct KvDims {
   int Hkv, D, page;
+  int shift;   // page = 1 << shift
 };
 int kv_append_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const void* k, const void* v,
                      long long kv_stride, const int32_t* cu_new, int T_new, int* status, cudaStream_t stream,
@@ -145,7 +146,7 @@ struct KvAttention {
   float* weights;
   long long w_stride;
 };
-size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len);
+size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int T_q);
 int kv_attention_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, void* ws,
                         int* status, cudaStream_t stream, int* launches);
 struct KvEvict {

@@ -22,7 +22,9 @@ int check_seqs(const moe_kv_seqs* s) {
 }
 
 // what a call with work to do needs of its pool and sequences
-int check_pointers(const moe_kv_pool* p, const moe_kv_seqs* s) {
+int check_pointers(const moe_kv_dims* d, const moe_kv_pool* p, const moe_kv_seqs* s) {
+  // (the rows of a pool are counted in 32 bits: 2^32 of 64 bytes pass the card's memory with K and V)
+  if (static_cast<uint64_t>(p->num_pages) * d->Hkv * d->page > UINT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (!s->seq_lens || (s->width > 0 && !s->page_table)) return MOE_ERR_INVALID;
   if (p->num_pages > 0 && (!p->k || !p->v || !p->k_scale || !p->v_scale)) return MOE_ERR_INVALID;
   if (!aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->k_scale, 4) || !aligned(p->v_scale, 4) ||
@@ -31,7 +33,7 @@ int check_pointers(const moe_kv_pool* p, const moe_kv_seqs* s) {
   return MOE_OK;
 }
 
-moe::KvDims dims_of(const moe_kv_dims* d) { return {d->Hkv, d->D, d->page}; }
+moe::KvDims dims_of(const moe_kv_dims* d) { return {d->Hkv, d->D, d->page, __builtin_ctz(d->page)}; }
 moe::KvPool pool_of(const moe_kv_pool* p) {
   return {static_cast<uint8_t*>(p->k), static_cast<uint8_t*>(p->v), p->k_scale, p->v_scale, p->num_pages};
 }
@@ -51,7 +53,7 @@ int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_se
   if (kv_stride % 8) return MOE_ERR_UNSUPPORTED;
   if (T_new == 0 || s->B == 0) return MOE_OK;
   if (!k || !v || !cu_new) return MOE_ERR_INVALID;
-  if ((rc = check_pointers(pool, s))) return rc;
+  if ((rc = check_pointers(d, pool, s))) return rc;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_new, 4)) return MOE_ERR_UNSUPPORTED;
   int* status = nullptr;
   int sms = 0, n = 0;
@@ -61,9 +63,9 @@ int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_se
   return rc;
 }
 
-size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int B, int T_q, int max_q, int max_len) {
-  if (check_dims(d) || Hq <= 0 || Hq % d->Hkv || B < 0 || T_q < 0 || max_q < 0 || max_len < 0) return 0;
-  return moe::kv_attention_ws_bytes(dims_of(d), Hq, B, T_q, max_q, max_len);
+size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int T_q) {
+  if (check_dims(d) || Hq <= 0 || Hq % d->Hkv || T_q < 0) return 0;
+  return moe::kv_attention_ws_bytes(dims_of(d), Hq, T_q);
 }
 
 int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_seqs* s, const void* q,
@@ -77,12 +79,12 @@ int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv
   if (q_stride % 8 || static_cast<int64_t>(max_q) * Hq > INT_MAX) return MOE_ERR_UNSUPPORTED;
   if (T_q == 0 || max_q == 0 || s->B == 0) return MOE_OK;
   if (!q || !cu_q || !out || !ws) return MOE_ERR_INVALID;
-  if ((rc = check_pointers(pool, s))) return rc;
+  if ((rc = check_pointers(d, pool, s))) return rc;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cu_q, 4) || !aligned(lse, 4) || !aligned(weights, 4) ||
       !aligned(ws, 256))
     return MOE_ERR_UNSUPPORTED;
   const moe::KvDims kd = dims_of(d);
-  if (ws_bytes < moe::kv_attention_ws_bytes(kd, Hq, s->B, T_q, max_q, s->max_len)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < moe::kv_attention_ws_bytes(kd, Hq, T_q)) return MOE_ERR_WORKSPACE;
   int* status = nullptr;
   int sms = 0, n = 0;
   if ((rc = moe::current_device_info(&status, &sms))) return rc;
@@ -104,7 +106,7 @@ int moe_kv_evict(const moe_kv_dims* d, const moe_kv_pool* src, const moe_kv_seqs
   if (static_cast<int64_t>(dst_width) * d->page < most) return MOE_ERR_INVALID;
   if (s->B == 0) return MOE_OK;
   if (!weights || !dst_lens || !dst_weights || !kept || (dst_width > 0 && !dst_table)) return MOE_ERR_INVALID;
-  if ((rc = check_pointers(src, s)) || (rc = check_pointers(dst, s))) return rc;
+  if ((rc = check_pointers(d, src, s)) || (rc = check_pointers(d, dst, s))) return rc;
   if (!aligned(weights, 4) || !aligned(dst_table, 4) || !aligned(dst_lens, 4) || !aligned(dst_weights, 4) ||
       !aligned(kept, 4))
     return MOE_ERR_UNSUPPORTED;

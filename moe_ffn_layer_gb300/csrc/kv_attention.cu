@@ -10,17 +10,21 @@
 //
 // Both products run on the tensor cores with fp32 accumulation, their operands
 // exact or kept to 16 bits at least:
-//  - scores: f16.  A K code becomes f16 exactly: its sign at bit 15 and its
-//    seven other bits at bits 13..7 read as the code's value times 2^-8
-//    (subnormals included); the factor 2^8 goes into the score's scale.  A
-//    query row is scaled by a power of two to a largest magnitude in
-//    [2^7, 2^8), which keeps all of a bf16's bits down to 2^-21 of it.
+//  - scores: e4m3 MMAs, a K code as it is (no conversion).  A query row is
+//    scaled by a power of two to a largest magnitude in [2^7, 2^8) and enters
+//    as two e4m3 terms, hi = e4m3(x) and lo = e4m3(16 (x - hi)), with a sum
+//    each: together a bf16's eight bits, down to 2^-21 of the row's largest.
+//    (The e4m3 MMA rounds its sums as fp32 additions do, measured; the f16 one,
+//    which would also need K converted, truncates them and runs at half the
+//    rate per instruction for half the depth.)
 //  - output: bf16, which has fp32's range.  A V code becomes bf16 exactly; a
 //    weight p * vs enters as two bf16 terms, so that it keeps 16 bits however
 //    far it lies below the row's largest (a long sequence's many small weights
 //    count as they should, whatever the pages' scales).
 // Any code byte reads as a finite value, so what lies beyond a sequence's end
 // never turns a masked product into a NaN.
+#include <limits.h>
+
 #include "kv_cache.cuh"
 
 namespace moe {
@@ -29,8 +33,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTok = 32;          // tokens of a warp's step
 constexpr int kWarps = 4;
+constexpr int kSpan = kWarps * kTok;   // tokens of a CTA's step: one step of each warp
+constexpr int kStages = 2;
+constexpr float kSlack = 8.f;
+constexpr int kLeast = 2;              // steps that a CTA takes at least
 constexpr int kSMs = 152;         // of a GB300: the plan of a call depends on its sizes alone
-constexpr int kStages = 3;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -38,24 +45,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The bytes of v that sel picks (two code bytes, each followed by its sign
-// copy) as two f16 of 2^-8 times the codes' values.
-template <uint32_t kSel>
-__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t v) {
-  return (prmt(v, 0u, kSel) << 7) & 0xBF80BF80u;
-}
-// The same as two bf16 of the codes' values.
+// copy) as two bf16 of the codes' values.
 template <uint32_t kSel>
 __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t v) {
   return bf16x2_mul((prmt(v, 0u, kSel) << 4) & 0x87F087F0u, 0x7B807B80u);   // times 2^120: e4m3's bias for bf16's
 }
-constexpr uint32_t kBytes01 = 0x9180u, kBytes23 = 0xB3A2u, kBytes02 = 0xA280u, kBytes13 = 0xB391u;
+constexpr uint32_t kBytes02 = 0xA280u, kBytes13 = 0xB391u;
 
 // Two floats as bf16 pairs hi + lo: hi the upper halves as they are, lo what
 // is left, rounded (16 bits in all).
@@ -65,15 +61,15 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t* hi, uin
   *lo = pack_bf16x2(a - __uint_as_float(ua & 0xFFFF0000u), b - __uint_as_float(ub & 0xFFFF0000u));
 }
 
-// d += a (16x16, row) * b (16x8, col), f16 inputs, fp32 accumulator
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// d += a (16x32, row) * b (32x8, col), e4m3 inputs, fp32 accumulator
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// the same with bf16 inputs
+// d += a (16x16, row) * b (16x8, col), bf16 inputs, fp32 accumulator
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -92,6 +88,12 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void cp_async_wait() {
@@ -106,22 +108,27 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// A tile's query rows as MMA operands.  The MMA's K index may stand for any
-// order of the head dimension as long as both operands agree: lane (n, c) of a
-// K operand holds 16-byte chunk 2c + h of token n's row (chunk c for D = 64),
-// four codes d..d+3 per K step, so the query operand of step 4h + r holds
-// d = 16 (2c + h) + 4r + {0, 1} and + {2, 3}.  A tile has 8 R rows, R = 1 or 2
-// per lane: lane/4 and lane/4 + 8 (zeros for R = 1).
+// Four floats to two words of four e4m3 codes: hi, and lo = e4m3(16 (x - hi)).
+__device__ __forceinline__ void split_e4m3x4(float a, float b, float c, float d, uint32_t* hi, uint32_t* lo) {
+  const uint32_t h = e4m3x2_of(a, b) | e4m3x2_of(c, d) << 16;
+  *hi = h;
+  *lo = e4m3x2_of(16.f * (a - e4m3_to_f32(h)), 16.f * (b - e4m3_to_f32(h >> 8))) |
+        e4m3x2_of(16.f * (c - e4m3_to_f32(h >> 16)), 16.f * (d - e4m3_to_f32(h >> 24))) << 16;
+}
+
+// A tile's 8 R query rows as MMA operands, R = 1 or 2 of them per lane: lane/4
+// and lane/4 + 8.  With R = 1 the MMA's upper eight rows take the lo terms.
+// The MMA's K index may stand for any order of the head dimension as long as
+// both operands agree: lane (n, c) of a K operand holds 16-byte chunk 2c + h of
+// token n's row (chunk c for D = 64), eight codes per K step, so the query
+// operand of step 2h + r holds d = 16 (2c + h) + 8r + {0..3} and + {4..7}.
 template <int D, int R>
 struct QueryTile {
-  uint32_t a[D / 16][4];
-  float unscale[R];   // scale * log2(e) * 2^8 / (the row's power of two)
+  uint32_t a[R][D / 32][4];   // R = 1: {hi, lo}; R = 2: hi, then lo
+  float unscale[R];           // scale * log2(e) / (the row's power of two)
 
   __device__ __forceinline__ void load(const KvAttention& at, int first, int h, int g, int row0, int rows, int lane) {
     const int c = lane & 3;
-    uint32_t raw[D / 16][4];
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) a[k][1] = a[k][3] = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int r = row0 + (lane >> 2) + 8 * i;
@@ -129,14 +136,14 @@ struct QueryTile {
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(at.q) +
                                static_cast<long long>(first + (real ? r / g : 0)) * at.q_stride +
                                (static_cast<long long>(h) * g + (real ? r % g : 0)) * D;
+      uint4 raw[D / 32];
       uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int d0 = (D == 128 ? 16 * (2 * c + (k >> 2)) : 16 * c) + 4 * (k & 3);
-        const uint2 v = real ? __ldg(reinterpret_cast<const uint2*>(q + d0)) : make_uint2(0, 0);
-        raw[k][i] = v.x;
-        raw[k][2 + i] = v.y;
-        m = __vmaxu2(m, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+      for (int k = 0; k < D / 32; ++k) {
+        const int d0 = (D == 128 ? 16 * (2 * c + (k >> 1)) : 16 * c) + 8 * (k & 1);
+        raw[k] = real ? __ldg(reinterpret_cast<const uint4*>(q + d0)) : make_uint4(0, 0, 0, 0);
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(raw[k].x & 0x7FFF7FFFu, raw[k].y & 0x7FFF7FFFu),
+                                 __vmaxu2(raw[k].z & 0x7FFF7FFFu, raw[k].w & 0x7FFF7FFFu)));
       }
       m = max(m & 0xFFFFu, m >> 16);
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
@@ -145,31 +152,44 @@ struct QueryTile {
       // infinity in the row makes its scores NaN
       const uint32_t e = max(m >> 7, 8u);   // biased exponent of the largest
       const float up = __uint_as_float((261 - e) << 23), down = __uint_as_float((e - 7) << 23);
-      unscale[i] = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : at.scale * kLog2e * 256.f * down;
+      unscale[i] = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : at.scale * kLog2e * down;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        a[k][i] = pack_f16x2(bf16_lo(raw[k][i]) * up, bf16_hi(raw[k][i]) * up);
-        a[k][2 + i] = pack_f16x2(bf16_lo(raw[k][2 + i]) * up, bf16_hi(raw[k][2 + i]) * up);
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t hi[2], lo[2];
+        split_e4m3x4(bf16_lo(raw[k].x) * up, bf16_hi(raw[k].x) * up, bf16_lo(raw[k].y) * up, bf16_hi(raw[k].y) * up,
+                     &hi[0], &lo[0]);
+        split_e4m3x4(bf16_lo(raw[k].z) * up, bf16_hi(raw[k].z) * up, bf16_lo(raw[k].w) * up, bf16_hi(raw[k].w) * up,
+                     &hi[1], &lo[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          a[0][k][2 * j + i] = hi[j];
+          a[R - 1][k][2 * j + (R == 1 ? 1 : i)] = lo[j];
+        }
       }
     }
   }
 };
 
-// s[nt] = raw scores of the tile's rows and 8 tokens each (in units that QueryTile::unscale and the page's scale undo)
+// s[nt] = raw scores of the lane's rows and two tokens of each eight (in units
+// that QueryTile::unscale and the page's scale undo)
 template <int D, int R>
-__device__ __forceinline__ void scores(float (&s)[kTok / 8][4], const QueryTile<D, R>& q, uint32_t k_tile, int lane) {
+__device__ __forceinline__ void scores(float (&s)[kTok / 8][2 * R], const QueryTile<D, R>& q, uint32_t k_tile,
+                                       int lane) {
   const int n = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < kTok / 8; ++nt) {
-    s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    float acc[R][4] = {};
 #pragma unroll
     for (int half = 0; half < D / 64; ++half) {
       const uint4 v = lds_u4(k_tile + swz<D>(nt * 8 + n, D == 128 ? 2 * c + half : c));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        mma_f16(s[nt], q.a[4 * half + r], codes_to_f16x2<kBytes01>(w[r]), codes_to_f16x2<kBytes23>(w[r]));
+      for (int r = 0; r < R; ++r) {
+        mma_e4m3(acc[r], q.a[r][2 * half], v.x, v.y);
+        mma_e4m3(acc[r], q.a[r][2 * half + 1], v.z, v.w);
+      }
     }
+#pragma unroll
+    for (int e = 0; e < 2 * R; ++e) s[nt][e] = fmaf(R == 1 ? acc[0][e + 2] : acc[R - 1][e], 0.0625f, acc[0][e]);
   }
 }
 
@@ -194,45 +214,74 @@ struct Tile {
   __device__ __forceinline__ int sees(int r, int g) const { return max(len - n + min(r, rows - 1) / g + 1, 0); }
 };
 
-// One warp's ring of token steps in shared memory.
+// One warp's ring of 32-token steps in shared memory.  A step is two halves of
+// 16 tokens (a page holds whole halves).
 template <int D>
 struct Ring {
   static constexpr int kStageBytes = 2 * kTok * D;
-  uint32_t base;       // kStages x (K rows, V rows)
-  float* scales;       // kStages x {ks, ks, vs, vs} of the step's two 16-token halves (a page holds whole halves)
-  // Starts the copies of tokens [t0, t0 + 32); rows at or beyond `end` are zeros.
-  __device__ __forceinline__ void fetch(int stage, const KvDims& d, const KvPool& pool, const KvSeqs& s, int b, int h,
-                                        int t0, int end, int lane, int* status) const {
-    constexpr int kChunks = D / 16, kRowsAtOnce = 32 / kChunks;
-    int id[2];
-    bool ok[2];
+  uint32_t base;         // stages x (K rows, V rows)
+  float* scales;         // stages x {ks, ks, vs, vs} of the halves
+  // The page ids of a step, asked for a step before copy() needs them.
+  __device__ __forceinline__ void look(int (&id)[2], const KvDims& d, const KvSeqs& s, int b, int t0, int end) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = t0 + 16 * i;
-      id[i] = t < end ? __ldg(s.table + static_cast<size_t>(b) * s.width + t / d.page) : -1;
-      ok[i] = id[i] >= 0 && id[i] < pool.num_pages;
-      if (t < end && !ok[i]) set_status(status, MOE_ERR_DEVICE_CHECK);
+      id[i] = t < end ? __ldg(s.table + static_cast<size_t>(b) * s.width + (t >> d.shift)) : -1;
     }
+  }
+  // Starts the copies of tokens [t0, t0 + 32); rows at or beyond `end` are zeros.
+  __device__ __forceinline__ void copy(int stage, const int (&id)[2], const KvDims& d, const KvPool& pool, int h,
+                                       int t0, int end, int lane, int* status) const {
+    constexpr int kChunks = D / 16, kRowsAtOnce = 32 / kChunks;
     const uint32_t k = base + stage * kStageBytes, v = k + kTok * D;
+    const int row = lane / kChunks, c = lane % kChunks;
+    const uint32_t pages = pool.num_pages;
+    if (t0 + kTok <= end && static_cast<uint32_t>(id[0]) < pages && static_cast<uint32_t>(id[1]) < pages) {
 #pragma unroll
-    for (int j = 0; j < kTok / kRowsAtOnce; ++j) {
-      const int r = j * kRowsAtOnce + lane / kChunks, c = lane % kChunks, i = j * kRowsAtOnce >> 4;
-      const bool in = ok[i] && t0 + r < end;
-      const size_t at = in ? kv_row(id[i], d.Hkv, h, d.page, (t0 + r) % d.page, D) + c * 16 : 0;
-      cp_async16(k + swz<D>(r, c), pool.k + at, in);
-      cp_async16(v + swz<D>(r, c), pool.v + at, in);
+      for (int i = 0; i < 2; ++i) {
+        const size_t at = kv_row(id[i], d.Hkv, h, d.page, ((t0 + 16 * i) & (d.page - 1)) + row, D) + c * 16;
+        const uint8_t *ks = pool.k + at, *vs = pool.v + at;
+#pragma unroll
+        for (int j = 0; j < 16; j += kRowsAtOnce) {
+          const uint32_t to = swz<D>(16 * i + j + row, c);
+          cp_async16(k + to, ks + j * D);
+          cp_async16(v + to, vs + j * D);
+        }
+      }
+      if (lane < 4)
+        cp_async4(smem_u32(scales + stage * 4 + lane), (lane < 2 ? pool.k_scale : pool.v_scale) +
+                                                           static_cast<size_t>(lane & 1 ? id[1] : id[0]) * d.Hkv + h);
+      return;
     }
-    if (lane < 4) {
-      const int i = lane & 1;
-      // a page that is not there: a NaN of its own, taken as masked
-      scales[stage * 4 + lane] = ok[i] ? __ldg((lane < 2 ? pool.k_scale : pool.v_scale) +
-                                               static_cast<size_t>(id[i]) * d.Hkv + h)
-                                       : (lane < 2 ? __uint_as_float(0x7FFFFFFFu) : 0.f);
+    // the sequence ends here, or a page is not there
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + 16 * i;
+      const bool ok = static_cast<uint32_t>(id[i]) < pages;
+      if (t < end && !ok) set_status(status, MOE_ERR_DEVICE_CHECK);
+      const size_t at = ok ? kv_row(id[i], d.Hkv, h, d.page, (t & (d.page - 1)) + row, D) + c * 16 : 0;
+#pragma unroll
+      for (int j = 0; j < 16; j += kRowsAtOnce) {
+        const bool in = ok && t + j + row < end;
+        const uint32_t to = swz<D>(16 * i + j + row, c);
+        cp_async16(k + to, pool.k + at + (in ? j * D : 0), in);
+        cp_async16(v + to, pool.v + at + (in ? j * D : 0), in);
+      }
+      if ((lane & 1) == i && lane < 4) {
+        float* to = scales + stage * 4 + lane;
+        const size_t of = static_cast<size_t>(ok ? id[i] : 0) * d.Hkv + h;
+        if (ok)
+          cp_async4(smem_u32(to), (lane < 2 ? pool.k_scale : pool.v_scale) + of);
+        else   // a page that is not there: a NaN of its own, taken as masked
+          *to = lane < 2 ? __uint_as_float(0x7FFFFFFFu) : 0.f;
+      }
     }
   }
 };
 
 __device__ __forceinline__ bool no_page(float k_scale) { return __float_as_uint(k_scale) == 0x7FFFFFFFu; }
+
+__device__ __forceinline__ float exp2_diff(float a, float b) { return a == -INFINITY ? 0.f : exp2_approx(a - b); }
 
 // Running softmax and output of a warp's rows.  For R = 1 the MMA's upper
 // eight rows take the weights' low terms, so o[..][2..3] adds to o[..][0..1].
@@ -253,106 +302,60 @@ struct State {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][p][i] = 0.f;
   }
-};
 
-// 2^(a - b), 0 where a is -inf (also against b = -inf)
-__device__ __forceinline__ float exp2_diff(float a, float b) { return a == -INFINITY ? 0.f : exp2_approx(a - b); }
-
-// Partial results of one (row, head) of one chunk, relative to its own maximum: in the workspace, [T_q * Hq][chunks].
-struct Partials {
-  float* o;      // [..][D]
-  float2* ml;    // running maximum (base 2) and sum
-  int chunks;    // per row
-  int chunk;     // tokens of a chunk
-};
-
-// Grid: (chunk, row tile) x kv head x sequence.  Each warp takes every
-// kWarps-th 32-token step of the chunk through its own ring, with its own
-// running softmax; the warps' states meet in shared memory at the end.
-template <int D, int R>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(KvDims d, KvPool pool, KvSeqs s, KvAttention at,
-                                                                      Partials part, int* status) {
-  constexpr int kRows = 8 * R;
-  extern __shared__ __align__(128) uint8_t smem[];
-  chain_wait();
-  ChainReleaseAtExit release;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int chunk = blockIdx.x % part.chunks, mt = blockIdx.x / part.chunks, h = blockIdx.y, b = blockIdx.z;
-  const int g = at.Hq / d.Hkv;
-  Tile tile;
-  if (!tile.find(s, at, b, g, mt, kRows, d.page, status)) return;
-  const int begin = chunk * part.chunk;
-  if (begin >= tile.seen && chunk > 0) return;
-  const int end = min(begin + part.chunk, tile.seen);
-  const int steps = (end - begin + kTok - 1) / kTok;   // may be 0: rows that see nothing
-
-  Ring<D> ring{smem_u32(smem) + warp * kStages * Ring<D>::kStageBytes,
-               reinterpret_cast<float*>(smem + kWarps * kStages * Ring<D>::kStageBytes) + warp * kStages * 4};
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    const int st = warp + i * kWarps;
-    if (st < steps) ring.fetch(i, d, pool, s, b, h, begin + st * kTok, end, lane, status);
-    cp_async_commit();
-  }
-  QueryTile<D, R> q;
-  q.load(at, tile.first, h, g, tile.row0, tile.rows, lane);
-  State<D, R> x;
-  x.clear();
-  int sees[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) sees[i] = tile.sees(tile.row0 + (lane >> 2) + 8 * i, g);
-  const int sees_least = tile.sees(tile.row0, g);
-  int stage = 0;
-  for (int st = warp; st < steps; st += kWarps) {
-    {
-      const int next = st + (kStages - 1) * kWarps;
-      __syncwarp();   // every lane is done with the stage that is filled now
-      if (next < steps)
-        ring.fetch(stage == 0 ? kStages - 1 : stage - 1, d, pool, s, b, h, begin + next * kTok, end, lane, status);
-      cp_async_commit();
-    }
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
+  // One step: the ring stage's 32 tokens from t0 on; row i sees those below sees[i].
+  __device__ __forceinline__ void add(const QueryTile<D, R>& q, const Ring<D>& ring, int stage, int t0,
+                                      const int (&sees)[R], int sees_least, int lane) {
     const uint32_t k_tile = ring.base + stage * Ring<D>::kStageBytes, v_tile = k_tile + kTok * D;
-    const float ks0 = ring.scales[stage * 4], ks1 = ring.scales[stage * 4 + 1];
-    const float vs0 = ring.scales[stage * 4 + 2], vs1 = ring.scales[stage * 4 + 3];
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-    float sc[kTok / 8][4];
+    const float4 page = *reinterpret_cast<const float4*>(ring.scales + stage * 4);
+    const float ks0 = page.x, ks1 = page.y, vs0 = page.z, vs1 = page.w;
+    float sc[kTok / 8][2 * R];
     scores<D, R>(sc, q, k_tile, lane);
-    const int t0 = begin + st * kTok;
-    const bool masks = t0 + kTok > sees_least || no_page(ks0) || no_page(ks1);
-    float m[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float f0 = ks0 * q.unscale[i], f1 = ks1 * q.unscale[i];
+#pragma unroll
+      for (int nt = 0; nt < kTok / 8; ++nt) {
+        sc[nt][2 * i] *= nt < 2 ? f0 : f1;
+        sc[nt][2 * i + 1] *= nt < 2 ? f0 : f1;
+      }
+    }
+    if (t0 + kTok > sees_least || no_page(ks0) || no_page(ks1)) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int nt = 0; nt < kTok / 8; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (t0 + nt * 8 + 2 * (lane & 3) + e >= sees[i] || no_page(nt < 2 ? ks0 : ks1)) sc[nt][2 * i + e] = -INFINITY;
+    }
+    // The maximum that the exponents are taken against follows the scores only
+    // where they pass it by more than 2^kSlack: the weights then stay below
+    // 2^kSlack, which costs no accuracy, and o is seldom rescaled.
+    float top[R];
     bool grew = false;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      m[i] = x.m[i];
+      top[i] = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < kTok / 8; ++nt) {
-        const float ks = nt < 2 ? ks0 : ks1;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& v = sc[nt][2 * i + e];
-          v *= ks * q.unscale[i];
-          if (masks && (t0 + nt * 8 + 2 * (lane & 3) + e >= sees[i] || no_page(ks))) v = -INFINITY;
-          m[i] = fmaxf(m[i], v);
-        }
-      }
-      m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 1));
-      m[i] = fmaxf(m[i], __shfl_xor_sync(0xFFFFFFFFu, m[i], 2));
-      grew |= m[i] != x.m[i];
+      for (int nt = 0; nt < kTok / 8; ++nt) top[i] = fmaxf(top[i], fmaxf(sc[nt][2 * i], sc[nt][2 * i + 1]));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], 2));
+      grew |= top[i] > m[i] + kSlack;
     }
     if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const float f = exp2_diff(x.m[i], m[i]);
-        x.m[i] = m[i];
-        x.l[i] *= f;
+        top[i] = fmaxf(top[i], m[i]);
+        const float f = exp2_diff(m[i], top[i]);
+        m[i] = top[i];
+        l[i] *= f;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int e = 2 * i; e < (R == 1 ? 4 : 2 * i + 2); ++e) x.o[j][p][e] *= f;
+            for (int e = 2 * i; e < (R == 1 ? 4 : 2 * i + 2); ++e) o[j][p][e] *= f;
       }
     }
     uint32_t hi[kTok / 16][4], lo[kTok / 16][4];   // R = 1: both terms in hi
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(KvDims d, 
       for (int nt = 0; nt < kTok / 8; ++nt) {
         const float vs = nt < 2 ? vs0 : vs1;
         const float p0 = exp2_approx(sc[nt][2 * i] - base), p1 = exp2_approx(sc[nt][2 * i + 1] - base);
-        x.l[i] += p0 + p1;
+        l[i] += p0 + p1;
         uint32_t* a = hi[nt >> 1] + 2 * (nt & 1);
         split_bf16x2(p0 * vs, p1 * vs, a + i, R == 1 ? a + 1 : lo[nt >> 1] + 2 * (nt & 1) + i);
       }
@@ -376,111 +379,345 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(KvDims d, 
       for (int k = 0; k < kTok / 16; ++k) {
         const uint32_t even0 = codes_to_bf16x2<kBytes02>(v[2 * k]), even1 = codes_to_bf16x2<kBytes02>(v[2 * k + 1]);
         const uint32_t odd0 = codes_to_bf16x2<kBytes13>(v[2 * k]), odd1 = codes_to_bf16x2<kBytes13>(v[2 * k + 1]);
-        mma_bf16(x.o[j][0], hi[k], even0, even1);
-        mma_bf16(x.o[j][1], hi[k], odd0, odd1);
+        mma_bf16(o[j][0], hi[k], even0, even1);
+        mma_bf16(o[j][1], hi[k], odd0, odd1);
         if (R == 2) {
-          mma_bf16(x.o[j][0], lo[k], even0, even1);
-          mma_bf16(x.o[j][1], lo[k], odd0, odd1);
+          mma_bf16(o[j][0], lo[k], even0, even1);
+          mma_bf16(o[j][1], lo[k], odd0, odd1);
         }
       }
     }
   }
-  cp_async_wait<0>();
-  __syncthreads();   // the rings become the meeting place: kWarps x kRows x (D + 4 outputs, {m, l})
-  constexpr int kPitch = D + 4;
-  float* all_o = reinterpret_cast<float*>(smem);
-  float2* all_ml = reinterpret_cast<float2*>(smem + kWarps * kRows * kPitch * sizeof(float));
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    float l = x.l[i];
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    const int r = (lane >> 2) + 8 * i;
-    if ((lane & 3) == 0) all_ml[warp * kRows + r] = make_float2(x.m[i], l);
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {   // even and odd columns of the V bytes interleave: d = 16 j + 4 c + 0..3
-      float v[2][2];
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) v[p][e] = x.o[j][p][2 * i + e] + (R == 1 ? x.o[j][p][2 + e] : 0.f);
-      *reinterpret_cast<float4*>(all_o + (warp * kRows + r) * kPitch + 16 * j + 4 * (lane & 3)) =
-          make_float4(v[0][0], v[1][0], v[0][1], v[1][1]);
-    }
+
+  // Columns 16 j + 4 (lane % 4) .. + 3 of the lane's row i: even and odd
+  // columns of the V bytes interleave.
+  __device__ __forceinline__ float4 out(int j, int i) const {
+    if (R == 1) return make_float4(o[j][0][0] + o[j][0][2], o[j][1][0] + o[j][1][2], o[j][0][1] + o[j][0][3], o[j][1][1] + o[j][1][3]);
+    return make_float4(o[j][0][2 * i], o[j][1][2 * i], o[j][0][2 * i + 1], o[j][1][2 * i + 1]);
   }
-  __syncthreads();
-  const bool alone = tile.seen <= part.chunk;   // the only chunk of this tile: the result, not a part
-  for (int i = threadIdx.x; i < kRows * D / 4; i += kWarps * 32) {
-    const int r = i / (D / 4), c = i % (D / 4) * 4;
-    if (tile.row0 + r >= tile.rows) break;
+  __device__ __forceinline__ void give(float* to, int lane) const {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        *reinterpret_cast<float4*>(to + ((lane >> 2) + 8 * i) * (D + 4) + 16 * j + 4 * (lane & 3)) = out(j, i);
+  }
+  // this state times own plus the given one times other (by row)
+  __device__ __forceinline__ void take(const float* from, const float (&own)[R], const float (&other)[R], int lane) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(from + ((lane >> 2) + 8 * i) * (D + 4) + 16 * j + 4 * (lane & 3));
+        const float4 x = out(j, i);
+        o[j][0][2 * i] = x.x * own[i] + v.x * other[i];
+        o[j][1][2 * i] = x.y * own[i] + v.y * other[i];
+        o[j][0][2 * i + 1] = x.z * own[i] + v.z * other[i];
+        o[j][1][2 * i + 1] = x.w * own[i] + v.w * other[i];
+        if (R == 1) o[j][0][2] = o[j][0][3] = o[j][1][2] = o[j][1][3] = 0.f;
+      }
+  }
+};
+
+// The work of a call: units (sequence, kv head, row tile), each of as many
+// steps as its sequence has spans of 128 tokens, one after another in that
+// order.  CTA c of n takes steps [c q + min(c, r), ...) of the total n q + r,
+// so all end together whatever the lengths; a unit cut between CTAs is joined
+// by the CTA that finishes last.
+struct Cursor {
+  int b, h, mt, step;              // where
+  int first, n, len, tiles, steps;   // of sequence b: queries, length; its row tiles and its spans
+  int seen;                          // tokens that the last real row of tile mt sees
+  // sequence b's sizes; no units where it has no rows or fails its checks
+  __device__ __forceinline__ void sequence(const KvDims& d, const KvSeqs& s, const KvAttention& at, int tile_rows,
+                                           int* status) {
+    tiles = 0;
+    steps = 1;
+    if (!kv_sequence(s, at.cu_q, at.T_q, b, d.page, status, &first, &n, &len)) return;
+    if (n > at.max_q) {
+      set_status(status, MOE_ERR_DEVICE_CHECK);
+      return;
+    }
+    tiles = (n * (at.Hq / d.Hkv) + tile_rows - 1) / tile_rows;
+    steps = max((len + kSpan - 1) / kSpan, 1);
+  }
+  __device__ __forceinline__ void look(int g, int tile_rows) {
+    seen = max(len - n + (min((mt + 1) * tile_rows, n * g) - 1) / g + 1, 0);
+  }
+  __device__ __forceinline__ void next(const KvDims& d, const KvSeqs& s, const KvAttention& at, int tile_rows,
+                                       int* status) {
+    if (++step < steps) return;
+    step = 0;
+    if (++mt == tiles) {
+      mt = 0;
+      if (++h == d.Hkv) {
+        h = 0;
+        do {
+          if (++b >= s.B) return;
+          sequence(d, s, at, tile_rows, status);
+        } while (tiles == 0);
+      }
+    }
+    if (tiles > 1 || h == 0) look(at.Hq / d.Hkv, tile_rows);
+  }
+};
+
+// Steps of sequence b.
+__device__ __forceinline__ uint32_t steps_of(Cursor& c, int b, const KvDims& d, const KvSeqs& s,
+                                              const KvAttention& at, int tile_rows, int* status) {
+  if (b >= s.B) return 0;
+  c.b = b;
+  c.sequence(d, s, at, tile_rows, status);
+  return static_cast<uint32_t>(c.tiles) * c.steps * d.Hkv;
+}
+
+// Workspace of a call: tickets (zero between calls), and two slots of partial
+// results per CTA: slot 0 for the unit that an earlier CTA began, slot 1 for
+// the one that it began itself.
+constexpr int kMostCtas = 512;
+struct Parts {
+  int* ticket;   // by the CTA that began the unit
+  float* o;      // [CTA][2][rows][D], relative to the row's maximum
+  float2* ml;    // [CTA][2][rows]: maximum (base 2) and sum
+};
+
+// The n parts of a unit, in order: a warp takes every kWarps-th row, a lane D / 32 columns.
+template <int D, int R>
+__device__ __forceinline__ void join_parts(const Parts& parts, int c0, int n, const KvAttention& at, int first, int h,
+                                           int g, int row0, int rows, int warp, int lane) {
+  constexpr int kRows = 8 * R, kPer = D / 32;
+  for (int r = warp; r < kRows && row0 + r < rows; r += kWarps) {
+    const auto slot = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kRows + r; };
     float m = -INFINITY;
+    for (int p = lane; p < n; p += 32) m = fmaxf(m, __ldcg(parts.ml + slot(p)).x);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, all_ml[w * kRows + r].x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = all_ml[w * kRows + r];
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float acc[kPer] = {}, l = 0.f;
+#pragma unroll 8
+    for (int p = 0; p < n; ++p) {
+      const float2 ml = __ldcg(parts.ml + slot(p));
       const float f = exp2_diff(ml.x, m);
-      const float4 v = *reinterpret_cast<const float4*>(all_o + (w * kRows + r) * kPitch + c);
-      l += ml.y != ml.y ? ml.y : f * ml.y;   // (a NaN sum belongs to a row of NaN scores, whose maximum is -inf)
-      o.x += f * v.x;
-      o.y += f * v.y;
-      o.z += f * v.z;
-      o.w += f * v.w;
+      l += ml.y != ml.y ? ml.y : f * ml.y;
+      const float* o = parts.o + slot(p) * D + lane * kPer;
+      if (kPer == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
+        acc[0] += f * v.x;
+        acc[1] += f * v.y;
+        acc[kPer - 2] += f * v.z;
+        acc[kPer - 1] += f * v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+        acc[0] += f * v.x;
+        acc[1] += f * v.y;
+      }
     }
-    const int row = tile.row0 + r;
-    const size_t at_row = static_cast<size_t>(tile.first + row / g) * at.Hq + h * g + row % g;
-    if (alone) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D + c) =
-          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-      if (c == 0 && at.lse) at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    } else {
-      const size_t slot = at_row * part.chunks + chunk;
-      *reinterpret_cast<float4*>(part.o + slot * D + c) = o;
-      if (c == 0) part.ml[slot] = make_float2(m, l);
-    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row = row0 + r;
+    const size_t at_row = static_cast<size_t>(first + row / g) * at.Hq + h * g + row % g;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D + lane * kPer);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && at.lse) at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
-// Joins the chunks of every row whose tile had more than one: a warp per (row, head), the chunks in order.
-template <int D>
-__global__ void __launch_bounds__(128) kv_join_kernel(KvDims d, KvSeqs s, KvAttention at, Partials part, int tile_rows,
-                                                      int* status) {
+template <int R>
+constexpr int ctas_per_sm() { return R == 1 ? 3 : 2; }   // (registers; measured: three of two stages beat two of three)
+
+// Bound: HBM (2 D bytes per token and kv head, read once).  Each of a CTA's
+// four warps takes a quarter of every 128-token span, with a ring of
+// asynchronous copies and a running softmax of its own; the ring runs on
+// across units.  At a unit's end the warps' states meet in shared memory.
+template <int D, int R>
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kernel(KvDims d, KvPool pool, KvSeqs s,
+                                                                                 KvAttention at, Parts parts,
+                                                                                 int* status) {
+  constexpr int kRows = 8 * R, kPitch = D + 4;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 all_ml[kWarps * kRows];
+  __shared__ int last;
   chain_wait();
   ChainReleaseAtExit release;
-  const int lane = threadIdx.x & 31, g = at.Hq / d.Hkv;
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 5);   // (query, head) of sequence b
-  const int b = blockIdx.y;
-  const int query = i / at.Hq, head = i % at.Hq;
-  Tile tile;
-  if (query >= at.max_q || !tile.find(s, at, b, g, 0, tile_rows, d.page, status) || query >= tile.n) return;
-  tile.find(s, at, b, g, (query * g + head % g) / tile_rows, tile_rows, d.page, status);
-  if (tile.seen <= part.chunk) return;
-  const int n = (tile.seen + part.chunk - 1) / part.chunk;
-  const size_t at_row = static_cast<size_t>(tile.first + query) * at.Hq + head;
-  const float2* ml = part.ml + at_row * part.chunks;
-  float m = -INFINITY;
-  for (int c = lane; c < n; c += 32) m = fmaxf(m, ml[c].x);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = at.Hq / d.Hkv;
+  Cursor cur;
+  uint32_t total = 0;   // (below 2^31: checked on the host for the largest lengths)
+  for (int base = 0; base < s.B; base += 32)
+    total += __reduce_add_sync(0xFFFFFFFFu, steps_of(cur, base + lane, d, s, at, kRows, status));
+  const uint32_t ctas = min((total + kLeast - 1) / kLeast, gridDim.x), cta = blockIdx.x;
+  if (cta >= ctas) return;
+  const uint32_t q = total / ctas, r = total - q * ctas;
+  const uint32_t start = cta * q + min(cta, r);
+  const int count = static_cast<int>(q + (cta < r));
+  uint32_t before = 0;   // the sequence, unit and step at `start`
+  for (int base = 0;; base += 32) {
+    const uint32_t w = steps_of(cur, base + lane, d, s, at, kRows, status);
+    uint32_t upto = w;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  constexpr int kPer = D / 32;
-  float acc[kPer] = {};
-  float l = 0.f;
-  for (int c = 0; c < n; ++c) {
-    const float2 x = ml[c];
-    const float f = exp2_diff(x.x, m);
-    l += x.y != x.y ? x.y : f * x.y;
-    const float* o = part.o + (at_row * part.chunks + c) * D + lane * kPer;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += f * o[e];
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += up;
+    }
+    const uint32_t beyond = __ballot_sync(0xFFFFFFFFu, before + upto > start);
+    if (beyond) {
+      const int l = __ffs(beyond) - 1;
+      const uint32_t in = start - before - __shfl_sync(0xFFFFFFFFu, upto - w, l);
+      cur.b = base + l;
+      cur.sequence(d, s, at, kRows, status);
+      const uint32_t unit = in / cur.steps;
+      cur.step = static_cast<int>(in - unit * cur.steps);
+      cur.h = static_cast<int>(unit / cur.tiles);
+      cur.mt = static_cast<int>(unit - cur.h * cur.tiles);
+      cur.look(g, kRows);
+      break;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D + lane * kPer);
+  Ring<D> ring{smem_u32(smem) + warp * kStages * Ring<D>::kStageBytes,
+               reinterpret_cast<float*>(smem + kWarps * kStages * Ring<D>::kStageBytes) + warp * kStages * 4};
+  float* meet = reinterpret_cast<float*>(smem + kWarps * kStages * (Ring<D>::kStageBytes + 16));
+  Cursor ahead = cur;   // the step that is copied next
+  int id[2];
+  ring.look(id, d, s, ahead.b, ahead.step * kSpan + warp * kTok, ahead.seen);
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && at.lse) at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < count) {
+      ring.copy(i, id, d, pool, ahead.h, ahead.step * kSpan + warp * kTok, ahead.seen, lane, status);
+      if (i + 1 < count) {
+        ahead.next(d, s, at, kRows, status);
+        ring.look(id, d, s, ahead.b, ahead.step * kSpan + warp * kTok, ahead.seen);
+      }
+    }
+    cp_async_commit();
+  }
+  QueryTile<D, R> query;
+  State<D, R> x;
+  int sees[R], sees_least = 0, row0 = 0, rows = 0;
+  int stage = 0;
+  bool fresh = true;   // the unit that cur is in begins, for this CTA
+  int from = cur.step;
+  for (int i = 0; i < count; ++i) {
+    __syncwarp();   // every lane is done with the stage that is filled now
+    if (i + kStages - 1 < count) {
+      ring.copy((stage + kStages - 1) % kStages, id, d, pool, ahead.h, ahead.step * kSpan + warp * kTok, ahead.seen,
+                lane, status);
+      if (i + kStages < count) {
+        ahead.next(d, s, at, kRows, status);
+        ring.look(id, d, s, ahead.b, ahead.step * kSpan + warp * kTok, ahead.seen);
+      }
+    }
+    cp_async_commit();
+    if (fresh) {
+      fresh = false;
+      from = cur.step;
+      row0 = cur.mt * kRows;
+      rows = cur.n * g;
+      query.load(at, cur.first, cur.h, g, row0, rows, lane);
+      x.clear();
+#pragma unroll
+      for (int j = 0; j < R; ++j)   // (rows beyond the last real one see what it sees)
+        sees[j] = max(cur.len - cur.n + min(row0 + (lane >> 2) + 8 * j, rows - 1) / g + 1, 0);
+      sees_least = max(cur.len - cur.n + row0 / g + 1, 0);
+    }
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const int t0 = cur.step * kSpan + warp * kTok;
+    if (t0 < cur.seen) x.add(query, ring, stage, t0, sees, sees_least, lane);
+    stage = (stage + 1) % kStages;
+    const bool whole = cur.step + 1 == cur.steps;
+    if (whole || i + 1 == count) {
+      // the warps' states meet: 2 and 3 hand theirs to 0 and 1, then 1 to 0
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        float l = x.l[j];
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+        if ((lane & 3) == 0) all_ml[warp * kRows + (lane >> 2) + 8 * j] = make_float2(x.m[j], l);
+      }
+      if (warp >= 2) x.give(meet + (warp - 2) * kRows * kPitch, lane);
+      __syncthreads();
+      float m[R], l[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const float2* ml = all_ml + (lane >> 2) + 8 * j;
+        m[j] = fmaxf(fmaxf(ml[0].x, ml[kRows].x), fmaxf(ml[2 * kRows].x, ml[3 * kRows].x));
+        l[j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 v = ml[w * kRows];   // (a NaN sum belongs to a row of NaN scores, whose maximum is -inf)
+          l[j] += v.y != v.y ? v.y : exp2_diff(v.x, m[j]) * v.y;
+        }
+      }
+      if (warp < 2) {
+        float own[R], other[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          own[j] = exp2_diff(x.m[j], m[j]);
+          other[j] = exp2_diff(all_ml[(warp + 2) * kRows + (lane >> 2) + 8 * j].x, m[j]);
+        }
+        x.take(meet + warp * kRows * kPitch, own, other, lane);
+      }
+      __syncthreads();
+      if (warp == 1) x.give(meet, lane);
+      __syncthreads();
+      const bool begun = from == 0;
+      if (warp == 0) {
+        float one[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) one[j] = 1.f;
+        x.take(meet, one, one, lane);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const int row = row0 + (lane >> 2) + 8 * j;
+          if (row < rows) {
+            const size_t at_row = static_cast<size_t>(cur.first + row / g) * at.Hq + cur.h * g + row % g;
+            const size_t slot = (static_cast<size_t>(cta) * 2 + begun) * kRows + (lane >> 2) + 8 * j;
+            const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const float4 o = x.out(c, j);
+              const int col = 16 * c + 4 * (lane & 3);
+              if (begun && whole)
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D + col) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+              else
+                *reinterpret_cast<float4*>(parts.o + slot * D + col) = o;
+            }
+            if ((lane & 3) == 0) {
+              if (!(begun && whole))
+                parts.ml[slot] = make_float2(m[j], l[j]);
+              else if (at.lse)
+                at.lse[at_row] = l[j] == 0.f ? -INFINITY : (m[j] + log2f(l[j])) * kLn2;
+            }
+          }
+        }
+      }
+      if (!(begun && whole)) {
+        // the CTAs of this unit's first and last step; the last to arrive joins their parts in order
+        const uint32_t u0 = start + i - cur.step, u1 = u0 + cur.steps - 1;
+        const auto owner = [&](uint32_t t) {
+          const uint32_t longer = r * (q + 1);
+          return static_cast<int>(t < longer ? t / (q + 1) : r + (t - longer) / q);
+        };
+        const int c0 = owner(u0), n_parts = owner(u1) - c0 + 1;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          __threadfence();
+          last = atomicAdd(parts.ticket + c0, 1) == n_parts - 1;
+          __threadfence();
+        }
+        __syncthreads();
+        if (last) {
+          if (threadIdx.x == 0) parts.ticket[c0] = 0;
+          join_parts<D, R>(parts, c0, n_parts, at, cur.first, cur.h, g, row0, rows, warp, lane);
+        }
+      }
+      __syncthreads();   // `meet` is free again
+      fresh = true;
+    }
+    if (i + 1 < count) cur.next(d, s, at, kRows, status);
+  }
+  cp_async_wait<0>();
 }
 
 // weights[b][h][t] += sum over the rows of (b, h) of exp(s_t - lse): a warp per
@@ -497,7 +734,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv_weights_kernel(KvDims d, KvPoo
   if (!tile.find(s, at, b, g, 0, 16, d.page, status) || t0 >= tile.len) return;
   Ring<D> ring{smem_u32(smem) + warp * Ring<D>::kStageBytes,
                reinterpret_cast<float*>(smem + kWarps * Ring<D>::kStageBytes) + warp * 4};
-  ring.fetch(0, d, pool, s, b, h, t0, tile.len, lane, status);
+  int id[2];
+  ring.look(id, d, s, b, t0, tile.len);
+  ring.copy(0, id, d, pool, h, t0, tile.len, lane, status);
   cp_async_commit();
   cp_async_wait<0>();
   __syncwarp();
@@ -541,64 +780,55 @@ __global__ void __launch_bounds__(kWarps * 32) kv_weights_kernel(KvDims d, KvPoo
     }
 }
 
-// How a call is cut: tokens of a chunk, chunks of a row, and the workspace behind them.
-struct Plan {
-  int rows;   // of a tile: 8 where every sequence's rows fit, else 16
-  int chunk, chunks, tiles;
+// Workspace: the tickets first, at the same place for every call, then the parts, then the log-sum-exps.
+struct Layout {
   size_t o, ml, lse, total;
 };
+Layout layout(const KvDims& d, int Hq, int T_q) {
+  constexpr size_t slots = static_cast<size_t>(kSMs) * ctas_per_sm<2>() * 2 * 16;
+  static_assert(slots >= static_cast<size_t>(kSMs) * ctas_per_sm<1>() * 2 * 8, "slots of 8-row tiles");
+  static_assert(kSMs * ctas_per_sm<1>() <= kMostCtas && kSMs * ctas_per_sm<2>() <= kMostCtas, "tickets");
+  Layout w{};
+  w.o = align_up(kMostCtas * sizeof(int));
+  w.ml = w.o + align_up(slots * d.D * sizeof(float));
+  w.lse = w.ml + align_up(slots * sizeof(float2));
+  w.total = w.lse + align_up(static_cast<size_t>(T_q) * Hq * sizeof(float));
+  return w;
+}
 
-Plan plan(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len) {
-  Plan p{};
-  const int g = Hq / d.Hkv;
-  p.rows = static_cast<long long>(max_q) * g <= 8 ? 8 : 16;
-  p.tiles = static_cast<int>((static_cast<long long>(max_q) * g + p.rows - 1) / p.rows);
-  // enough CTAs for four rounds of two per SM, chunks of at least 256 tokens
-  const long long units = static_cast<long long>(B) * d.Hkv * p.tiles;
-  const long long want = (8ll * kSMs + units - 1) / (units > 0 ? units : 1);
-  long long chunk = (max_len + want - 1) / want;
-  chunk = (chunk + kWarps * kTok - 1) / (kWarps * kTok) * (kWarps * kTok);
-  p.chunk = static_cast<int>(chunk < 256 ? 256 : chunk);
-  p.chunks = max_len > p.chunk ? static_cast<int>((static_cast<long long>(max_len) + p.chunk - 1) / p.chunk) : 1;
-  const size_t rows = static_cast<size_t>(T_q) * Hq;
-  size_t at = 0;
-  auto take = [&](size_t bytes) {
-    const size_t r = at;
-    at += align_up(bytes);
-    return r;
-  };
-  p.lse = take(rows * sizeof(float));
-  if (p.chunks > 1) {
-    p.ml = take(rows * p.chunks * sizeof(float2));
-    p.o = take(rows * p.chunks * d.D * sizeof(float));
-  }
-  p.total = at;
-  return p;
+template <int D, int R>
+int launch_decode(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, const Parts& parts,
+                  int* status, cudaStream_t stream, int* launches) {
+  constexpr size_t smem = kWarps * kStages * (Ring<D>::kStageBytes + 16) + 2 * 8 * R * (D + 4) * sizeof(float);
+  if (cudaFuncSetAttribute(kv_decode_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  // no more CTAs than the longest call of these sizes gives steps to
+  const long long tiles = (static_cast<long long>(a.max_q) * (a.Hq / d.Hkv) + 8 * R - 1) / (8 * R);
+  const double steps = static_cast<double>(s.B) * d.Hkv * tiles * ((static_cast<long long>(s.max_len) + kSpan - 1) / kSpan + 1);
+  if (steps > INT_MAX) return MOE_ERR_UNSUPPORTED;
+  const double most = steps / kLeast + 1;
+  const int ctas = most < kSMs * ctas_per_sm<R>() ? static_cast<int>(most) : kSMs * ctas_per_sm<R>();
+  if (launch_chained(kv_decode_kernel<D, R>, dim3(ctas), dim3(kWarps * 32), smem, stream, d, pool, s, a, parts,
+                     status) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  ++*launches;
+  return MOE_OK;
 }
 
 template <int D>
 int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, void* ws, int* status,
            cudaStream_t stream, int* launches) {
-  const Plan p = plan(d, a.Hq, s.B, a.T_q, a.max_q, s.max_len);
+  const Layout w = layout(d, a.Hq, a.T_q);
   uint8_t* base = static_cast<uint8_t*>(ws);
-  if (a.weights && !a.lse) a.lse = reinterpret_cast<float*>(base + p.lse);
-  const Partials part{reinterpret_cast<float*>(base + p.o), reinterpret_cast<float2*>(base + p.ml), p.chunks, p.chunk};
-  const size_t ring = kWarps * kStages * (Ring<D>::kStageBytes + 4 * sizeof(float));
-  const size_t meet = kWarps * p.rows * ((D + 4) * sizeof(float) + sizeof(float2));
-  const size_t smem = ring > meet ? ring : meet;
-  const auto kernel = p.rows == 8 ? kv_attention_kernel<D, 1> : kv_attention_kernel<D, 2>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  if (launch_chained(kernel, dim3(static_cast<unsigned>(p.chunks) * p.tiles, d.Hkv, s.B), dim3(kWarps * 32), smem,
-                     stream, d, pool, s, a, part, status) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  ++*launches;
-  if (p.chunks > 1) {
-    const unsigned rows = static_cast<unsigned>((static_cast<long long>(a.max_q) * a.Hq + 3) / 4);
-    if (launch_chained(kv_join_kernel<D>, dim3(rows, s.B), dim3(128), 0, stream, d, s, a, part, p.rows, status) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    ++*launches;
-  }
+  if (a.weights && !a.lse) a.lse = reinterpret_cast<float*>(base + w.lse);
+  const Parts parts{reinterpret_cast<int*>(base), reinterpret_cast<float*>(base + w.o),
+                    reinterpret_cast<float2*>(base + w.ml)};
+  // tiles of 8 rows where every sequence's rows fit one, else of 16
+  const int rc = static_cast<long long>(a.max_q) * (a.Hq / d.Hkv) <= 8
+                     ? launch_decode<D, 1>(d, pool, s, a, parts, status, stream, launches)
+                     : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
+  if (rc) return rc;
   if (a.weights) {
     const unsigned blocks = (static_cast<unsigned>(s.max_len) + kWarps * kTok - 1) / (kWarps * kTok);
     if (launch_chained(kv_weights_kernel<D>, dim3(blocks, d.Hkv, s.B), dim3(kWarps * 32),
@@ -612,9 +842,7 @@ int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, 
 
 }  // namespace
 
-size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len) {
-  return plan(d, Hq, B, T_q, max_q, max_len).total;
-}
+size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int T_q) { return layout(d, Hq, T_q).total; }
 
 int kv_attention_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, void* ws,
                         int* status, cudaStream_t stream, int* launches) {

@@ -8,9 +8,11 @@
 namespace moe {
 
 // Row of a code pool ([num_pages][Hkv][page][D]) that holds slot `slot` of a
-// page for one head, as a byte offset (64 bits: a pool can pass 4 GB).
+// page for one head, as a byte offset (64 bits: a pool can pass 4 GB; its rows
+// fit 32, which the host checks).
 __device__ __forceinline__ size_t kv_row(int page_id, int Hkv, int h, int page, int slot, int D) {
-  return ((static_cast<size_t>(page_id) * Hkv + h) * page + slot) * static_cast<size_t>(D);
+  const uint32_t row = (static_cast<uint32_t>(page_id) * Hkv + h) * page + slot;
+  return static_cast<size_t>(row) * static_cast<uint32_t>(D);
 }
 
 // The least power of two s with amax <= 448 s (448 = 1.75 * 2^8, the largest

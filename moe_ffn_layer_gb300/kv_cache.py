@@ -68,12 +68,13 @@ class KVCache8:
         B.moe_kv_append(self.dims, self.pool, seqs, k, v, stride, cu_new, T, self._stream(stream))
 
     def workspace(self, need: int, stream) -> torch.Tensor:
-        """The stream's workspace, of at least `need` bytes."""
+        """The stream's workspace, of at least `need` bytes, zero-filled when
+        allocated (the library keeps its counters zero from call to call)."""
         key = B.handle(stream)
         ws = self._ws.get(key)
         if ws is None or ws.numel() < need:
             with torch.cuda.stream(stream):
-                ws = self._ws[key] = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+                ws = self._ws[key] = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
         return ws
 
     def attend(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor, max_q: int,
@@ -98,7 +99,7 @@ class KVCache8:
             _want("lse", lse, torch.float32, 2, self.device, (T, Hq))
         if weights is not None:
             _want("weights", weights, torch.float32, 3, self.device, (seqs.B, self.kv_heads, weights.shape[2]))
-        need = B.moe_kv_attention_workspace_bytes(self.dims, Hq, seqs.B, T, max_q, max_len)
+        need = B.moe_kv_attention_workspace_bytes(self.dims, Hq, T)
         ws = self.workspace(need, stream)
         B.moe_kv_attention(self.dims, self.pool, seqs, q, q.stride(0) if T > 1 else Hq * self.head_dim, Hq, cu_q, T,
                            max_q, self.head_dim ** -0.5 if scale is None else scale, out, lse, weights,
