@@ -149,6 +149,9 @@ struct KvAttention {
 size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int T_q);
 int kv_attention_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, void* ws,
                         int* status, cudaStream_t stream, int* launches);
+// The attention for many query rows per sequence (tcgen05): out, and lse where given.
+int kv_prefill_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, int* status,
+                      cudaStream_t stream, int* launches);
 struct KvEvict {
   const float* weights;
   long long w_stride;

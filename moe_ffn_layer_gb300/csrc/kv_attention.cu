@@ -35,6 +35,7 @@ constexpr int kTok = 32;          // tokens of a warp's step
 constexpr int kWarps = 4;
 constexpr int kSpan = kWarps * kTok;   // tokens of a CTA's step: one step of each warp
 constexpr int kStages = 2;
+constexpr int kDecodeRows = 64;        // query rows of a kv head up to which the decode kernel is taken
 constexpr float kSlack = 8.f;
 constexpr int kLeast = 2;              // steps that a CTA takes at least
 constexpr int kSMs = 152;         // of a GB300: the plan of a call depends on its sizes alone
@@ -824,8 +825,11 @@ int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, 
   if (a.weights && !a.lse) a.lse = reinterpret_cast<float*>(base + w.lse);
   const Parts parts{reinterpret_cast<int*>(base), reinterpret_cast<float*>(base + w.o),
                     reinterpret_cast<float2*>(base + w.ml)};
-  // tiles of 8 rows where every sequence's rows fit one, else of 16
-  const int rc = static_cast<long long>(a.max_q) * (a.Hq / d.Hkv) <= 8
+  // tiles of 8 rows where every sequence's rows fit one, else of 16; many rows go to the tcgen05 kernel
+  const long long rows = static_cast<long long>(a.max_q) * (a.Hq / d.Hkv);
+  const int rc = rows > kDecodeRows
+                     ? kv_prefill_launch(d, pool, s, a, status, stream, launches)
+                 : rows <= 8
                      ? launch_decode<D, 1>(d, pool, s, a, parts, status, stream, launches)
                      : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
   if (rc) return rc;
