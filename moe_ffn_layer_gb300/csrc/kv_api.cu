@@ -17,7 +17,8 @@ int check_dims(const moe_kv_dims* d) {
 
 int check_seqs(const moe_kv_seqs* s) {
   if (!s || s->B < 0 || s->width < 0 || s->max_len < 0) return MOE_ERR_INVALID;
-  if (s->B > 65535) return MOE_ERR_UNSUPPORTED;   // a grid's z
+  // (a grid's z; positions a few tiles past the end still fit an int)
+  if (s->B > 65535 || s->max_len > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

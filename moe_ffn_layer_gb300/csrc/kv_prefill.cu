@@ -3,7 +3,7 @@
 // kv_attention.cu's; rows are (query, head) pairs of one kv head.
 //
 // A CTA takes two tiles of 128 rows of one (sequence, kv head) over the tokens
-// that they see, 128 at a time:
+// that they see, 64 at a time:
 //  - four warps convert the tokens' codes into shared memory, K to f16 and V to
 //    bf16 (both exact), in the 128-byte swizzle of the MMA's operands;
 //  - one thread issues the MMAs: S = Q K^T (f16, accumulator in tensor memory),
@@ -13,7 +13,8 @@
 //    P takes the tensor memory of S: the 32 columns of 32 tokens' scores become
 //    16 of their weights' high bf16 terms and 16 of the low ones (16 bits in
 //    all, at any size, as in the decode kernel), so PV is two MMAs per step.
-// The two tiles alternate: one's softmax runs under the other's MMAs.
+// A tile's S has two buffers, so that the scores of the next step are there when
+// a softmax ends, and neither it nor the MMAs wait for each other's last piece.
 //
 // A page's V scale is 2^e times a mantissa in [1, 2): 2^e goes into the V
 // operand (exact), the mantissa into the weights' exponent, and the row's sum
@@ -25,11 +26,15 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 128;              // rows of a tile, and tokens of a step
-constexpr int kThreads = 416;           // 2 x 4 softmax warps, 4 converter warps, 1 MMA warp
-constexpr int kConverter0 = 256, kMmaWarp = 12;
+constexpr int kTile = 128;              // rows of a tile
+constexpr int kStep = 64;               // tokens of a step
+constexpr int kRing = 4;                // steps of K and of V in shared memory
+// Warps: 0 issues the MMAs (the scheduler favours the lowest), 1 to 4 and 5 to 8
+// are the tiles' softmax, 9 to 12 convert.
+constexpr int kThreads = 416;
+constexpr int kSoftmaxWarp = 1, kConvertWarp = 9;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;           // see the decode kernel: the maximum follows beyond 2^8 only
+constexpr uint32_t kLarge = 0x4400u;    // 2^9 in bf16: where a weight passes it, the maximum that they are taken against follows
 
 struct PrefillArgs {
   KvDims d;
@@ -51,20 +56,70 @@ constexpr uint32_t kNoPage = 0x7FFFFFFFu;   // (a NaN)
 
 template <int D>
 struct Smem {
-  static constexpr int kOperand = kTile * D * 2;   // a tile of Q, K or V: D / 64 blocks of 128 rows x 128 bytes
-  static constexpr int kBlock = kTile * 128;
-  static constexpr int q = 0, k = 2 * kOperand, v = 4 * kOperand, ctrl = 6 * kOperand;
-  static constexpr int kCtrl = 1024;
+  // D / 64 blocks of rows of 128 bytes: 128 rows of Q, 64 of K and of V
+  static constexpr int kQBlock = kTile * 128, kBlock = kStep * 128;
+  static constexpr int kQ = kTile * D * 2, kOperand = kStep * D * 2;
+  static constexpr int q = 0, k = 2 * kQ, v = k + kRing * kOperand, ctrl = v + kRing * kOperand;
+  static constexpr int kCtrl = 2048;
   static constexpr int total = ctrl + kCtrl + 1024;   // the tiles start on 1024 bytes
 };
 
+constexpr int kGroupRing = 8;   // steps whose groups are kept: a step's are read until the step four later is converted
 struct Ctrl {
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], scale_full[4], drain;
+  uint64_t q_full[2], k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing], s_full[2][2], p_full[2][2], o_full[2],
+      scale_full[kGroupRing], drain;
   uint32_t tmem;
   int abort;
-  Group group[4][8];   // four steps: a step's are read until the step two later has its scores
+  Group group[kGroupRing][kStep / 16];
 };
-static_assert(sizeof(Ctrl) <= 1024, "control region");
+static_assert(sizeof(Ctrl) <= 2048, "control region");
+
+// Waits of the pipeline: one test inline, the rest (the barrier's own sleep, up
+// to a millisecond at a time, the abort flag and the time limit) out of line,
+// so that a wait that is over costs the MMA warp a few instructions.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(limit_ns == 0 ? 0u : 1000000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 >= limit_ns) {
+      set_status(status, MOE_ERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                         uint64_t limit_ns) {
+  const uint32_t at = smem_u32(bar);
+  return test(at, parity) || wait_on(at, parity, abort, status, limit_ns);
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -108,79 +163,89 @@ __device__ __forceinline__ int v_exponent(float vs) {
 }
 __device__ __forceinline__ bool v_is_zero(float vs) { return (__float_as_uint(vs) & 0x7F800000u) == 0; }
 
-// The converters' part: K and V of every step, each into a ring of two.
+// The converters' part: K and V of every step, each into a ring of its own.
 template <int D>
 __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, int b, int h, int end,
                                         int steps) {
   using S = Smem<D>;
-  constexpr int kHalves = D / 64;
-  const int tid = threadIdx.x - kConverter0;
+  constexpr int kHalves = D / 64, kRows = kStep / 32;   // a thread has a chunk of each half of kRows rows
+  const int tid = threadIdx.x - kConvertWarp * 32;
   // a quarter warp covers two rows' four chunks: its 16-byte stores meet no bank twice
   const int q4 = tid & 3, r = tid >> 2;
   volatile int* abort = &ctrl->abort;
-  int id[4];
-  const auto look = [&](int t0) {
+  // Page ids are asked for two steps ahead, codes and scales one: nothing is
+  // waited for when its turn comes.
+  const auto look = [&](int (&id)[kRows], int t0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       const int t = t0 + 32 * i + r;
-      id[i] = -1;
-      if (t < end) {
-        id[i] = __ldg(a.s.table + static_cast<size_t>(b) * a.s.width + (t >> a.d.shift));
-        if (static_cast<uint32_t>(id[i]) >= static_cast<uint32_t>(a.pool.num_pages)) {
-          set_status(a.status, MOE_ERR_DEVICE_CHECK);
-          id[i] = -1;
-        }
-      }
+      id[i] = t < end ? __ldg(a.s.table + static_cast<size_t>(b) * a.s.width + (t >> a.d.shift)) : -1;
     }
   };
-  const auto load = [&](uint4 (&x)[4 * kHalves], const uint8_t* pool, int t0) {
+  const auto check = [&](int (&id)[kRows], int t0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kRows; ++i)
+      if (static_cast<uint32_t>(id[i]) >= static_cast<uint32_t>(a.pool.num_pages)) {
+        if (t0 + 32 * i + r < end) set_status(a.status, MOE_ERR_DEVICE_CHECK);
+        id[i] = -1;
+      }
+  };
+  const auto load = [&](uint4 (&x)[kRows * kHalves], const uint8_t* pool, const int (&id)[kRows], int t0) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
       const uint8_t* row = pool;
       if (id[i] >= 0) row += kv_row(id[i], a.d.Hkv, h, a.d.page, (t0 + 32 * i + r) & (a.d.page - 1), D) + q4 * 16;
 #pragma unroll
       for (int f = 0; f < kHalves; ++f)
-        x[4 * f + i] = id[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(row + 64 * f)) : make_uint4(0, 0, 0, 0);
+        x[kRows * f + i] = id[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(row + 64 * f)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  // The scales of the thread's rows.  Two threads (writes) have the first row of
+  // every 16-token group: group 2 i + (r >> 4).
+  const bool writes = q4 == 0 && (r & 15) == 0;
+  const auto scales = [&](float (&ks)[kRows], float (&vs)[kRows], const int (&id)[kRows]) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const size_t of = static_cast<size_t>(max(id[i], 0)) * a.d.Hkv + h;
+      vs[i] = id[i] >= 0 ? __ldg(a.pool.v_scale + of) : 0.f;
+      if (writes) ks[i] = id[i] >= 0 ? __ldg(a.pool.k_scale + of) : __uint_as_float(kNoPage);
     }
   };
   const auto at = [&](int f, int row, int e) {
     return f * S::kBlock + row * 128 + (((2 * q4 + e) ^ (row & 7)) << 4);
   };
-  uint4 kx[4 * kHalves], vx[4 * kHalves];
-  float vs[4];
-  look(0);
-  load(kx, a.pool.k, 0);
+  uint4 kx[kRows * kHalves], vx[kRows * kHalves];
+  float ks[kRows], vs[kRows], ks_next[kRows], vs_next[kRows];
+  int id[kRows], id_next[kRows];
+  look(id, 0);
+  look(id_next, kStep);
+  check(id, 0);
+  load(kx, a.pool.k, id, 0);
+  scales(ks, vs, id);
   for (int j = 0; j < steps; ++j) {
-    const int t0 = j * kTile, st = j & 1;
-    const uint32_t parity = (j >> 1) & 1;
-    load(vx, a.pool.v, t0);
+    const int t0 = j * kStep, st = j % kRing;
+    const uint32_t parity = (j / kRing) & 1;
+    load(vx, a.pool.v, id, t0);
+    if (writes) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      vs[i] = id[i] >= 0 ? __ldg(a.pool.v_scale + static_cast<size_t>(id[i]) * a.d.Hkv + h) : 0.f;
-    if (tid < 8) {
-      const int t = t0 + 16 * tid;
-      int page = t < end ? __ldg(a.s.table + static_cast<size_t>(b) * a.s.width + (t >> a.d.shift)) : -1;
-      Group g{__uint_as_float(kNoPage), 0.f, 1.f, 0.f};
-      if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pool.num_pages)) {
-        const size_t of = static_cast<size_t>(page) * a.d.Hkv + h;
-        g.ks = __ldg(a.pool.k_scale + of);
-        const float v = __ldg(a.pool.v_scale + of);
-        if (!v_is_zero(v)) {
-          const float m = v * __uint_as_float(static_cast<uint32_t>(127 - v_exponent(v)) << 23);
-          g.lv = log2f(m);
-          g.inv = 1.f / m;
+      for (int i = 0; i < kRows; ++i) {
+        float lv = 0.f, inv = 1.f;
+        if (!v_is_zero(vs[i])) {
+          const float m = vs[i] * __uint_as_float(static_cast<uint32_t>(127 - v_exponent(vs[i])) << 23);
+          lv = log2f(m);
+          inv = 1.f / m;
         }
+        *reinterpret_cast<float4*>(&ctrl->group[j % kGroupRing][2 * i + (r >> 4)]) = make_float4(ks[i], lv, inv, 0.f);
       }
-      *reinterpret_cast<float4*>(&ctrl->group[j & 3][tid]) = make_float4(g.ks, g.lv, g.inv, 0.f);
-      mbar_arrive(&ctrl->scale_full[j & 3]);
+      mbar_arrive(&ctrl->scale_full[j % kGroupRing]);
     }
-    if (!mbar_wait(&ctrl->k_empty[st], parity ^ 1u, abort, a.status, a.wait_ns)) return;
+    if (!wait_for(&ctrl->k_empty[st], parity ^ 1u, abort, a.status, a.wait_ns)) return;
     const uint32_t kt = smem + S::k + st * S::kOperand, vt = smem + S::v + st * S::kOperand;
 #pragma unroll
     for (int f = 0; f < kHalves; ++f)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 x = kx[4 * f + i];
+      for (int i = 0; i < kRows; ++i) {
+        const uint4 x = kx[kRows * f + i];
         const uint2 c0 = e4m3x4_to_f16x4(x.x), c1 = e4m3x4_to_f16x4(x.y), c2 = e4m3x4_to_f16x4(x.z),
                     c3 = e4m3x4_to_f16x4(x.w);
         sts_u4(kt + at(f, 32 * i + r, 0), make_uint4(c0.x, c0.y, c1.x, c1.y));
@@ -188,18 +253,17 @@ __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32
       }
     fence_proxy_async_smem();
     mbar_arrive(&ctrl->k_full[st]);
-    if (j + 1 < steps) {
-      look(t0 + kTile);
-      load(kx, a.pool.k, t0 + kTile);
-    }
-    if (!mbar_wait(&ctrl->v_empty[st], parity ^ 1u, abort, a.status, a.wait_ns)) return;
+    check(id_next, t0 + kStep);   // (rows beyond the end have none)
+    load(kx, a.pool.k, id_next, t0 + kStep);
+    scales(ks_next, vs_next, id_next);
+    if (!wait_for(&ctrl->v_empty[st], parity ^ 1u, abort, a.status, a.wait_ns)) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       const uint32_t u = v_is_zero(vs[i]) ? 0u : static_cast<uint32_t>(v_exponent(vs[i]) + 247) << 7;
       const uint32_t unit = u | u << 16;
 #pragma unroll
       for (int f = 0; f < kHalves; ++f) {
-        const uint4 x = vx[4 * f + i];
+        const uint4 x = vx[kRows * f + i];
         const uint2 c0 = e4m3x4_to_bf16x4(x.x, unit), c1 = e4m3x4_to_bf16x4(x.y, unit),
                     c2 = e4m3x4_to_bf16x4(x.z, unit), c3 = e4m3x4_to_bf16x4(x.w, unit);
         sts_u4(vt + at(f, 32 * i + r, 0), make_uint4(c0.x, c0.y, c1.x, c1.y));
@@ -208,57 +272,85 @@ __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32
     }
     fence_proxy_async_smem();
     mbar_arrive(&ctrl->v_full[st]);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      id[i] = id_next[i];
+      ks[i] = ks_next[i];
+      vs[i] = vs_next[i];
+    }
+    look(id_next, t0 + 2 * kStep);
   }
 }
 
-// The MMA thread's part.
+// The MMA warp's part: per step and tile, the scores of the step after, then
+// the output of this one.  The whole warp runs it, so that descriptors and
+// addresses stay in uniform registers; one elected lane issues.
 template <int D>
 __device__ __forceinline__ void multiply(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int tiles,
                                          int steps) {
   using S = Smem<D>;
-  constexpr uint32_t kScores = idesc_f32(kTile, kTile, false, false), kOut = idesc_f32(kTile, D, true, true);
+  constexpr uint32_t kScores = idesc_f32(kTile, kStep, false, false), kOut = idesc_f32(kTile, D, true, true);
   volatile int* abort = &ctrl->abort;
-  const auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort, a.status, a.wait_ns); };
-  // S of tile t over step j's tokens
-  const auto scores = [&](int t, int j) {
-    const uint32_t q = smem + S::q + t * S::kOperand, k = smem + S::k + (j & 1) * S::kOperand;
-    tc_fence_after();
-#pragma unroll
-    for (int f = 0; f < D / 64; ++f) {
-      const uint64_t dq = smem_desc_k128(q + f * S::kBlock), dk = smem_desc_k128(k + f * S::kBlock);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) umma_bf16(tmem + t * kTile, dq + 2 * i, dk + 2 * i, kScores, f + i > 0);
-    }
-    umma_commit(&ctrl->s_full[t]);
+  const bool one = elect_one();
+  const auto wait = [&](uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xFFFFFFFFu, test(bar, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, wait_on(bar, parity, abort, a.status, a.wait_ns)) != 0;
   };
+  const uint32_t q_full = smem_u32(ctrl->q_full), k_full = smem_u32(ctrl->k_full), v_full = smem_u32(ctrl->v_full),
+                 o_full = smem_u32(ctrl->o_full), p_full = smem_u32(ctrl->p_full);
   for (int t = 0; t < tiles; ++t)
-    if (!wait(&ctrl->q_full[t], 0)) return;
-  if (!wait(&ctrl->k_full[0], 0)) return;
-  for (int t = 0; t < tiles; ++t) scores(t, 0);
-  umma_commit(&ctrl->k_empty[0]);
-  for (int j = 0; j < steps; ++j) {
-    const uint32_t v = smem + S::v + (j & 1) * S::kOperand;
+    if (!wait(q_full + 8 * t, 0)) return;
+  const uint64_t q0 = smem_desc_k128(smem + S::q), k0 = smem_desc_k128(smem + S::k),
+                 v0 = smem_desc_n128(smem + S::v, S::kBlock);
+  // j: the step whose output is due; the scores are those of step j + 1
+  int stage = 0, stage_next = 0;          // of step j and of step j + 1
+  uint32_t phase = 0, phase_next = 0;     // and their rings' parities
+  for (int j = -1; j < steps; ++j) {
+    const bool more = j + 1 < steps;
+    const uint64_t dk = k0 + stage_next * (S::kOperand >> 4), dv = v0 + stage * (S::kOperand >> 4);
+    const uint32_t buf = j & 1;   // of step j
+#pragma unroll 1
     for (int t = 0; t < tiles; ++t) {
-      if (t == 0 && !wait(&ctrl->v_full[j & 1], (j >> 1) & 1)) return;
-      if (!wait(&ctrl->p_full[t], j & 1)) return;
-      tc_fence_after();
-      const uint32_t o = tmem + 2 * kTile + t * D, p = tmem + t * kTile;
+      const uint32_t s_t = tmem + t * 2 * kStep, o = tmem + 4 * kStep + t * D;
+      if (more) {
+        if (t == 0 && !wait(k_full + 8 * stage_next, phase_next)) return;
+        // these scores take the place of step j - 1's weights: once their product is done
+        if (j > 0 && !wait(o_full + 8 * t, buf ^ 1u)) return;
+        tc_fence_after();
+        const uint64_t dq = q0 + t * (S::kQ >> 4);
+        const uint32_t to = s_t + (buf ^ 1u) * kStep;
+        if (one) {
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i) {
-        const uint64_t dv = smem_desc_n128(v + i * 2048, S::kBlock);
-        const uint32_t hi = p + 32 * (i >> 1) + 8 * (i & 1);
-        umma_bf16_ts(o, hi, dv, kOut, j + i > 0);
-        umma_bf16_ts(o, hi + 16, dv, kOut, 1);
+          for (int i = 0; i < D / 16; ++i)
+            umma_bf16(to, dq + (i >> 2) * (S::kQBlock >> 4) + 2 * (i & 3), dk + (i >> 2) * (S::kBlock >> 4) + 2 * (i & 3),
+                      kScores, i > 0);
+          umma_commit(&ctrl->s_full[t][buf ^ 1u]);
+          if (t + 1 == tiles) umma_commit(&ctrl->k_empty[stage_next]);
+        }
+        __syncwarp();
       }
-      umma_commit(&ctrl->o_full[t]);
-      if (t + 1 == tiles) umma_commit(&ctrl->v_empty[j & 1]);
-      if (j + 1 < steps) {
-        if (t == 0 && !wait(&ctrl->k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) return;
-        // the next scores overwrite the weights: only once their product is done
-        if (!wait(&ctrl->o_full[t], j & 1)) return;
-        scores(t, j + 1);
-        if (t + 1 == tiles) umma_commit(&ctrl->k_empty[(j + 1) & 1]);
+      if (j < 0) continue;
+      if (t == 0 && !wait(v_full + 8 * stage, phase)) return;
+      if (!wait(p_full + 16 * t + 8 * buf, (j >> 1) & 1)) return;
+      tc_fence_after();
+      const uint32_t p = s_t + buf * kStep;
+      if (one) {
+#pragma unroll
+        for (int i = 0; i < kStep / 16; ++i) {
+          const uint32_t hi = p + 32 * (i >> 1) + 8 * (i & 1);
+          umma_bf16_ts(o, hi, dv + i * (2048 >> 4), kOut, j + i > 0);
+          umma_bf16_ts(o, hi + 16, dv + i * (2048 >> 4), kOut, 1);
+        }
+        umma_commit(&ctrl->o_full[t]);
+        if (t + 1 == tiles) umma_commit(&ctrl->v_empty[stage]);
       }
+      __syncwarp();
+    }
+    stage = stage_next;
+    phase = phase_next;
+    if (++stage_next == kRing) {
+      stage_next = 0;
+      phase_next ^= 1u;
     }
   }
 }
@@ -302,104 +394,133 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(c[k]) : "f"(bf16_hi(w[k]) * up), "f"(bf16_lo(w[k]) * up));
-      sts_u4(smem + S::q + t * S::kOperand + (i >> 3) * S::kBlock + in_tile * 128 + (((i & 7) ^ (in_tile & 7)) << 4),
+      sts_u4(smem + S::q + t * S::kQ + (i >> 3) * S::kQBlock + in_tile * 128 + (((i & 7) ^ (in_tile & 7)) << 4),
              make_uint4(c[0], c[1], c[2], c[3]));
     }
     fence_proxy_async_smem();
     mbar_arrive(&ctrl->q_full[t]);
   }
   const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // 32 quad in the address's lane field
-  const uint32_t sc = tmem + lanes + t * kTile, o = tmem + lanes + 2 * kTile + t * D;
+  const uint32_t o = tmem + lanes + 4 * kStep + t * D;
+  // m: what the exponents are taken against, a whole number, so that a change
+  // of it scales l, O and the weights already written exactly.  It follows the
+  // scores only where a weight comes out above kLarge.
   float m = -INFINITY, l = 0.f;
   for (int j = 0; j < steps; ++j) {
-    const Group* group = ctrl->group[j & 3];
-    bool ok = mbar_wait(&ctrl->scale_full[j & 3], (j >> 2) & 1, abort, a.status, a.wait_ns) &&
-              mbar_wait(&ctrl->s_full[t], j & 1, abort, a.status, a.wait_ns);
+    const uint32_t groups = smem_u32(ctrl->group[j % kGroupRing]);
+    const uint32_t sc = tmem + lanes + t * 2 * kStep + (j & 1) * kStep;
+    const bool ok = wait_for(&ctrl->scale_full[j % kGroupRing], (j / kGroupRing) & 1, abort, a.status, a.wait_ns) &&
+                    wait_for(&ctrl->s_full[t][j & 1], (j >> 1) & 1, abort, a.status, a.wait_ns);
     if (!__all_sync(0xFFFFFFFFu, ok)) return;
     tc_fence_after();
-    const int t0 = j * kTile;
-    bool masks = t0 + kTile > sees_least;
-    float top = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t s[32];
-      tmem_ld_32cols(sc + 32 * c, s);
-      tmem_ld_wait();
+    const int t0 = j * kStep;
+    bool failed = false;
+    // 32 tokens (two groups): their scores s to weights, in place
+    const auto weigh = [&](int c, uint32_t (&s)[32]) {
+      float f[2], lv[2], inv[2];
+      bool gone[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float ks = group[2 * c + e].ks;
-        masks |= __float_as_uint(ks) == kNoPage;
-        float x = -INFINITY;
-        if (!masks) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x = fmaxf(x, __uint_as_float(s[16 * e + i]));
-        } else if (__float_as_uint(ks) != kNoPage) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (t0 + 32 * c + 16 * e + i < sees) x = fmaxf(x, __uint_as_float(s[16 * e + i]));
-        }
-        if (x != -INFINITY) top = fmaxf(top, x * (ks * unscale));
+        const uint4 gr = lds_u4(groups + (2 * c + e) * sizeof(Group));
+        f[e] = __uint_as_float(gr.x) * unscale;
+        lv[e] = __uint_as_float(gr.y);
+        inv[e] = __uint_as_float(gr.z);
+        gone[e] = gr.x == kNoPage;
       }
-    }
-    if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
-      top = fmaxf(top, m);
-      const float f = m == -INFINITY ? 0.f : ex2(m - top);
-      m = top;
-      l *= f;
-      if (j > 0) {   // (the scores of step j came after the product of step j - 1)
+      if (t0 + 32 * c + 32 > sees_least || gone[0] || gone[1]) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          tmem_ld_32cols(o + 32 * c, v);
+        for (int e = 0; e < 2; ++e) {
+          const int left = gone[e] ? 0 : sees - (t0 + 32 * c + 16 * e);
+          const bool flat = f[e] == 0.f || gone[e];   // (no -inf times 0)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[16 * e + i] = i >= left ? 0xFF800000u : flat ? 0u : s[16 * e + i];
+          if (flat) f[e] = 1.f;
+        }
+      }
+      uint32_t hi[16], lo[16];
+      float sum[4];
+      bool raised = false;
+      for (;;) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float add = lv[e] - (m == -INFINITY ? 0.f : m);
+          float part[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float w0 = ex2(fmaf(__uint_as_float(s[16 * e + 2 * i]), f[e], add));
+            const float w1 = ex2(fmaf(__uint_as_float(s[16 * e + 2 * i + 1]), f[e], add));
+            part[0] += w0;
+            part[1] += w1;
+            const uint32_t u0 = __float_as_uint(w0), u1 = __float_as_uint(w1);
+            hi[8 * e + i] = prmt(u0, u1, 0x7632u);
+            most = __vmaxu2(most, hi[8 * e + i]);
+            lo[8 * e + i] = pack_bf16x2(w0 - __uint_as_float(u0 & 0xFFFF0000u), w1 - __uint_as_float(u1 & 0xFFFF0000u));
+          }
+          sum[2 * e] = part[0];
+          sum[2 * e + 1] = part[1];
+        }
+        // Too large a weight (or a first one, or a NaN, which stays): m is raised
+        // to the scores' maximum and everything so far scaled down to it.
+        const bool large = max(most & 0xFFFFu, most >> 16) > kLarge || m == -INFINITY;
+        if (raised || !__any_sync(0xFFFFFFFFu, large)) break;
+        raised = true;
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]) * f[i >> 4]);
+        const float to = large && top > m ? ceilf(top) : m;   // (a row goes by its own weights alone)
+        const float r = to == m ? 1.f : ex2(m - to);   // (0 for the first)
+        m = to;
+        l *= r;
+        // O so far: once the last step's product is in it (the one before was, ahead
+        // of these scores; the next one waits for these weights)
+        if (j > 0) {
+          failed |= !wait_for(&ctrl->o_full[t], (j - 1) & 1, abort, a.status, a.wait_ns);
+          tc_fence_after();
+        }
+        const int parts = j > 0 ? D / 16 : 0;
+#pragma unroll 1
+        for (int k = 0; k < parts; ++k) {
+          uint32_t v[16];
+          tmem_ld_16cols(o + 16 * k, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-          tmem_st_32cols(o + 32 * c, v);
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * r);
+          tmem_st_16cols(o + 16 * k, v);
+        }
+        const uint32_t r2 = pack_bf16x2(r, r);
+#pragma unroll 1
+        for (int k = 0; k < 2 * c; ++k) {
+          uint32_t v[16];
+          tmem_ld_16cols(sc + 16 * k, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = bf16x2_mul(v[i], r2);
+          tmem_st_16cols(sc + 16 * k, v);
         }
       }
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
+      l = fmaf(sum[0] + sum[1], inv[0], l);
+      l = fmaf(sum[2] + sum[3], inv[1], l);
+      tmem_st_16cols(sc + 32 * c, hi);
+      tmem_st_16cols(sc + 32 * c + 16, lo);
+    };
+#pragma unroll 1
+    for (int c = 0; c < kStep / 32; ++c) {
       uint32_t s[32];
       tmem_ld_32cols(sc + 32 * c, s);
       tmem_ld_wait();
-      uint32_t hi[16], lo[16];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 gr = *reinterpret_cast<const float4*>(&group[2 * c + e]);
-        const float f = gr.x * unscale, add = gr.y - base;
-        const int t_first = t0 + 32 * c + 16 * e;
-        if (masks) {
-          const int left = __float_as_uint(gr.x) == kNoPage ? 0 : sees - t_first;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[16 * e + i] = i < left ? __float_as_uint(fmaf(__uint_as_float(s[16 * e + i]), f, add)) : 0xFF800000u;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[16 * e + i] = __float_as_uint(fmaf(__uint_as_float(s[16 * e + i]), f, add));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float w0 = ex2(__uint_as_float(s[16 * e + 2 * i])), w1 = ex2(__uint_as_float(s[16 * e + 2 * i + 1]));
-          l = fmaf(w0, gr.z, l);
-          l = fmaf(w1, gr.z, l);
-          const uint32_t u0 = __float_as_uint(w0), u1 = __float_as_uint(w1);
-          hi[8 * e + i] = prmt(u0, u1, 0x7632u);
-          lo[8 * e + i] = pack_bf16x2(w0 - __uint_as_float(u0 & 0xFFFF0000u), w1 - __uint_as_float(u1 & 0xFFFF0000u));
-        }
-      }
-      tmem_st_16cols(sc + 32 * c, hi);
-      tmem_st_16cols(sc + 32 * c + 16, lo);
+      weigh(c, s);
     }
     tmem_st_wait();
     tc_fence_before();
-    mbar_arrive(&ctrl->p_full[t]);
+    mbar_arrive(&ctrl->p_full[t][j & 1]);
+    if (__any_sync(0xFFFFFFFFu, failed)) return;
   }
-  if (steps > 0) {
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctrl->o_full[t], (steps - 1) & 1, abort, a.status, a.wait_ns))) return;
-    tc_fence_after();
-  }
+  // The last scores followed the third last product, so up to two are still to
+  // come: a wait for each, or its parity would be taken for the one before.
+  for (int j = max(steps - 2, 0); j < steps; ++j)
+    if (!__all_sync(0xFFFFFFFFu, wait_for(&ctrl->o_full[t], j & 1, abort, a.status, a.wait_ns))) return;
+  tc_fence_after();
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D);
 #pragma unroll
@@ -447,48 +568,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   if (row0 >= rows) return;
   const int tiles = row0 + kTile < rows ? 2 : 1;
   const int end = max(len - n + (min(row0 + 2 * kTile, rows) - 1) / g + 1, 0);   // what the last row sees
-  const int steps = (end + kTile - 1) / kTile;
-  const int warp = threadIdx.x >> 5;
+  const int steps = (end + kStep - 1) / kStep;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctrl->q_full[i], kTile);
-      mbar_init(&ctrl->k_full[i], kTile);
-      mbar_init(&ctrl->v_full[i], kTile);
-      mbar_init(&ctrl->p_full[i], kTile);
+      mbar_init(&ctrl->o_full[i], 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&ctrl->s_full[i][k], 1);
+        mbar_init(&ctrl->p_full[i][k], kTile);
+      }
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&ctrl->k_full[i], 128);
+      mbar_init(&ctrl->v_full[i], 128);
       mbar_init(&ctrl->k_empty[i], 1);
       mbar_init(&ctrl->v_empty[i], 1);
-      mbar_init(&ctrl->s_full[i], 1);
-      mbar_init(&ctrl->o_full[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&ctrl->scale_full[i], 8);
+    for (int i = 0; i < kGroupRing; ++i) mbar_init(&ctrl->scale_full[i], 2);
     mbar_init(&ctrl->drain, 1);
     ctrl->abort = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     tmem_alloc(&ctrl->tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctrl->tmem;
-  if (warp < 8) {
-    if (warp / 4 < tiles) softmax<D>(a, ctrl, smem, tmem, warp / 4, b, h, g, first, n, len, row0, steps);
-  } else if (warp < kMmaWarp) {
-    convert<D>(a, ctrl, smem, b, h, end, steps);
-  } else {
-    if ((threadIdx.x & 31) == 0 && steps > 0) {
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl->tmem, 0);
+  if (warp == 0) {
+    if (steps > 0) {
       multiply<D>(a, ctrl, smem, tmem, tiles, steps);
       // whatever was issued is done before the tensor memory goes
-      umma_commit(&ctrl->drain);
-      mbar_wait_timed(&ctrl->drain, 0, a.status);
+      __syncwarp();
+      if (elect_one()) {
+        umma_commit(&ctrl->drain);
+        mbar_wait_timed(&ctrl->drain, 0, a.status);
+      }
+      __syncwarp();
     }
-    __syncwarp();
+  } else if (warp < kConvertWarp) {
+    const int t = (warp - kSoftmaxWarp) / 4;
+    if (t < tiles) softmax<D>(a, ctrl, smem, tmem, t, b, h, g, first, n, len, row0, steps);
+  } else {
+    convert<D>(a, ctrl, smem, b, h, end, steps);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
