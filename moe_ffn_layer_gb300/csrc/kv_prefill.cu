@@ -20,6 +20,7 @@
 // operand (exact), the mantissa into the weights' exponent, and the row's sum
 // takes it out again, w / mantissa; for power-of-two scales it is 1.
 #include <limits.h>
+#include <stddef.h>
 
 #include "kv_cache.cuh"
 
@@ -29,10 +30,11 @@ namespace {
 constexpr int kTile = 128;              // rows of a tile
 constexpr int kStep = 64;               // tokens of a step
 constexpr int kRing = 4;                // steps of K and of V in shared memory
-// Warps: 0 issues the MMAs (the scheduler favours the lowest), 1 to 4 and 5 to 8
-// are the tiles' softmax, 9 to 12 convert.
-constexpr int kThreads = 416;
-constexpr int kSoftmaxWarp = 1, kConvertWarp = 9;
+// Warps: 0 and 1 issue the tiles' MMAs (one warp for both spent half its time
+// between waits and MMAs: PLACEHOLDER2), 2 to 5 and 6 to 9 are
+// the tiles' softmax, 10 to 13 convert.
+constexpr int kThreads = 448;
+constexpr int kSoftmaxWarp = 2, kConvertWarp = 10;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kLarge = 0x4400u;    // 2^9 in bf16: where a weight passes it, the maximum that they are taken against follows
 
@@ -46,7 +48,7 @@ struct PrefillArgs {
 };
 
 // What the softmax needs of a step's 16-token groups.
-struct Group {
+struct alignas(16) Group {   // (one 16-byte access)
   float ks;    // K scale; kNoPage: the page is not there
   float lv;    // log2 of the V scale's mantissa
   float inv;   // its inverse
@@ -67,12 +69,12 @@ struct Smem {
 constexpr int kGroupRing = 8;   // steps whose groups are kept: a step's are read until the step four later is converted
 struct Ctrl {
   uint64_t q_full[2], k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing], s_full[2][2], p_full[2][2], o_full[2],
-      scale_full[kGroupRing], drain;
+      scale_full[kGroupRing], drain[2];
   uint32_t tmem;
   int abort;
   Group group[kGroupRing][kStep / 16];
 };
-static_assert(sizeof(Ctrl) <= 2048, "control region");
+static_assert(sizeof(Ctrl) <= 2048 && sizeof(Group) == 16 && offsetof(Ctrl, group) % 16 == 0, "control region");
 
 // Waits of the pipeline: one test inline, the rest (the barrier's own sleep, up
 // to a millisecond at a time, the abort flag and the time limit) out of line,
@@ -282,11 +284,11 @@ __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32
   }
 }
 
-// The MMA warp's part: per step and tile, the scores of the step after, then
-// the output of this one.  The whole warp runs it, so that descriptors and
-// addresses stay in uniform registers; one elected lane issues.
+// A tile's MMA warp: per step the scores of the step after, then the output of
+// this one.  The whole warp runs it, so that descriptors and addresses stay in
+// uniform registers; one elected lane issues.
 template <int D>
-__device__ __forceinline__ void multiply(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int tiles,
+__device__ __forceinline__ void multiply(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int t,
                                          int steps) {
   using S = Smem<D>;
   constexpr uint32_t kScores = idesc_f32(kTile, kStep, false, false), kOut = idesc_f32(kTile, D, true, true);
@@ -296,44 +298,40 @@ __device__ __forceinline__ void multiply(const PrefillArgs& a, Ctrl* ctrl, uint3
     if (__all_sync(0xFFFFFFFFu, test(bar, parity))) return true;
     return __all_sync(0xFFFFFFFFu, wait_on(bar, parity, abort, a.status, a.wait_ns)) != 0;
   };
-  const uint32_t q_full = smem_u32(ctrl->q_full), k_full = smem_u32(ctrl->k_full), v_full = smem_u32(ctrl->v_full),
-                 o_full = smem_u32(ctrl->o_full), p_full = smem_u32(ctrl->p_full);
-  for (int t = 0; t < tiles; ++t)
-    if (!wait(q_full + 8 * t, 0)) return;
-  const uint64_t q0 = smem_desc_k128(smem + S::q), k0 = smem_desc_k128(smem + S::k),
+  const uint32_t k_full = smem_u32(ctrl->k_full), v_full = smem_u32(ctrl->v_full), o_full = smem_u32(&ctrl->o_full[t]),
+                 p_full = smem_u32(ctrl->p_full[t]);
+  if (!wait(smem_u32(&ctrl->q_full[t]), 0)) return;
+  const uint64_t dq = smem_desc_k128(smem + S::q + t * S::kQ), k0 = smem_desc_k128(smem + S::k),
                  v0 = smem_desc_n128(smem + S::v, S::kBlock);
+  const uint32_t s_t = tmem + t * 2 * kStep, o = tmem + 4 * kStep + t * D;
   // j: the step whose output is due; the scores are those of step j + 1
   int stage = 0, stage_next = 0;          // of step j and of step j + 1
   uint32_t phase = 0, phase_next = 0;     // and their rings' parities
   for (int j = -1; j < steps; ++j) {
-    const bool more = j + 1 < steps;
-    const uint64_t dk = k0 + stage_next * (S::kOperand >> 4), dv = v0 + stage * (S::kOperand >> 4);
     const uint32_t buf = j & 1;   // of step j
-#pragma unroll 1
-    for (int t = 0; t < tiles; ++t) {
-      const uint32_t s_t = tmem + t * 2 * kStep, o = tmem + 4 * kStep + t * D;
-      if (more) {
-        if (t == 0 && !wait(k_full + 8 * stage_next, phase_next)) return;
-        // these scores take the place of step j - 1's weights: once their product is done
-        if (j > 0 && !wait(o_full + 8 * t, buf ^ 1u)) return;
-        tc_fence_after();
-        const uint64_t dq = q0 + t * (S::kQ >> 4);
-        const uint32_t to = s_t + (buf ^ 1u) * kStep;
-        if (one) {
+    if (j + 1 < steps) {
+      if (!wait(k_full + 8 * stage_next, phase_next)) return;
+      // these scores take the place of step j - 1's weights: once their product is done
+      if (j > 0 && !wait(o_full, buf ^ 1u)) return;
+      tc_fence_after();
+      const uint32_t to = s_t + (buf ^ 1u) * kStep;
+      const uint64_t dk = k0 + stage_next * (S::kOperand >> 4);
+      if (one) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            umma_bf16(to, dq + (i >> 2) * (S::kQBlock >> 4) + 2 * (i & 3), dk + (i >> 2) * (S::kBlock >> 4) + 2 * (i & 3),
-                      kScores, i > 0);
-          umma_commit(&ctrl->s_full[t][buf ^ 1u]);
-          if (t + 1 == tiles) umma_commit(&ctrl->k_empty[stage_next]);
-        }
-        __syncwarp();
+        for (int i = 0; i < D / 16; ++i)
+          umma_bf16(to, dq + (i >> 2) * (S::kQBlock >> 4) + 2 * (i & 3), dk + (i >> 2) * (S::kBlock >> 4) + 2 * (i & 3),
+                    kScores, i > 0);
+        umma_commit(&ctrl->s_full[t][buf ^ 1u]);
+        umma_commit(&ctrl->k_empty[stage_next]);
       }
-      if (j < 0) continue;
-      if (t == 0 && !wait(v_full + 8 * stage, phase)) return;
-      if (!wait(p_full + 16 * t + 8 * buf, (j >> 1) & 1)) return;
+      __syncwarp();
+    }
+    if (j >= 0) {
+      if (!wait(v_full + 8 * stage, phase)) return;
+      if (!wait(p_full + 8 * buf, (j >> 1) & 1)) return;
       tc_fence_after();
       const uint32_t p = s_t + buf * kStep;
+      const uint64_t dv = v0 + stage * (S::kOperand >> 4);
       if (one) {
 #pragma unroll
         for (int i = 0; i < kStep / 16; ++i) {
@@ -342,7 +340,7 @@ __device__ __forceinline__ void multiply(const PrefillArgs& a, Ctrl* ctrl, uint3
           umma_bf16_ts(o, hi + 16, dv + i * (2048 >> 4), kOut, 1);
         }
         umma_commit(&ctrl->o_full[t]);
-        if (t + 1 == tiles) umma_commit(&ctrl->v_empty[stage]);
+        umma_commit(&ctrl->v_empty[stage]);
       }
       __syncwarp();
     }
@@ -399,6 +397,7 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
     }
     fence_proxy_async_smem();
     mbar_arrive(&ctrl->q_full[t]);
+    __syncwarp();
   }
   const uint32_t lanes = static_cast<uint32_t>(quad) << 21;   // 32 quad in the address's lane field
   const uint32_t o = tmem + lanes + 4 * kStep + t * D;
@@ -412,6 +411,7 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
     const bool ok = wait_for(&ctrl->scale_full[j % kGroupRing], (j / kGroupRing) & 1, abort, a.status, a.wait_ns) &&
                     wait_for(&ctrl->s_full[t][j & 1], (j >> 1) & 1, abort, a.status, a.wait_ns);
     if (!__all_sync(0xFFFFFFFFu, ok)) return;
+    __syncwarp();
     tc_fence_after();
     const int t0 = j * kStep;
     bool failed = false;
@@ -475,7 +475,8 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
         // O so far: once the last step's product is in it (the one before was, ahead
         // of these scores; the next one waits for these weights)
         if (j > 0) {
-          failed |= !wait_for(&ctrl->o_full[t], (j - 1) & 1, abort, a.status, a.wait_ns);
+          failed |= !__all_sync(0xFFFFFFFFu, wait_for(&ctrl->o_full[t], (j - 1) & 1, abort, a.status, a.wait_ns));
+          __syncwarp();   // (the tensor-memory accesses below want the whole warp)
           tc_fence_after();
         }
         const int parts = j > 0 ? D / 16 : 0;
@@ -520,6 +521,7 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
   // come: a wait for each, or its parity would be taken for the one before.
   for (int j = max(steps - 2, 0); j < steps; ++j)
     if (!__all_sync(0xFFFFFFFFu, wait_for(&ctrl->o_full[t], j & 1, abort, a.status, a.wait_ns))) return;
+  __syncwarp();
   tc_fence_after();
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D);
@@ -533,15 +535,17 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0;
     }
-    if (!real) continue;
+    if (real) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
-      out[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < 4; ++k)
+          w[k] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
+        out[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
+    __syncwarp();
   }
   if (real && at.lse) at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
@@ -582,14 +586,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&ctrl->k_full[i], 128);
       mbar_init(&ctrl->v_full[i], 128);
-      mbar_init(&ctrl->k_empty[i], 1);
-      mbar_init(&ctrl->v_empty[i], 1);
+      mbar_init(&ctrl->k_empty[i], tiles);
+      mbar_init(&ctrl->v_empty[i], tiles);
     }
     for (int i = 0; i < kGroupRing; ++i) mbar_init(&ctrl->scale_full[i], 2);
-    mbar_init(&ctrl->drain, 1);
+    mbar_init(&ctrl->drain[0], 1);
+    mbar_init(&ctrl->drain[1], 1);
     ctrl->abort = 0;
     fence_barrier_init();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(&ctrl->tmem, 512);
     tmem_relinquish();
@@ -598,14 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl->tmem, 0);
-  if (warp == 0) {
-    if (steps > 0) {
-      multiply<D>(a, ctrl, smem, tmem, tiles, steps);
+  if (warp < kSoftmaxWarp) {
+    if (warp < tiles && steps > 0) {
+      multiply<D>(a, ctrl, smem, tmem, warp, steps);
       // whatever was issued is done before the tensor memory goes
       __syncwarp();
       if (elect_one()) {
-        umma_commit(&ctrl->drain);
-        mbar_wait_timed(&ctrl->drain, 0, a.status);
+        umma_commit(&ctrl->drain[warp]);
+        mbar_wait_timed(&ctrl->drain[warp], 0, a.status);
       }
       __syncwarp();
     }
