@@ -801,9 +801,7 @@ template <int D, int R>
 int launch_decode(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, const Parts& parts,
                   int* status, cudaStream_t stream, int* launches) {
   constexpr size_t smem = kWarps * kStages * (Ring<D>::kStageBytes + 16) + 2 * 8 * R * (D + 4) * sizeof(float);
-  if (cudaFuncSetAttribute(kv_decode_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  if (kv_allow_smem<kv_decode_kernel<D, R>>(smem) != cudaSuccess) return MOE_ERR_CUDA;
   // no more CTAs than the longest call of these sizes gives steps to
   const long long tiles = (static_cast<long long>(a.max_q) * (a.Hq / d.Hkv) + 8 * R - 1) / (8 * R);
   const double steps = static_cast<double>(s.B) * d.Hkv * tiles * ((static_cast<long long>(s.max_len) + kSpan - 1) / kSpan + 1);

@@ -2,10 +2,25 @@
 // token lies, the cache's scale rule, and e4m3 in registers.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace moe {
+
+// Allows a kernel its dynamic shared memory, once per device and kernel.
+template <auto kKernel>
+inline cudaError_t kv_allow_smem(size_t bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t r = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (r == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+  return r;
+}
 
 // Row of a code pool ([num_pages][Hkv][page][D]) that holds slot `slot` of a
 // page for one head, as a byte offset (64 bits: a pool can pass 4 GB; its rows

@@ -631,8 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
 
 template <int D>
 int launch(const PrefillArgs& a, cudaStream_t stream, int* launches) {
-  if (cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::total) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  if (kv_allow_smem<kv_prefill_kernel<D>>(Smem<D>::total) != cudaSuccess) return MOE_ERR_CUDA;
   const long long rows = static_cast<long long>(a.at.max_q) * (a.at.Hq / a.d.Hkv);
   const long long pairs = (rows + 2 * kTile - 1) / (2 * kTile);
   const double ctas = static_cast<double>(pairs) * a.s.B * a.d.Hkv;

@@ -33,6 +33,7 @@ class KVCache8:
 
     def _hold(self, k, v, k_scale, v_scale):
         self.device = k.device
+        self._dev = k.get_device()
         _want("k", k, torch.uint8, 4, self.device)
         _want("v", v, torch.uint8, 4, self.device, k.shape)
         _want("k_scale", k_scale, torch.float32, 2, self.device, k.shape[:2])
@@ -41,16 +42,20 @@ class KVCache8:
         self.num_pages, self.kv_heads, self.page, self.head_dim = k.shape
         self.dims = B.moe_kv_dims(self.kv_heads, self.head_dim, self.page)
         self.pool = B.moe_kv_pool(*(B.ptr(t) for t in (k, v, k_scale, v_scale)), self.num_pages)
-        self._ws = {}   # by stream: calls of different streams may overlap
+        self._ws = {}     # by stream: calls of different streams may overlap
+        self._need = {}   # workspace bytes by sizes
 
-    def _seqs(self, page_table, seq_lens, max_len):
-        _want("page_table", page_table, torch.int32, 2, self.device)
-        _want("seq_lens", seq_lens, torch.int32, 1, self.device, page_table.shape[:1])
+    def _want_table(self, page_table, seq_lens, cu, cu_name):
+        """Checks the sequences' tensors; returns the table's rows and width."""
         n, width = page_table.shape
-        return B.moe_kv_seqs(B.ptr(page_table), B.ptr(seq_lens), n, width, max_len)
-
-    def _stream(self, stream):
-        return stream if stream is not None else torch.cuda.current_stream(self.device)
+        dev = self._dev
+        if not (_is(page_table, torch.int32, dev, page_table.shape) and _is(seq_lens, torch.int32, dev, (n,)) and
+                (cu is None or _is(cu, torch.int32, dev, (n + 1,)))):
+            _want("page_table", page_table, torch.int32, 2, self.device)
+            _want("seq_lens", seq_lens, torch.int32, 1, self.device, (n,))
+            if cu is not None:
+                _want(cu_name, cu, torch.int32, 1, self.device, (n + 1,))
+        return n, width
 
     def append(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
                cu_new: torch.Tensor, stream=None) -> None:
@@ -58,14 +63,20 @@ class KVCache8:
         stride apart); seq_lens already counts them, cu_new int32 [B+1] says
         whose they are."""
         T = k.shape[0]
-        for name, t in (("k", k), ("v", v)):
-            _want(name, t, torch.bfloat16, 3, self.device, (T, self.kv_heads, self.head_dim), rows=True)
-        if T > 1 and k.stride(0) != v.stride(0):
-            raise ValueError(f"k and v rows lie {k.stride(0)} and {v.stride(0)} elements apart")
-        _want("cu_new", cu_new, torch.int32, 1, self.device, (page_table.shape[0] + 1,))
-        seqs = self._seqs(page_table, seq_lens, page_table.shape[1] * self.page)
-        stride = k.stride(0) if T > 1 else self.kv_heads * self.head_dim
-        B.moe_kv_append(self.dims, self.pool, seqs, k, v, stride, cu_new, T, self._stream(stream))
+        shape = (T, self.kv_heads, self.head_dim)
+        if not (_is_rows(k, self._dev, shape) and _is_rows(v, self._dev, shape)):
+            _want("k", k, torch.bfloat16, 3, self.device, shape, rows=True)
+            _want("v", v, torch.bfloat16, 3, self.device, shape, rows=True)
+        stride = k.stride(0)
+        if T <= 1:
+            stride = self.kv_heads * self.head_dim
+        elif stride != v.stride(0):
+            raise ValueError(f"k and v rows lie {stride} and {v.stride(0)} elements apart")
+        n, width = self._want_table(page_table, seq_lens, cu_new, "cu_new")
+        seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, min(width * self.page, 1 << 30))
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        B.moe_kv_append(self.dims, self.pool, seqs, k, v, stride, cu_new, T, stream)
 
     def workspace(self, need: int, stream) -> torch.Tensor:
         """The stream's workspace, of at least `need` bytes, zero-filled when
@@ -87,23 +98,34 @@ class KVCache8:
         log-sum-exps; weights fp32 [B, Hkv, >= max_len], where given, gains the
         softmax weights."""
         T, Hq = q.shape[0], q.shape[1]
-        _want("q", q, torch.bfloat16, 3, self.device, (T, Hq, self.head_dim), rows=True)
-        _want("cu_q", cu_q, torch.int32, 1, self.device, (page_table.shape[0] + 1,))
-        seqs = self._seqs(page_table, seq_lens, max_len)
-        stream = self._stream(stream)
-        if out is None:
+        dev, D = self._dev, self.head_dim
+        shape = (T, Hq, D)
+        if not _is_rows(q, dev, shape):
+            _want("q", q, torch.bfloat16, 3, self.device, shape, rows=True)
+        n, width = self._want_table(page_table, seq_lens, cu_q, "cu_q")
+        seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, max_len)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+            if out is None:
+                out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        elif out is None:
             with torch.cuda.stream(stream):
-                out = torch.empty((T, Hq, self.head_dim), dtype=torch.bfloat16, device=self.device)
-        _want("out", out, torch.bfloat16, 3, self.device, (T, Hq, self.head_dim))
-        if lse is not None:
+                out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        if not _is(out, torch.bfloat16, dev, shape):
+            _want("out", out, torch.bfloat16, 3, self.device, shape)
+        if lse is not None and not _is(lse, torch.float32, dev, (T, Hq)):
             _want("lse", lse, torch.float32, 2, self.device, (T, Hq))
+        w_stride = 0
         if weights is not None:
-            _want("weights", weights, torch.float32, 3, self.device, (seqs.B, self.kv_heads, weights.shape[2]))
-        need = B.moe_kv_attention_workspace_bytes(self.dims, Hq, T)
+            w_stride = weights.shape[-1]
+            if not _is(weights, torch.float32, dev, (n, self.kv_heads, w_stride)):
+                _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
+        need = self._need.get((Hq, T))
+        if need is None:
+            need = self._need[Hq, T] = B.moe_kv_attention_workspace_bytes(self.dims, Hq, T)
         ws = self.workspace(need, stream)
-        B.moe_kv_attention(self.dims, self.pool, seqs, q, q.stride(0) if T > 1 else Hq * self.head_dim, Hq, cu_q, T,
-                           max_q, self.head_dim ** -0.5 if scale is None else scale, out, lse, weights,
-                           0 if weights is None else weights.shape[2], ws, ws.numel(), stream)
+        B.moe_kv_attention(self.dims, self.pool, seqs, q, q.stride(0) if T > 1 else Hq * D, Hq, cu_q, T, max_q,
+                           D ** -0.5 if scale is None else scale, out, lse, weights, w_stride, ws, ws.numel(), stream)
         return out
 
     def evict(self, weights: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int, budget: int,
@@ -117,18 +139,38 @@ class KVCache8:
         dst = self if dst is None else dst
         if dst.k.shape[1:] != self.k.shape[1:]:
             raise ValueError(f"dst holds pages of {tuple(dst.k.shape[1:])}, not {tuple(self.k.shape[1:])}")
-        seqs = self._seqs(page_table, seq_lens, max_len)
-        _want("weights", weights, torch.float32, 3, self.device, (seqs.B, self.kv_heads, weights.shape[2]))
-        _want("dst_table", dst_table, torch.int32, 2, self.device, (seqs.B, dst_table.shape[1]))
-        stream = self._stream(stream)
-        shape = (seqs.B, self.kv_heads, max(budget, 0))
-        with torch.cuda.stream(stream):
-            lens = torch.empty(seqs.B, dtype=torch.int32, device=self.device)
-            kept_w = torch.empty(shape, dtype=torch.float32, device=self.device)
-            kept = torch.empty(shape, dtype=torch.int32, device=self.device)
-        B.moe_kv_evict(self.dims, self.pool, seqs, weights, weights.shape[2], budget, sink, recent, dst.pool,
-                       dst_table, dst_table.shape[1], lens, kept_w, kept, stream)
-        return lens, kept_w, kept
+        n, width = self._want_table(page_table, seq_lens, None, "")
+        w_stride, dst_width = weights.shape[-1], dst_table.shape[-1]
+        if not (_is(weights, torch.float32, self._dev, (n, self.kv_heads, w_stride)) and
+                _is(dst_table, torch.int32, self._dev, (n, dst_width))):
+            _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
+            _want("dst_table", dst_table, torch.int32, 2, self.device, (n, dst_width))
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+            made = self._evict_outputs(n, budget)
+        else:
+            with torch.cuda.stream(stream):
+                made = self._evict_outputs(n, budget)
+        seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, max_len)
+        B.moe_kv_evict(self.dims, self.pool, seqs, weights, w_stride, budget, sink, recent, dst.pool, dst_table,
+                       dst_width, *made, stream)
+        return made
+
+    def _evict_outputs(self, n, budget):
+        shape = (n, self.kv_heads, max(budget, 0))
+        return (torch.empty(n, dtype=torch.int32, device=self.device),
+                torch.empty(shape, dtype=torch.float32, device=self.device),
+                torch.empty(shape, dtype=torch.int32, device=self.device))
+
+
+def _is(t, dtype, dev, shape):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _is_rows(t, dev, shape):
+    """A bf16 tensor of that shape, contiguous within each row of its first axis."""
+    return (t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev and t.stride(2) == 1 and
+            t.stride(1) == shape[2])
 
 
 def _want(name, t, dtype, ndim, device, shape=None, rows=False):
