@@ -323,8 +323,8 @@ MOE_API int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const m
  *  weights fp32 [B][Hkv][w_stride] or NULL, w_stride >= max_len: token t of
  *          (sequence, kv head) gains sum p_t over the call's queries and the
  *          heads of that kv head; other entries keep their values
- *  ws      scratch of moe_kv_attention_workspace_bytes(...) bytes, 256-byte
- *          aligned and zero-filled before its first use (calls leave its
+ *  ws      scratch of moe_kv_attention_workspace_bytes(...) bytes (weights: not 0
+ *          for a call that has them), 256-byte aligned and zero-filled before its first use (calls leave its
  *          counters zero; they sit at the same place for every size, so calls
  *          of any sizes may use one buffer in turn); calls that share it must
  *          not overlap on the GPU
@@ -334,7 +334,8 @@ MOE_API int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const m
  * Sums, maxima and outputs are held in fp32; the products' operands are exact
  * (q, K, V) or keep 16 bits (the softmax weights, at any size).  Results do not
  * depend on scheduling. */
-MOE_API size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int T_q);
+MOE_API size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int B, int T_q, int max_q,
+                                                int max_len, int weights);
 MOE_API int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_seqs* s, const void* q,
                              int64_t q_stride, int Hq, const int32_t* cu_q, int T_q, int max_q, float scale, void* out,
                              float* lse, float* weights, int64_t w_stride, void* ws, size_t ws_bytes,

@@ -77,7 +77,7 @@ _SIGS = {
     "moe_forward_w8": (_I, [ctypes.POINTER(moe_dims), ctypes.POINTER(moe_weights_w8), _P, _I, _P, _P, _Z, _P, _P,
                             _P, _P]),
     "moe_kv_append": (_I, [_R(moe_kv_dims), _R(moe_kv_pool), _R(moe_kv_seqs), _P, _P, _L, _P, _I, _P]),
-    "moe_kv_attention_workspace_bytes": (_Z, [_R(moe_kv_dims), _I, _I]),
+    "moe_kv_attention_workspace_bytes": (_Z, [_R(moe_kv_dims), _I, _I, _I, _I, _I, _I]),
     "moe_kv_attention": (_I, [_R(moe_kv_dims), _R(moe_kv_pool), _R(moe_kv_seqs), _P, _L, _I, _P, _I, _I, _F, _P, _P,
                               _P, _L, _P, _Z, _P]),
     "moe_kv_evict": (_I, [_R(moe_kv_dims), _R(moe_kv_pool), _R(moe_kv_seqs), _P, _L, _I, _I, _I, _R(moe_kv_pool), _P,
@@ -211,8 +211,9 @@ def moe_kv_append(dims: moe_kv_dims, pool: moe_kv_pool, seqs: moe_kv_seqs, k, v,
                                                        handle(stream)))
 
 
-def moe_kv_attention_workspace_bytes(dims: moe_kv_dims, Hq: int, T_q: int) -> int:
-    return lib().moe_kv_attention_workspace_bytes(ctypes.byref(dims), Hq, T_q)
+def moe_kv_attention_workspace_bytes(dims: moe_kv_dims, Hq: int, B: int, T_q: int, max_q: int, max_len: int,
+                                     weights: int) -> int:
+    return lib().moe_kv_attention_workspace_bytes(ctypes.byref(dims), Hq, B, T_q, max_q, max_len, weights)
 
 
 def moe_kv_attention(dims: moe_kv_dims, pool: moe_kv_pool, seqs: moe_kv_seqs, q, q_stride, Hq, cu_q, T_q, max_q,

@@ -146,7 +146,7 @@ struct KvAttention {
   float* weights;
   long long w_stride;
 };
-size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int T_q);
+size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights);
 int kv_attention_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, void* ws,
                         int* status, cudaStream_t stream, int* launches);
 // The attention for many query rows per sequence (tcgen05): out, and lse where given.

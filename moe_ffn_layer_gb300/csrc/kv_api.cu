@@ -64,9 +64,10 @@ int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_se
   return rc;
 }
 
-size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int T_q) {
-  if (check_dims(d) || Hq <= 0 || Hq % d->Hkv || T_q < 0) return 0;
-  return moe::kv_attention_ws_bytes(dims_of(d), Hq, T_q);
+size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int B, int T_q, int max_q, int max_len,
+                                        int weights) {
+  if (check_dims(d) || Hq <= 0 || Hq % d->Hkv || B < 0 || T_q < 0 || max_q < 0 || max_len < 0) return 0;
+  return moe::kv_attention_ws_bytes(dims_of(d), Hq, B, T_q, max_q, max_len, weights != 0);
 }
 
 int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_seqs* s, const void* q,
@@ -85,7 +86,8 @@ int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv
       !aligned(ws, 256))
     return MOE_ERR_UNSUPPORTED;
   const moe::KvDims kd = dims_of(d);
-  if (ws_bytes < moe::kv_attention_ws_bytes(kd, Hq, T_q)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < moe::kv_attention_ws_bytes(kd, Hq, s->B, T_q, max_q, s->max_len, weights != nullptr))
+    return MOE_ERR_WORKSPACE;
   int* status = nullptr;
   int sms = 0, n = 0;
   if ((rc = moe::current_device_info(&status, &sms))) return rc;

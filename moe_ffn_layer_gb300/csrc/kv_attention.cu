@@ -304,9 +304,10 @@ struct State {
         for (int i = 0; i < 4; ++i) o[j][p][i] = 0.f;
   }
 
-  // One step: the ring stage's 32 tokens from t0 on; row i sees those below sees[i].
+  // One step: the ring stage's 32 tokens from t0 on; row i sees those below
+  // sees[i].  keep (R = 1, nullable): where the lane's row keeps its scores.
   __device__ __forceinline__ void add(const QueryTile<D, R>& q, const Ring<D>& ring, int stage, int t0,
-                                      const int (&sees)[R], int sees_least, int lane) {
+                                      const int (&sees)[R], int sees_least, float* keep, int lane) {
     const uint32_t k_tile = ring.base + stage * Ring<D>::kStageBytes, v_tile = k_tile + kTok * D;
     const float4 page = *reinterpret_cast<const float4*>(ring.scales + stage * 4);
     const float ks0 = page.x, ks1 = page.y, vs0 = page.z, vs1 = page.w;
@@ -329,6 +330,11 @@ struct State {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             if (t0 + nt * 8 + 2 * (lane & 3) + e >= sees[i] || no_page(nt < 2 ? ks0 : ks1)) sc[nt][2 * i + e] = -INFINITY;
+    }
+    if (R == 1 && keep) {
+#pragma unroll
+      for (int nt = 0; nt < kTok / 8; ++nt)
+        *reinterpret_cast<float2*>(keep + t0 + nt * 8 + 2 * (lane & 3)) = make_float2(sc[nt][0], sc[nt][1]);
     }
     // The maximum that the exponents are taken against follows the scores only
     // where they pass it by more than 2^kSlack: the weights then stay below
@@ -480,6 +486,8 @@ struct Parts {
   int* ticket;   // by the CTA that began the unit
   float* o;      // [CTA][2][rows][D], relative to the row's maximum
   float2* ml;    // [CTA][2][rows]: maximum (base 2) and sum
+  float* scores;   // 8-row tiles, nullable: [T_q * Hq][pitch], every row's scores in units of the base-2 exponent
+  int pitch;
 };
 
 // The n parts of a unit, in order: a warp takes every kWarps-th row, a lane D / 32 columns.
@@ -594,6 +602,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kerne
   QueryTile<D, R> query;
   State<D, R> x;
   int sees[R], sees_least = 0, row0 = 0, rows = 0;
+  float* keep = nullptr;
   int stage = 0;
   bool fresh = true;   // the unit that cur is in begins, for this CTA
   int from = cur.step;
@@ -619,11 +628,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kerne
       for (int j = 0; j < R; ++j)   // (rows beyond the last real one see what it sees)
         sees[j] = max(cur.len - cur.n + min(row0 + (lane >> 2) + 8 * j, rows - 1) / g + 1, 0);
       sees_least = max(cur.len - cur.n + row0 / g + 1, 0);
+      if (R == 1 && parts.scores) {
+        const int row = row0 + (lane >> 2);
+        keep = row >= rows ? nullptr
+                           : parts.scores + (static_cast<size_t>(cur.first + row / g) * at.Hq + cur.h * g + row % g) * parts.pitch;
+      }
     }
     cp_async_wait<kStages - 1>();
     __syncwarp();
     const int t0 = cur.step * kSpan + warp * kTok;
-    if (t0 < cur.seen) x.add(query, ring, stage, t0, sees, sees_least, lane);
+    if (t0 < cur.seen) x.add(query, ring, stage, t0, sees, sees_least, keep, lane);
     stage = (stage + 1) % kStages;
     const bool whole = cur.step + 1 == cur.steps;
     if (whole || i + 1 == count) {
@@ -721,79 +735,207 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kerne
   cp_async_wait<0>();
 }
 
-// weights[b][h][t] += sum over the rows of (b, h) of exp(s_t - lse): a warp per
-// 32 tokens, all rows in order, so the sums do not depend on scheduling.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_weights_kernel(KvDims d, KvPool pool, KvSeqs s, KvAttention at,
-                                                                 int* status) {
-  extern __shared__ __align__(128) uint8_t smem[];
+// weights[b][h][t] += sum over the rows of (b, h) of exp(s_t - lse), the rows
+// in order, so that the sums do not depend on scheduling.
+
+// From the scores that the decode kernel kept (8-row tiles): a thread per token.
+// Writing and reading 4 bytes per row and token beats reading K again (D bytes)
+// up to these 8 rows.  Bound: HBM and L2, 4 rows + 8 bytes per token.
+constexpr int kGainThreads = 256;
+__global__ void __launch_bounds__(kGainThreads) kv_gain_kept_kernel(KvDims d, KvSeqs s, KvAttention at,
+                                                                    const float* __restrict__ scores, int pitch,
+                                                                    int* status) {
   chain_wait();
   ChainReleaseAtExit release;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv;
-  const int t0 = (blockIdx.x * kWarps + warp) * kTok;
+  const int h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv, t = blockIdx.x * kGainThreads + threadIdx.x;
   Tile tile;
-  if (!tile.find(s, at, b, g, 0, 16, d.page, status) || t0 >= tile.len) return;
-  Ring<D> ring{smem_u32(smem) + warp * Ring<D>::kStageBytes,
-               reinterpret_cast<float*>(smem + kWarps * Ring<D>::kStageBytes) + warp * 4};
-  int id[2];
-  ring.look(id, d, s, b, t0, tile.len);
-  ring.copy(0, id, d, pool, h, t0, tile.len, lane, status);
-  cp_async_commit();
-  cp_async_wait<0>();
-  __syncwarp();
-  const float ks0 = ring.scales[0], ks1 = ring.scales[1];
-  float sum[kTok / 8][2] = {};
-  for (int mt = 0; mt * 16 < tile.rows; ++mt) {
-    tile.find(s, at, b, g, mt, 16, d.page, status);
-    if (t0 >= tile.seen) continue;
-    QueryTile<D, 2> q;
-    q.load(at, tile.first, h, g, tile.row0, tile.rows, lane);
-    float sc[kTok / 8][4];
-    scores<D, 2>(sc, q, ring.base, lane);
+  if (!tile.find(s, at, b, g, 0, 8, d.page, status) || t >= tile.len) return;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int r = 0; r < tile.rows; ++r) {
+    const size_t at_row = static_cast<size_t>(tile.first + r / g) * at.Hq + h * g + r % g;
+    if (t < tile.sees(r, g)) sum += exp2_approx(scores[at_row * pitch + t] - at.lse[at_row] * kLog2e);
+  }
+  at.weights[(static_cast<long long>(b) * d.Hkv + h) * at.w_stride + t] += sum;
+}
+
+// More rows: the scores again, from K and the queries as MMA operands, which a
+// launch of their own lays out once in the order that lanes load them.
+struct Laid {
+  uint4* a;       // [tile][2 D / 32][32 lanes]: hi terms, then lo
+  float2* info;   // [tile][16]: what QueryTile::unscale is, and the row's lse in base 2 (+inf: adds nothing)
+};
+// The 16-row tiles of (sequence b, head h) lie at (floor(cu[b] g / 16) + b + tile) Hkv + h: a sequence of n
+// rows has at most floor(n / 16) + 1 beyond the next one's start, so none meet and no prefix sum is needed.
+__device__ __forceinline__ size_t laid_tile(const KvAttention& at, int first, int b, int g, int mt, int Hkv, int h) {
+  return (static_cast<size_t>(first) * g / 16 + b + mt) * Hkv + h;
+}
+size_t laid_tiles(int Hq, int Hkv, int B, int T_q) {
+  return (static_cast<size_t>(T_q) * (Hq / Hkv) / 16 + B) * Hkv;
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) kv_lay_kernel(KvDims d, KvSeqs s, KvAttention at, Laid laid, int* status) {
+  chain_wait();
+  ChainReleaseAtExit release;
+  const int lane = threadIdx.x & 31, mt = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
+  const int g = at.Hq / d.Hkv;
+  Tile tile;
+  if (!tile.find(s, at, b, g, mt, 16, d.page, status)) return;
+  QueryTile<D, 2> q;
+  q.load(at, tile.first, h, g, tile.row0, tile.rows, lane);
+  const size_t slot = laid_tile(at, tile.first, b, g, mt, d.Hkv, h);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+      laid.a[(slot * (D / 16) + i * (D / 32) + k) * 32 + lane] = make_uint4(q.a[i][k][0], q.a[i][k][1], q.a[i][k][2], q.a[i][k][3]);
+  if ((lane & 3) == 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = tile.row0 + (lane >> 2) + 8 * i;
-      const bool real = r < tile.rows;
-      const float lse = real ? at.lse[static_cast<size_t>(tile.first + r / g) * at.Hq + h * g + r % g] : INFINITY;
-      const float lse2 = lse * kLog2e;
-      const int sees = real ? tile.sees(r, g) : 0;
+      float lse = r < tile.rows ? at.lse[static_cast<size_t>(tile.first + r / g) * at.Hq + h * g + r % g] : -INFINITY;
+      if (lse == -INFINITY) lse = INFINITY;
+      laid.info[slot * 16 + (lane >> 2) + 8 * i] = make_float2(r < tile.rows ? q.unscale[i] : 0.f, lse * kLog2e);
+    }
+  }
+}
+
+// A CTA per 256 tokens of a (sequence, kv head): each of eight warps holds 32
+// tokens' codes in registers and runs over the row tiles that see them, the
+// even ones in warps 0 to 7, the odd ones in 8 to 15; the two sums are added at
+// the end.  Bound: the e4m3 MMAs and the exponentials' instructions alike.
+constexpr int kGainWarps = 16;
+template <int D>
+__global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPool pool, KvSeqs s, KvAttention at,
+                                                                  Laid laid, int* status) {
+  __shared__ float half[8][32];
+  chain_wait();
+  ChainReleaseAtExit release;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv;
+  const int t0 = (blockIdx.x * 8 + (warp & 7)) * kTok, part = warp >> 3, n = lane >> 2, c = lane & 3;
+  Tile tile;
+  if (!tile.find(s, at, b, g, 0, 16, d.page, status) || blockIdx.x * 8 * kTok >= tile.len) return;
+  float sum[kTok / 8][2] = {};
+  if (t0 < tile.len) {
+    uint4 k[kTok / 8][D / 64];
+    float ks[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + 16 * i;
+      const int id = t < tile.len ? __ldg(s.table + static_cast<size_t>(b) * s.width + (t >> d.shift)) : -1;
+      const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(pool.num_pages);
+      if (t < tile.len && !ok) set_status(status, MOE_ERR_DEVICE_CHECK);
+      ks[i] = ok ? __ldg(pool.k_scale + static_cast<size_t>(id) * d.Hkv + h) : __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+      for (int nt = 2 * i; nt < 2 * i + 2; ++nt) {
+        const bool in = ok && t0 + nt * 8 + n < tile.len;
+        const uint8_t* row = pool.k + (in ? kv_row(id, d.Hkv, h, d.page, (t0 + nt * 8 + n) & (d.page - 1), D) : 0);
+#pragma unroll
+        for (int f = 0; f < D / 64; ++f)
+          k[nt][f] = in ? __ldg(reinterpret_cast<const uint4*>(row) + (D == 128 ? 2 * c + f : c)) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    const int tiles = (tile.rows + 15) / 16;
+    // the first row that sees token t0
+    const long long row_first = static_cast<long long>(t0 - (tile.len - tile.n)) * g;
+    int mt = row_first > 0 ? static_cast<int>(row_first / 16) : 0;
+    mt += (mt & 1) != part;
+    for (; mt < tiles; mt += 2) {
+      const size_t slot = laid_tile(at, tile.first, b, g, mt, d.Hkv, h);
+      uint32_t a[2][D / 32][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f)
+          *reinterpret_cast<uint4*>(a[i][f]) = __ldg(laid.a + (slot * (D / 16) + i * (D / 32) + f) * 32 + lane);
+      const float2 r0 = __ldg(laid.info + slot * 16 + n), r1 = __ldg(laid.info + slot * 16 + 8 + n);
+      const int sees0 = tile.sees(mt * 16, g);   // of the tile's first row
+      const bool masks = t0 + kTok > sees0 || no_page(ks[0]) || no_page(ks[1]);
+      int seen[2] = {0, 0};
+      if (masks) {
+        seen[0] = tile.sees(mt * 16 + n, g);
+        seen[1] = tile.sees(mt * 16 + 8 + n, g);
+      }
 #pragma unroll
       for (int nt = 0; nt < kTok / 8; ++nt) {
-        const float ks = nt < 2 ? ks0 : ks1;
+        float x[2][4] = {};
+#pragma unroll
+        for (int f = 0; f < D / 64; ++f)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_e4m3(x[i], a[i][2 * f], k[nt][f].x, k[nt][f].y);
+            mma_e4m3(x[i], a[i][2 * f + 1], k[nt][f].z, k[nt][f].w);
+          }
+        const float f0 = ks[nt >> 1] * r0.x, f1 = ks[nt >> 1] * r1.x;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int t = t0 + nt * 8 + 2 * (lane & 3) + e;
-          if (t < sees && !no_page(ks)) sum[nt][e] += exp2_approx(sc[nt][2 * i + e] * (ks * q.unscale[i]) - lse2);
+          float p0 = exp2_approx(fmaf(fmaf(x[1][e], 0.0625f, x[0][e]), f0, -r0.y));
+          float p1 = exp2_approx(fmaf(fmaf(x[1][2 + e], 0.0625f, x[0][2 + e]), f1, -r1.y));
+          if (masks) {
+            const int t = t0 + nt * 8 + 2 * c + e;
+            if (t >= seen[0] || no_page(ks[nt >> 1])) p0 = 0.f;
+            if (t >= seen[1] || no_page(ks[nt >> 1])) p1 = 0.f;
+          }
+          sum[nt][e] += p0 + p1;
         }
       }
     }
   }
-  float* w = at.weights + (static_cast<long long>(b) * d.Hkv + h) * at.w_stride;
 #pragma unroll
   for (int nt = 0; nt < kTok / 8; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float v = sum[nt][e];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      const int t = t0 + nt * 8 + 2 * (lane & 3) + e;
-      if ((lane >> 2) == 0 && t < tile.len) w[t] += v;
+      for (int o = 4; o < 32; o <<= 1) sum[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][e], o);
+      if (part == 1 && n == 0) half[warp & 7][nt * 8 + 2 * c + e] = sum[nt][e];
     }
+  __syncthreads();
+  if (part == 0 && n == 0) {
+    float* w = at.weights + (static_cast<long long>(b) * d.Hkv + h) * at.w_stride;
+#pragma unroll
+    for (int nt = 0; nt < kTok / 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = nt * 8 + 2 * c + e;
+        if (t0 + i < tile.len) w[t0 + i] += sum[nt][e] + half[warp][i];
+      }
+  }
 }
 
-// Workspace: the tickets first, at the same place for every call, then the parts, then the log-sum-exps.
+// Workspace: the tickets first, at the same place for every call, then the
+// parts, the log-sum-exps, and for the weights the kept scores or the laid out
+// queries.
 struct Layout {
-  size_t o, ml, lse, total;
+  size_t o, ml, lse, scores, laid, info, total;
+  int pitch;
 };
-Layout layout(const KvDims& d, int Hq, int T_q) {
+bool few_rows(int Hq, int Hkv, int max_q) { return static_cast<long long>(max_q) * (Hq / Hkv) <= 8; }
+Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights) {
   constexpr size_t slots = static_cast<size_t>(kSMs) * ctas_per_sm<2>() * 2 * 16;
   static_assert(slots >= static_cast<size_t>(kSMs) * ctas_per_sm<1>() * 2 * 8, "slots of 8-row tiles");
   static_assert(kSMs * ctas_per_sm<1>() <= kMostCtas && kSMs * ctas_per_sm<2>() <= kMostCtas, "tickets");
   Layout w{};
-  w.o = align_up(kMostCtas * sizeof(int));
-  w.ml = w.o + align_up(slots * d.D * sizeof(float));
-  w.lse = w.ml + align_up(slots * sizeof(float2));
-  w.total = w.lse + align_up(static_cast<size_t>(T_q) * Hq * sizeof(float));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += align_up(bytes);
+    return r;
+  };
+  take(kMostCtas * sizeof(int));
+  const size_t rows = static_cast<size_t>(T_q) * Hq;
+  w.o = take(slots * d.D * sizeof(float));
+  w.ml = take(slots * sizeof(float2));
+  w.lse = take(rows * sizeof(float));
+  if (weights && few_rows(Hq, d.Hkv, max_q)) {
+    w.pitch = static_cast<int>((static_cast<long long>(max_len) + kTok - 1) / kTok * kTok);
+    w.scores = take(rows * w.pitch * sizeof(float));
+  } else if (weights) {
+    const size_t tiles = laid_tiles(Hq, d.Hkv, B, T_q);
+    w.laid = take(tiles * 32 * d.D);
+    w.info = take(tiles * 16 * sizeof(float2));
+  }
+  w.total = at;
   return w;
 }
 
@@ -818,33 +960,42 @@ int launch_decode(const KvDims& d, const KvPool& pool, const KvSeqs& s, const Kv
 template <int D>
 int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, void* ws, int* status,
            cudaStream_t stream, int* launches) {
-  const Layout w = layout(d, a.Hq, a.T_q);
+  const Layout w = layout(d, a.Hq, s.B, a.T_q, a.max_q, s.max_len, a.weights != nullptr);
   uint8_t* base = static_cast<uint8_t*>(ws);
   if (a.weights && !a.lse) a.lse = reinterpret_cast<float*>(base + w.lse);
+  const bool few = few_rows(a.Hq, d.Hkv, a.max_q);   // tiles of 8 rows where every sequence's rows fit one, else of 16
   const Parts parts{reinterpret_cast<int*>(base), reinterpret_cast<float*>(base + w.o),
-                    reinterpret_cast<float2*>(base + w.ml)};
-  // tiles of 8 rows where every sequence's rows fit one, else of 16; many rows go to the tcgen05 kernel
+                    reinterpret_cast<float2*>(base + w.ml),
+                    a.weights && few ? reinterpret_cast<float*>(base + w.scores) : nullptr, w.pitch};
   const long long rows = static_cast<long long>(a.max_q) * (a.Hq / d.Hkv);
-  const int rc = rows > kDecodeRows
-                     ? kv_prefill_launch(d, pool, s, a, status, stream, launches)
-                 : rows <= 8
-                     ? launch_decode<D, 1>(d, pool, s, a, parts, status, stream, launches)
-                     : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
-  if (rc) return rc;
-  if (a.weights) {
-    const unsigned blocks = (static_cast<unsigned>(s.max_len) + kWarps * kTok - 1) / (kWarps * kTok);
-    if (launch_chained(kv_weights_kernel<D>, dim3(blocks, d.Hkv, s.B), dim3(kWarps * 32),
-                       kWarps * (Ring<D>::kStageBytes + 4 * sizeof(float)), stream, d, pool, s, a,
-                       status) != cudaSuccess)
+  const int rc = rows > kDecodeRows ? kv_prefill_launch(d, pool, s, a, status, stream, launches)   // tcgen05
+                 : few              ? launch_decode<D, 1>(d, pool, s, a, parts, status, stream, launches)
+                                    : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
+  if (rc || !a.weights || s.max_len == 0) return rc;
+  if (few) {
+    const unsigned blocks = (static_cast<unsigned>(s.max_len) + kGainThreads - 1) / kGainThreads;
+    if (launch_chained(kv_gain_kept_kernel, dim3(blocks, d.Hkv, s.B), dim3(kGainThreads), 0, stream, d, s, a,
+                       parts.scores, parts.pitch, status) != cudaSuccess)
       return MOE_ERR_CUDA;
     ++*launches;
+    return MOE_OK;
   }
+  const Laid laid{reinterpret_cast<uint4*>(base + w.laid), reinterpret_cast<float2*>(base + w.info)};
+  const unsigned tiles = static_cast<unsigned>((rows + 15) / 16), blocks = (static_cast<unsigned>(s.max_len) + 255) / 256;
+  if (launch_chained(kv_lay_kernel<D>, dim3((tiles + 3) / 4, d.Hkv, s.B), dim3(128), 0, stream, d, s, a, laid,
+                     status) != cudaSuccess ||
+      launch_chained(kv_gain_kernel<D>, dim3(blocks, d.Hkv, s.B), dim3(kGainWarps * 32), 0, stream, d, pool, s, a, laid,
+                     status) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  *launches += 2;
   return MOE_OK;
 }
 
 }  // namespace
 
-size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int T_q) { return layout(d, Hq, T_q).total; }
+size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights) {
+  return layout(d, Hq, B, T_q, max_q, max_len, weights).total;
+}
 
 int kv_attention_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, void* ws,
                         int* status, cudaStream_t stream, int* launches) {

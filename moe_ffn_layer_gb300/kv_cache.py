@@ -42,8 +42,7 @@ class KVCache8:
         self.num_pages, self.kv_heads, self.page, self.head_dim = k.shape
         self.dims = B.moe_kv_dims(self.kv_heads, self.head_dim, self.page)
         self.pool = B.moe_kv_pool(*(B.ptr(t) for t in (k, v, k_scale, v_scale)), self.num_pages)
-        self._ws = {}     # by stream: calls of different streams may overlap
-        self._need = {}   # workspace bytes by sizes
+        self._ws = {}   # by stream: calls of different streams may overlap
 
     def _want_table(self, page_table, seq_lens, cu, cu_name):
         """Checks the sequences' tensors; returns the table's rows and width."""
@@ -120,9 +119,7 @@ class KVCache8:
             w_stride = weights.shape[-1]
             if not _is(weights, torch.float32, dev, (n, self.kv_heads, w_stride)):
                 _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
-        need = self._need.get((Hq, T))
-        if need is None:
-            need = self._need[Hq, T] = B.moe_kv_attention_workspace_bytes(self.dims, Hq, T)
+        need = B.moe_kv_attention_workspace_bytes(self.dims, Hq, n, T, max_q, max_len, weights is not None)
         ws = self.workspace(need, stream)
         B.moe_kv_attention(self.dims, self.pool, seqs, q, q.stride(0) if T > 1 else Hq * D, Hq, cu_q, T, max_q,
                            D ** -0.5 if scale is None else scale, out, lse, weights, w_stride, ws, ws.numel(), stream)

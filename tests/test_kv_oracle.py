@@ -137,8 +137,8 @@ def test_calls_refuse_bad_arguments_before_a_launch():
     assert code(B.moe_kv_attention, *attn(w=fake, ws_=255)) == -1 and code(B.moe_kv_attention, *attn(nb=0)) == -3
     assert code(B.moe_kv_attention, *attn(ws=fake + 128)) == -2
     assert B.moe_kv_attention(*attn(T=0, q=None)) == 0 and B.moe_kv_attention(*attn(s=B.moe_kv_seqs(None, None, 0, 0, 0))) == 0
-    assert B.moe_kv_attention_workspace_bytes(good, 4, 1) > 0
-    assert B.moe_kv_attention_workspace_bytes(good, 5, 1) == 0
+    assert 0 < B.moe_kv_attention_workspace_bytes(good, 4, 1, 1, 1, 256, 0) < B.moe_kv_attention_workspace_bytes(good, 4, 1, 1, 1, 256, 1)
+    assert B.moe_kv_attention_workspace_bytes(good, 5, 1, 1, 1, 256, 0) == 0
 
     def app(d=good, p=pool, s=seqs, k=fake, v=fake, stride=256, cu=fake, T=1):
         return (d, p, s, k, v, stride, cu, T, None)
