@@ -10,13 +10,11 @@
 //
 // Both products run on the tensor cores with fp32 accumulation, their operands
 // exact or kept to 16 bits at least:
-//  - scores: e4m3 MMAs, a K code as it is (no conversion).  A query row is
-//    scaled by a power of two to a largest magnitude in [2^7, 2^8) and enters
-//    as two e4m3 terms, hi = e4m3(x) and lo = e4m3(16 (x - hi)), with a sum
-//    each: together a bf16's eight bits, down to 2^-21 of the row's largest.
-//    (The e4m3 MMA rounds its sums as fp32 additions do, measured; the f16 one,
-//    which would also need K converted, truncates them and runs at half the
-//    rate per instruction for half the depth.)
+//  - scores: f16, which holds a K code exactly.  A query row is scaled by a
+//    power of two to a largest magnitude in [2^7, 2^8), which keeps all of a
+//    bf16's bits down to 2^-21 of it.  (An e4m3 MMA takes the codes as they
+//    are, but this GPU runs it as conversions and f16 MMAs: 5.8 clocks an SM
+//    for 16x8x32 when its operands change, against 4.9 for two f16 ones.)
 //  - output: bf16, which has fp32's range.  A V code becomes bf16 exactly; a
 //    weight p * vs enters as two bf16 terms, so that it keeps 16 bits however
 //    far it lies below the row's largest (a long sequence's many small weights
@@ -46,6 +44,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // The bytes of v that sel picks (two code bytes, each followed by its sign
 // copy) as two bf16 of the codes' values.
 template <uint32_t kSel>
@@ -62,10 +66,10 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t* hi, uin
   *lo = pack_bf16x2(a - __uint_as_float(ua & 0xFFFF0000u), b - __uint_as_float(ub & 0xFFFF0000u));
 }
 
-// d += a (16x32, row) * b (32x8, col), e4m3 inputs, fp32 accumulator
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// d += a (16x16, row) * b (16x8, col), f16 inputs, fp32 accumulator
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -109,27 +113,21 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Four floats to two words of four e4m3 codes: hi, and lo = e4m3(16 (x - hi)).
-__device__ __forceinline__ void split_e4m3x4(float a, float b, float c, float d, uint32_t* hi, uint32_t* lo) {
-  const uint32_t h = e4m3x2_of(a, b) | e4m3x2_of(c, d) << 16;
-  *hi = h;
-  *lo = e4m3x2_of(16.f * (a - e4m3_to_f32(h)), 16.f * (b - e4m3_to_f32(h >> 8))) |
-        e4m3x2_of(16.f * (c - e4m3_to_f32(h >> 16)), 16.f * (d - e4m3_to_f32(h >> 24))) << 16;
-}
-
 // A tile's 8 R query rows as MMA operands, R = 1 or 2 of them per lane: lane/4
-// and lane/4 + 8.  With R = 1 the MMA's upper eight rows take the lo terms.
-// The MMA's K index may stand for any order of the head dimension as long as
-// both operands agree: lane (n, c) of a K operand holds 16-byte chunk 2c + h of
-// token n's row (chunk c for D = 64), eight codes per K step, so the query
-// operand of step 2h + r holds d = 16 (2c + h) + 8r + {0..3} and + {4..7}.
+// and lane/4 + 8 (zeros for R = 1).  The MMA's K index may stand for any order
+// of the head dimension as long as both operands agree: lane (n, c) of a K
+// operand holds 16-byte chunk 2c + h of token n's row (chunk c for D = 64), four
+// codes per K step, so the query operand of step 4h + r holds
+// d = 16 (2c + h) + 4r + {0, 1} and + {2, 3}.
 template <int D, int R>
 struct QueryTile {
-  uint32_t a[R][D / 32][4];   // R = 1: {hi, lo}; R = 2: hi, then lo
-  float unscale[R];           // scale * log2(e) / (the row's power of two)
+  uint32_t a[D / 16][4];
+  float unscale[R];   // scale * log2(e) / (the row's power of two)
 
   __device__ __forceinline__ void load(const KvAttention& at, int first, int h, int g, int row0, int rows, int lane) {
     const int c = lane & 3;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) a[k][1] = a[k][3] = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int r = row0 + (lane >> 2) + 8 * i;
@@ -156,16 +154,10 @@ struct QueryTile {
       unscale[i] = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : at.scale * kLog2e * down;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
-        uint32_t hi[2], lo[2];
-        split_e4m3x4(bf16_lo(raw[k].x) * up, bf16_hi(raw[k].x) * up, bf16_lo(raw[k].y) * up, bf16_hi(raw[k].y) * up,
-                     &hi[0], &lo[0]);
-        split_e4m3x4(bf16_lo(raw[k].z) * up, bf16_hi(raw[k].z) * up, bf16_lo(raw[k].w) * up, bf16_hi(raw[k].w) * up,
-                     &hi[1], &lo[1]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          a[0][k][2 * j + i] = hi[j];
-          a[R - 1][k][2 * j + (R == 1 ? 1 : i)] = lo[j];
-        }
+        a[2 * k][i] = pack_f16x2(bf16_lo(raw[k].x) * up, bf16_hi(raw[k].x) * up);
+        a[2 * k][2 + i] = pack_f16x2(bf16_lo(raw[k].y) * up, bf16_hi(raw[k].y) * up);
+        a[2 * k + 1][i] = pack_f16x2(bf16_lo(raw[k].z) * up, bf16_hi(raw[k].z) * up);
+        a[2 * k + 1][2 + i] = pack_f16x2(bf16_lo(raw[k].w) * up, bf16_hi(raw[k].w) * up);
       }
     }
   }
@@ -179,18 +171,19 @@ __device__ __forceinline__ void scores(float (&s)[kTok / 8][2 * R], const QueryT
   const int n = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < kTok / 8; ++nt) {
-    float acc[R][4] = {};
+    float x[4] = {};
 #pragma unroll
     for (int half = 0; half < D / 64; ++half) {
       const uint4 v = lds_u4(k_tile + swz<D>(nt * 8 + n, D == 128 ? 2 * c + half : c));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        mma_e4m3(acc[r], q.a[r][2 * half], v.x, v.y);
-        mma_e4m3(acc[r], q.a[r][2 * half + 1], v.z, v.w);
+      for (int r = 0; r < 4; ++r) {
+        const uint2 b = e4m3x4_to_f16x4(w[r]);
+        mma_f16(x, q.a[4 * half + r], b.x, b.y);
       }
     }
 #pragma unroll
-    for (int e = 0; e < 2 * R; ++e) s[nt][e] = fmaf(R == 1 ? acc[0][e + 2] : acc[R - 1][e], 0.0625f, acc[0][e]);
+    for (int e = 0; e < 2 * R; ++e) s[nt][e] = x[e];
   }
 }
 
@@ -762,7 +755,7 @@ __global__ void __launch_bounds__(kGainThreads) kv_gain_kept_kernel(KvDims d, Kv
 // More rows: the scores again, from K and the queries as MMA operands, which a
 // launch of their own lays out once in the order that lanes load them.
 struct Laid {
-  uint4* a;       // [tile][2 D / 32][32 lanes]: hi terms, then lo
+  uint4* a;       // [tile][D / 16][32 lanes]
   float2* info;   // [tile][16]: what QueryTile::unscale is, and the row's lse in base 2 (+inf: adds nothing)
 };
 // The 16-row tiles of (sequence b, head h) lie at (floor(cu[b] g / 16) + b + tile) Hkv + h: a sequence of n
@@ -786,10 +779,8 @@ __global__ void __launch_bounds__(128) kv_lay_kernel(KvDims d, KvSeqs s, KvAtten
   q.load(at, tile.first, h, g, tile.row0, tile.rows, lane);
   const size_t slot = laid_tile(at, tile.first, b, g, mt, d.Hkv, h);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k)
-      laid.a[(slot * (D / 16) + i * (D / 32) + k) * 32 + lane] = make_uint4(q.a[i][k][0], q.a[i][k][1], q.a[i][k][2], q.a[i][k][3]);
+  for (int k = 0; k < D / 16; ++k)
+    laid.a[(slot * (D / 16) + k) * 32 + lane] = make_uint4(q.a[k][0], q.a[k][1], q.a[k][2], q.a[k][3]);
   if ((lane & 3) == 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -804,84 +795,116 @@ __global__ void __launch_bounds__(128) kv_lay_kernel(KvDims d, KvSeqs s, KvAtten
 // A CTA per 256 tokens of a (sequence, kv head): each of eight warps holds 32
 // tokens' codes in registers and runs over the row tiles that see them, the
 // even ones in warps 0 to 7, the odd ones in 8 to 15; the two sums are added at
-// the end.  Bound: the e4m3 MMAs and the exponentials' instructions alike.
-constexpr int kGainWarps = 16;
+// the end.  The tiles come through a ring in shared memory that all warps read.
+constexpr int kGainWarps = 16, kGainStages = 4;
+template <int D>
+struct GainStage {
+  uint4 a[2][D / 16][32];   // a pair of tiles
+  float2 info[2][16];
+};
 template <int D>
 __global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPool pool, KvSeqs s, KvAttention at,
                                                                   Laid laid, int* status) {
   __shared__ float half[8][32];
+  __shared__ __align__(16) GainStage<D> ring[kGainStages];
   chain_wait();
   ChainReleaseAtExit release;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv;
-  const int t0 = (blockIdx.x * 8 + (warp & 7)) * kTok, part = warp >> 3, n = lane >> 2, c = lane & 3;
+  const int first = blockIdx.x * 8 * kTok, t0 = first + (warp & 7) * kTok, part = warp >> 3, n = lane >> 2, c = lane & 3;
   Tile tile;
-  if (!tile.find(s, at, b, g, 0, 16, d.page, status) || blockIdx.x * 8 * kTok >= tile.len) return;
-  float sum[kTok / 8][2] = {};
-  if (t0 < tile.len) {
-    uint4 k[kTok / 8][D / 64];
-    float ks[2];
+  if (!tile.find(s, at, b, g, 0, 16, d.page, status) || first >= tile.len) return;
+  uint2 k[kTok / 8][D / 16];
+  float ks[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = t0 + 16 * i;
-      const int id = t < tile.len ? __ldg(s.table + static_cast<size_t>(b) * s.width + (t >> d.shift)) : -1;
-      const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(pool.num_pages);
-      if (t < tile.len && !ok) set_status(status, MOE_ERR_DEVICE_CHECK);
-      ks[i] = ok ? __ldg(pool.k_scale + static_cast<size_t>(id) * d.Hkv + h) : __uint_as_float(0x7FFFFFFFu);
+  for (int i = 0; i < 2; ++i) {
+    const int t = t0 + 16 * i;
+    const int id = t < tile.len ? __ldg(s.table + static_cast<size_t>(b) * s.width + (t >> d.shift)) : -1;
+    const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(pool.num_pages);
+    if (t < tile.len && !ok) set_status(status, MOE_ERR_DEVICE_CHECK);
+    ks[i] = ok ? __ldg(pool.k_scale + static_cast<size_t>(id) * d.Hkv + h) : __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
-      for (int nt = 2 * i; nt < 2 * i + 2; ++nt) {
-        const bool in = ok && t0 + nt * 8 + n < tile.len;
-        const uint8_t* row = pool.k + (in ? kv_row(id, d.Hkv, h, d.page, (t0 + nt * 8 + n) & (d.page - 1), D) : 0);
+    for (int nt = 2 * i; nt < 2 * i + 2; ++nt) {
+      const bool in = ok && t0 + nt * 8 + n < tile.len;
+      const uint8_t* row = pool.k + (in ? kv_row(id, d.Hkv, h, d.page, (t0 + nt * 8 + n) & (d.page - 1), D) : 0);
 #pragma unroll
-        for (int f = 0; f < D / 64; ++f)
-          k[nt][f] = in ? __ldg(reinterpret_cast<const uint4*>(row) + (D == 128 ? 2 * c + f : c)) : make_uint4(0, 0, 0, 0);
-      }
-    }
-    const int tiles = (tile.rows + 15) / 16;
-    // the first row that sees token t0
-    const long long row_first = static_cast<long long>(t0 - (tile.len - tile.n)) * g;
-    int mt = row_first > 0 ? static_cast<int>(row_first / 16) : 0;
-    mt += (mt & 1) != part;
-    for (; mt < tiles; mt += 2) {
-      const size_t slot = laid_tile(at, tile.first, b, g, mt, d.Hkv, h);
-      uint32_t a[2][D / 32][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int f = 0; f < D / 32; ++f)
-          *reinterpret_cast<uint4*>(a[i][f]) = __ldg(laid.a + (slot * (D / 16) + i * (D / 32) + f) * 32 + lane);
-      const float2 r0 = __ldg(laid.info + slot * 16 + n), r1 = __ldg(laid.info + slot * 16 + 8 + n);
-      const int sees0 = tile.sees(mt * 16, g);   // of the tile's first row
-      const bool masks = t0 + kTok > sees0 || no_page(ks[0]) || no_page(ks[1]);
-      int seen[2] = {0, 0};
-      if (masks) {
-        seen[0] = tile.sees(mt * 16 + n, g);
-        seen[1] = tile.sees(mt * 16 + 8 + n, g);
-      }
-#pragma unroll
-      for (int nt = 0; nt < kTok / 8; ++nt) {
-        float x[2][4] = {};
-#pragma unroll
-        for (int f = 0; f < D / 64; ++f)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_e4m3(x[i], a[i][2 * f], k[nt][f].x, k[nt][f].y);
-            mma_e4m3(x[i], a[i][2 * f + 1], k[nt][f].z, k[nt][f].w);
-          }
-        const float f0 = ks[nt >> 1] * r0.x, f1 = ks[nt >> 1] * r1.x;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float p0 = exp2_approx(fmaf(fmaf(x[1][e], 0.0625f, x[0][e]), f0, -r0.y));
-          float p1 = exp2_approx(fmaf(fmaf(x[1][2 + e], 0.0625f, x[0][2 + e]), f1, -r1.y));
-          if (masks) {
-            const int t = t0 + nt * 8 + 2 * c + e;
-            if (t >= seen[0] || no_page(ks[nt >> 1])) p0 = 0.f;
-            if (t >= seen[1] || no_page(ks[nt >> 1])) p1 = 0.f;
-          }
-          sum[nt][e] += p0 + p1;
-        }
+      for (int f = 0; f < D / 64; ++f) {
+        const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(row) + (D == 128 ? 2 * c + f : c)) : make_uint4(0, 0, 0, 0);
+        k[nt][4 * f] = e4m3x4_to_f16x4(v.x);
+        k[nt][4 * f + 1] = e4m3x4_to_f16x4(v.y);
+        k[nt][4 * f + 2] = e4m3x4_to_f16x4(v.z);
+        k[nt][4 * f + 3] = e4m3x4_to_f16x4(v.w);
       }
     }
   }
+  // Row r sees token t where r >= (t - (len - n)) g.  Pairs of row tiles, from
+  // the first that sees the CTA's first token.
+  const int base = tile.len - tile.n, tiles = (tile.rows + 15) / 16, pairs = (tiles + 1) / 2;
+  const int pair0 = first > base ? (first - base) * g / 32 : 0;
+  const int need_any = t0 < tile.len ? max(t0 - base, 0) * g : INT_MAX;
+  const int need_all = max(min(t0 + kTok, tile.len) - 1 - base, 0) * g;
+  const bool gone = no_page(ks[0]) || no_page(ks[1]);
+  const auto fetch = [&](int pair) {
+    if (pair < pairs) {
+      GainStage<D>& st = ring[pair % kGainStages];
+#pragma unroll
+      for (int i = threadIdx.x; i < 2 * (D / 16) * 32; i += kGainWarps * 32) {
+        const int mt = 2 * pair + i / (D / 16 * 32), j = i % (D / 16 * 32);
+        if (mt < tiles)
+          cp_async16(smem_u32(&st.a[0][0][0] + i), laid.a + laid_tile(at, tile.first, b, g, mt, d.Hkv, h) * (D / 16 * 32) + j);
+      }
+      if (threadIdx.x < 16) {
+        const int mt = 2 * pair + threadIdx.x / 8;
+        if (mt < tiles)
+          cp_async16(smem_u32(&st.info[0][0] + 2 * threadIdx.x),
+                     laid.info + laid_tile(at, tile.first, b, g, mt, d.Hkv, h) * 16 + threadIdx.x % 8 * 2);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kGainStages - 1; ++i) fetch(pair0 + i);
+  float sum[kTok / 8][2] = {};
+  for (int pair = pair0; pair < pairs; ++pair) {
+    cp_async_wait<kGainStages - 2>();
+    __syncthreads();   // everybody's copies of this pair are there; everybody is done with the one before
+    fetch(pair + kGainStages - 1);
+    const int mt = 2 * pair + part;
+    if (mt >= tiles || mt * 16 + 15 < need_any) continue;
+    const GainStage<D>& st = ring[pair % kGainStages];
+    float x[kTok / 8][4] = {};
+#pragma unroll
+    for (int f = 0; f < D / 16; ++f) {
+      uint32_t a[4];
+      *reinterpret_cast<uint4*>(a) = lds_u4(smem_u32(&st.a[part][f][lane]));
+#pragma unroll
+      for (int nt = 0; nt < kTok / 8; ++nt) mma_f16(x[nt], a, k[nt][f].x, k[nt][f].y);
+    }
+    const float2 r0 = st.info[part][n], r1 = st.info[part][8 + n];
+#pragma unroll
+    for (int nt = 0; nt < kTok / 8; ++nt) {
+      const float f0 = ks[nt >> 1] * r0.x, f1 = ks[nt >> 1] * r1.x;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[nt][e] = exp2_approx(fmaf(x[nt][e], f0, -r0.y));
+        x[nt][2 + e] = exp2_approx(fmaf(x[nt][2 + e], f1, -r1.y));
+      }
+    }
+    if (mt * 16 < need_all || gone) {
+#pragma unroll
+      for (int nt = 0; nt < kTok / 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int need = (t0 + nt * 8 + 2 * c + e - base) * g;
+          if (mt * 16 + n < need || no_page(ks[nt >> 1])) x[nt][e] = 0.f;
+          if (mt * 16 + 8 + n < need || no_page(ks[nt >> 1])) x[nt][2 + e] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < kTok / 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sum[nt][e] += x[nt][e] + x[nt][2 + e];
+  }
+  cp_async_wait<0>();
 #pragma unroll
   for (int nt = 0; nt < kTok / 8; ++nt)
 #pragma unroll

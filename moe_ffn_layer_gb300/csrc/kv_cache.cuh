@@ -48,6 +48,15 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
   return r;
 }
 
+// Four e4m3 codes as f16 pairs (codes 0 and 1, 2 and 3): the hardware's conversion, exact.
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t v) {
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(v));
+  return r;
+}
+
 // Sixteen codes times a ratio, rounded to codes again (the codes 0x7f and 0xff, which the cache never holds, read as +-480).
 __device__ __forceinline__ uint4 e4m3x16_scaled(const uint4& v, float ratio) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -144,14 +144,6 @@ __device__ __forceinline__ uint64_t smem_desc_n128(uint32_t saddr, uint32_t bloc
          static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
 }
 
-// Two e4m3 codes (the halves of 16 bits) as f16: the hardware conversion, exact.
-__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t v) {
-  uint2 r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(r.x), "=r"(r.y)
-      : "r"(v));
-  return r;
-}
 // Four codes as bf16 times `unit` (a bf16 pair of 2^(120 + e))
 __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t v, uint32_t unit) {
   return make_uint2(bf16x2_mul((prmt(v, 0u, 0x9180u) << 4) & 0x87F087F0u, unit),
