@@ -32,10 +32,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTok = 32;          // tokens of a warp's step
 constexpr int kWarps = 4;
 constexpr int kSpan = kWarps * kTok;   // tokens of a CTA's step: one step of each warp
-constexpr int kStages = 2;
 constexpr int kDecodeRows = 64;        // query rows of a kv head up to which the decode kernel is taken
 constexpr float kSlack = 8.f;
-constexpr int kLeast = 2;              // steps that a CTA takes at least
 constexpr int kSMs = 152;         // of a GB300: the plan of a call depends on its sizes alone
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -523,8 +521,15 @@ __device__ __forceinline__ void join_parts(const Parts& parts, int c0, int n, co
   }
 }
 
+// CTAs an SM holds, and stages of a warp's ring.  Tiles of 8 rows: two CTAs of
+// three stages (64 sequences of 513 to 16384 tokens: 206 us) against three of
+// two (227 us: 168 registers, spilled); tiles of 16 rows have 8 KB more to meet
+// in, so two of two stages (57 us on 4 queries each of 16 sequences, 83 us at
+// one CTA of three).
 template <int R>
-constexpr int ctas_per_sm() { return R == 1 ? 3 : 2; }   // (registers; measured: three of two stages beat two of three)
+constexpr int ctas_per_sm() { return 2; }
+template <int R>
+constexpr int ring_stages() { return R == 1 ? 3 : 2; }
 
 // Bound: HBM (2 D bytes per token and kv head, read once).  Each of a CTA's
 // four warps takes a quarter of every 128-token span, with a ring of
@@ -534,7 +539,7 @@ template <int D, int R>
 __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kernel(KvDims d, KvPool pool, KvSeqs s,
                                                                                  KvAttention at, Parts parts,
                                                                                  int* status) {
-  constexpr int kRows = 8 * R, kPitch = D + 4;
+  constexpr int kRows = 8 * R, kPitch = D + 4, kStages = ring_stages<R>();
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 all_ml[kWarps * kRows];
   __shared__ int last;
@@ -546,7 +551,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kerne
   uint32_t total = 0;   // (below 2^31: checked on the host for the largest lengths)
   for (int base = 0; base < s.B; base += 32)
     total += __reduce_add_sync(0xFFFFFFFFu, steps_of(cur, base + lane, d, s, at, kRows, status));
-  const uint32_t ctas = min((total + kLeast - 1) / kLeast, gridDim.x), cta = blockIdx.x;
+  const uint32_t ctas = min(total, gridDim.x), cta = blockIdx.x;
   if (cta >= ctas) return;
   const uint32_t q = total / ctas, r = total - q * ctas;
   const uint32_t start = cta * q + min(cta, r);
@@ -965,14 +970,13 @@ Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, b
 template <int D, int R>
 int launch_decode(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, const Parts& parts,
                   int* status, cudaStream_t stream, int* launches) {
-  constexpr size_t smem = kWarps * kStages * (Ring<D>::kStageBytes + 16) + 2 * 8 * R * (D + 4) * sizeof(float);
+  constexpr size_t smem = kWarps * ring_stages<R>() * (Ring<D>::kStageBytes + 16) + 2 * 8 * R * (D + 4) * sizeof(float);
   if (kv_allow_smem<kv_decode_kernel<D, R>>(smem) != cudaSuccess) return MOE_ERR_CUDA;
   // no more CTAs than the longest call of these sizes gives steps to
   const long long tiles = (static_cast<long long>(a.max_q) * (a.Hq / d.Hkv) + 8 * R - 1) / (8 * R);
   const double steps = static_cast<double>(s.B) * d.Hkv * tiles * ((static_cast<long long>(s.max_len) + kSpan - 1) / kSpan + 1);
   if (steps > INT_MAX) return MOE_ERR_UNSUPPORTED;
-  const double most = steps / kLeast + 1;
-  const int ctas = most < kSMs * ctas_per_sm<R>() ? static_cast<int>(most) : kSMs * ctas_per_sm<R>();
+  const int ctas = steps < kSMs * ctas_per_sm<R>() ? static_cast<int>(steps) : kSMs * ctas_per_sm<R>();
   if (launch_chained(kv_decode_kernel<D, R>, dim3(ctas), dim3(kWarps * 32), smem, stream, d, pool, s, a, parts,
                      status) != cudaSuccess)
     return MOE_ERR_CUDA;

@@ -50,8 +50,10 @@ __device__ __forceinline__ float quotient(float x, float s, float inv, bool exac
 
 // Bound: the bf16 rows read once and their codes written once (3 bytes a
 // value); a decode step's single rows are launch latency.  The rows stay in
-// registers between the maximum and the rounding (up to 16 vectors a thread:
-// a whole page of 128 rows of 128).
+// registers between the maximum and the rounding: kVecs vectors a thread, as
+// many as a page has (4 to 16), so that small pages leave room for more CTAs
+// and their loads.
+template <int kVecs>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvPool pool, KvSeqs s,
                                                                    const __nv_bfloat16* __restrict__ kn,
                                                                    const __nv_bfloat16* __restrict__ vn,
@@ -62,13 +64,15 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
   const long long item = blockIdx.x;
   const int h = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
-  // the sequence whose numbers hold this item
-  int lo = 0, hi = s.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_item(cu, mid, d.page) <= item) lo = mid; else hi = mid - 1;
+  // the sequence whose numbers hold this item: each round of loads leaves one in 32
+  int b = 0;
+  for (int left = s.B; left > 1;) {
+    const int step = (left + 31) / 32, i = (threadIdx.x & 31) * step;
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, i < left && first_item(cu, b + min(i, left - 1), d.page) <= item);
+    const int k = below ? 31 - __clz(below) : 0;
+    b += k * step;
+    left = min(step, left - k * step);
   }
-  const int b = lo;
   int first, n, len;
   if (!kv_sequence(s, cu, T, b, d.page, status, &first, &n, &len)) return;
   const int start = len - n;
@@ -90,17 +94,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
   uint8_t* codes = (is_v ? pool.v : pool.k) + kv_row(page_id, d.Hkv, h, d.page, 0, d.D);
   float* scale = (is_v ? pool.v_scale : pool.k_scale) + static_cast<size_t>(page_id) * d.Hkv + h;
   const int per_row = d.D / 8, vecs = (s1 - s0) * per_row;
-  uint4 x[16];
+  uint4 x[kVecs];
   uint32_t m = 0;
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kVecs; ++i) {
     const int j = threadIdx.x + i * kAppendThreads;
     if (j >= vecs) break;
     x[i] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(j / per_row) * kv_stride + j % per_row * 8);
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kVecs; ++i) {
     if (threadIdx.x + i * kAppendThreads >= vecs) break;
     uint32_t a = absmax_bits(x[i]);
     if (a >= 0x7F80u) {
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
   const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0;
   const float inv = __fdiv_rn(1.f, now);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kVecs; ++i) {
     const int j = threadIdx.x + i * kAppendThreads;
     if (j >= vecs) break;
     const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -152,29 +156,6 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xFFFFFFFFu;
   const uint32_t u = __float_as_uint(w + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// Exclusive sum over the block of two counts packed in 16 bits each per warp
-// (a block counts at most 1024), and their totals.
-__device__ __forceinline__ void block_scan2(bool a, bool b, int* before_a, int* before_b, int* all_a, int* all_b,
-                                            int* shared) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t ba = __ballot_sync(0xFFFFFFFFu, a), bb = __ballot_sync(0xFFFFFFFFu, b);
-  const uint32_t below = (1u << lane) - 1;
-  if (lane == 0) {
-    shared[warp] = __popc(ba);
-    shared[32 + warp] = __popc(bb);
-  }
-  __syncthreads();
-  int ca = shared[lane], cb = shared[32 + lane];
-  const int all0 = __reduce_add_sync(0xFFFFFFFFu, ca), all1 = __reduce_add_sync(0xFFFFFFFFu, cb);
-  const int w0 = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? ca : 0);
-  const int w1 = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? cb : 0);
-  *before_a = w0 + __popc(ba & below);
-  *before_b = w1 + __popc(bb & below);
-  *all_a = all0;
-  *all_b = all1;
-  __syncthreads();
 }
 
 // Which tokens of (sequence b, head h) stay: all of a sequence within the
@@ -222,6 +203,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvS
       const int width = widths[pass], shift = 32 - bits_done - width, bins = 1 << width;
       for (int i = tid; i < bins; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int t = m0 + tid; t < m1; t += kSelectThreads) {
         const uint32_t key = weight_key(w[t]);
         if (bits_done == 0 || key >> (32 - bits_done) == prefix) atomicAdd(&hist[key >> shift & (bins - 1)], 1);
@@ -255,26 +237,50 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvS
       __syncthreads();
     }
   }
-  // `prefix` is the smallest key kept, `want` how many of the equal ones
-  int done = 0, equal = 0;
+  // `prefix` is the smallest key kept, `want` how many of the equal ones.  Each
+  // warp has a run of tokens of its own: it counts those that stay for sure and
+  // the equal ones; the sums over the warps before then say where its own go.
   const bool any = e.budget - e.sink - e.recent > 0;
-  for (int t0 = 0; t0 < len; t0 += kSelectThreads) {
-    const int t = t0 + tid;
-    const float x = t < len ? w[t] : 0.f;
-    const uint32_t key = weight_key(x);
+  const int lane = tid & 31, warp = tid >> 5, run = (len + kSelectThreads - 1) / kSelectThreads * 32;
+  const int r0 = min(warp * run, len), r1 = min(r0 + run, len);
+  const auto sort_of = [&](int t, float x, bool* equal) {   // stays for sure; equal: perhaps
     const bool ends = t < m0 || t >= m1;
-    const bool eq = t < len && !ends && any && key == prefix;
-    int at, eq_at, n, n_eq;
-    block_scan2(eq, false, &eq_at, &at, &n_eq, &n, scan);
-    const bool stay = t < len && (ends || (any && (key > prefix || (eq && equal + eq_at < want))));
-    int unused, none;
-    block_scan2(stay, false, &at, &unused, &n, &none, scan);
-    if (stay) {
-      kept[done + at] = t;
-      wout[done + at] = x;
+    const uint32_t key = weight_key(x);
+    *equal = t < r1 && !ends && any && key == prefix;
+    return t < r1 && (ends || (any && key > prefix));
+  };
+  int sure = 0, equal = 0;
+#pragma unroll 4
+  for (int t = r0 + lane; t < r0 + run && t - lane < r1; t += 32) {
+    bool eq;
+    const bool stays = sort_of(t, t < r1 ? w[t] : 0.f, &eq);
+    sure += __popc(__ballot_sync(0xFFFFFFFFu, stays));
+    equal += __popc(__ballot_sync(0xFFFFFFFFu, eq));
+  }
+  __syncthreads();   // (scan was read)
+  if (lane == 0) {
+    scan[warp] = sure;
+    scan[32 + warp] = equal;
+  }
+  __syncthreads();
+  const int sure_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scan[lane] : 0);
+  int equal_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? scan[32 + lane] : 0);
+  int at = sure_before + min(equal_before, want);
+#pragma unroll 4
+  for (int t = r0 + lane; t < r0 + run && t - lane < r1; t += 32) {
+    bool eq;
+    const float x = t < r1 ? w[t] : 0.f;
+    bool stays = sort_of(t, x, &eq);
+    const uint32_t eqs = __ballot_sync(0xFFFFFFFFu, eq), below = (1u << lane) - 1;
+    stays |= eq && equal_before + __popc(eqs & below) < want;
+    const uint32_t all = __ballot_sync(0xFFFFFFFFu, stays);
+    if (stays) {
+      const int to = at + __popc(all & below);
+      kept[to] = t;
+      wout[to] = x;
     }
-    done += n;
-    equal += n_eq;
+    at += __popc(all);
+    equal_before += __popc(eqs);
   }
 }
 
@@ -322,20 +328,31 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvP
     }
   }
   __syncthreads();
-  const int per_row = d.D / 16;
+  const int per_row = d.D / 16, chunks = n * per_row;
+  const float big[2] = {__uint_as_float(top[0]), __uint_as_float(top[1])};
+  const size_t to = kv_row(to_id, d.Hkv, h, d.page, 0, d.D);
+  if (tid < 2) (tid ? dst.v_scale : dst.k_scale)[static_cast<size_t>(to_id) * d.Hkv + h] = big[tid];
+  // four chunks of K and of V a thread are on their way at once
+  for (int j0 = tid; j0 < chunks; j0 += 4 * kGatherThreads) {
+    uint4 c[2][4];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const uint8_t* in = kv ? src.v : src.k;
-    uint8_t* out = (kv ? dst.v : dst.k) + kv_row(to_id, d.Hkv, h, d.page, 0, d.D);
-    const float big = __uint_as_float(top[kv]);
-    if (tid == 0) (kv ? dst.v_scale : dst.k_scale)[static_cast<size_t>(to_id) * d.Hkv + h] = big;
-#pragma unroll 8
-    for (int j = tid; j < n * per_row; j += kGatherThreads) {
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + i * kGatherThreads, r = j / per_row;
+      const bool in = j < chunks && from[min(r, n - 1)] != ~static_cast<size_t>(0);
+      const size_t at = in ? from[r] + j % per_row * 16 : 0;
+      c[0][i] = in ? __ldg(reinterpret_cast<const uint4*>(src.k + at)) : make_uint4(0, 0, 0, 0);
+      c[1][i] = in ? __ldg(reinterpret_cast<const uint4*>(src.v + at)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + i * kGatherThreads;
+      if (j >= chunks) break;
       const int r = j / per_row;
-      uint4 c = make_uint4(0, 0, 0, 0);
-      if (from[r] != ~static_cast<size_t>(0)) c = *reinterpret_cast<const uint4*>(in + from[r] + j % per_row * 16);
-      if (scale[kv][r] != big) c = e4m3x16_scaled(c, __fdiv_rn(scale[kv][r], big));
-      *reinterpret_cast<uint4*>(out + static_cast<size_t>(j) * 16) = c;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (scale[kv][r] != big[kv]) c[kv][i] = e4m3x16_scaled(c[kv][i], __fdiv_rn(scale[kv][r], big[kv]));
+        *reinterpret_cast<uint4*>((kv ? dst.v : dst.k) + to + static_cast<size_t>(j) * 16) = c[kv][i];
+      }
     }
   }
 }
@@ -346,9 +363,10 @@ int kv_append_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const
                      long long kv_stride, const int32_t* cu_new, int T_new, int* status, cudaStream_t stream,
                      int* launches) {
   const dim3 grid(static_cast<unsigned>(T_new / d.page + 2ll * s.B), 2u * d.Hkv);
-  if (launch_chained(kv_append_kernel, grid, dim3(kAppendThreads), 0, stream, d, pool, s,
-                     static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), kv_stride, cu_new,
-                     T_new, status) != cudaSuccess)
+  const int vecs = d.page * d.D / 8 / kAppendThreads;   // of a page, per thread: 1 to 16
+  const auto kernel = vecs <= 4 ? kv_append_kernel<4> : vecs <= 8 ? kv_append_kernel<8> : kv_append_kernel<16>;
+  if (launch_chained(kernel, grid, dim3(kAppendThreads), 0, stream, d, pool, s, static_cast<const __nv_bfloat16*>(k),
+                     static_cast<const __nv_bfloat16*>(v), kv_stride, cu_new, T_new, status) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++*launches;
   return MOE_OK;
