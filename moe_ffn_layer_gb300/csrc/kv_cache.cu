@@ -8,6 +8,8 @@
 // Evict: one CTA per (sequence, head) finds the tokens to keep by their
 // accumulated attention weight; then one CTA per destination (page, head)
 // gathers the kept rows.
+#include <limits.h>
+
 #include "kv_cache.cuh"
 
 namespace moe {
@@ -61,9 +63,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
                                                                    int T, int* status) {
   chain_wait();
   ChainReleaseAtExit release;
-  const long long item = blockIdx.x;
-  const int h = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
+  // heads, K and V of a page lie side by side: its tokens' rows are read whole
+  const int parts = 2 * d.Hkv, part = blockIdx.x % parts, h = part >> 1;
+  const long long item = blockIdx.x / parts;
+  const bool is_v = part & 1;
   // the sequence whose numbers hold this item: each round of loads leaves one in 32
   int b = 0;
   for (int left = s.B; left > 1;) {
@@ -163,8 +166,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // budget - sink - recent heaviest, the lower index first among equal ones.
 // Radix selection of the threshold key (11, 11 and 10 bits), then one pass in
 // index order writes the kept indices, so the result does not depend on
-// scheduling.
+// scheduling.  The weights are read five times; where the longest sequence's fit
+// (kStaged), the first pass leaves them in shared memory.
+constexpr int kMostStaged = 24576;   // 96 KB: two CTAs on an SM
+template <bool kStaged>
 __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvSeqs s, KvEvict e, int* status) {
+  extern __shared__ float staged[];
   chain_wait();
   ChainReleaseAtExit release;
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
@@ -198,6 +205,12 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvS
   uint32_t prefix = 0;
   int bits_done = 0;
   const int widths[3] = {11, 11, 10};
+  if (kStaged) {
+#pragma unroll 8
+    for (int t = tid; t < len; t += kSelectThreads) staged[t] = w[t];
+    __syncthreads();
+    w = staged;
+  }
   if (want > 0) {
     for (int pass = 0; pass < 3; ++pass) {
       const int width = widths[pass], shift = 32 - bits_done - width, bins = 1 << width;
@@ -362,10 +375,12 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvP
 int kv_append_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const void* k, const void* v,
                      long long kv_stride, const int32_t* cu_new, int T_new, int* status, cudaStream_t stream,
                      int* launches) {
-  const dim3 grid(static_cast<unsigned>(T_new / d.page + 2ll * s.B), 2u * d.Hkv);
+  const long long grid = (T_new / d.page + 2ll * s.B) * 2 * d.Hkv;
+  if (grid > INT_MAX) return MOE_ERR_UNSUPPORTED;
   const int vecs = d.page * d.D / 8 / kAppendThreads;   // of a page, per thread: 1 to 16
   const auto kernel = vecs <= 4 ? kv_append_kernel<4> : vecs <= 8 ? kv_append_kernel<8> : kv_append_kernel<16>;
-  if (launch_chained(kernel, grid, dim3(kAppendThreads), 0, stream, d, pool, s, static_cast<const __nv_bfloat16*>(k),
+  if (launch_chained(kernel, dim3(static_cast<unsigned>(grid)), dim3(kAppendThreads), 0, stream, d, pool, s,
+                     static_cast<const __nv_bfloat16*>(k),
                      static_cast<const __nv_bfloat16*>(v), kv_stride, cu_new, T_new, status) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++*launches;
@@ -374,8 +389,11 @@ int kv_append_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const
 
 int kv_evict_launch(const KvDims& d, const KvPool& src, const KvSeqs& s, const KvPool& dst, const KvEvict& e,
                     int* status, cudaStream_t stream, int* launches) {
-  if (launch_chained(kv_select_kernel, dim3(d.Hkv, s.B), dim3(kSelectThreads), 0, stream, d, s, e, status) !=
-      cudaSuccess)
+  const bool staged = s.max_len <= kMostStaged;
+  const size_t smem = staged ? s.max_len * sizeof(float) : 0;
+  if (staged && kv_allow_smem<kv_select_kernel<true>>(kMostStaged * sizeof(float)) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_chained(staged ? kv_select_kernel<true> : kv_select_kernel<false>, dim3(d.Hkv, s.B), dim3(kSelectThreads),
+                     smem, stream, d, s, e, status) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++*launches;
   const int most = s.max_len < e.budget ? s.max_len : e.budget;

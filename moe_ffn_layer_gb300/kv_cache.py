@@ -8,9 +8,27 @@ sequence is the caller's: ``page_table`` int32 [B, width] and ``seq_lens`` int32
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import binding as B
+
+# The calls are a few microseconds of kernels at decode sizes, and the host has
+# to keep ahead of them: streams are taken by handle, and the C entry points are
+# called with pointers at once.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current(device_index: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device_index)
+    return torch.cuda.current_stream(device_index).cuda_stream
+
+
+def _call(name: str, rc: int) -> None:
+    if rc != 0:
+        raise B.MoEError(name, rc)
 
 
 class KVCache8:
@@ -42,6 +60,9 @@ class KVCache8:
         self.num_pages, self.kv_heads, self.page, self.head_dim = k.shape
         self.dims = B.moe_kv_dims(self.kv_heads, self.head_dim, self.page)
         self.pool = B.moe_kv_pool(*(B.ptr(t) for t in (k, v, k_scale, v_scale)), self.num_pages)
+        self._dims, self._pool = ctypes.byref(self.dims), ctypes.byref(self.pool)
+        self._shape = tuple(k.shape[1:])
+        self._need = (None, 0)   # the last call's sizes and the workspace bytes they need
         self._ws = {}   # by stream: calls of different streams may overlap
 
     def _want_table(self, page_table, seq_lens, cu, cu_name):
@@ -73,17 +94,18 @@ class KVCache8:
             raise ValueError(f"k and v rows lie {stride} and {v.stride(0)} elements apart")
         n, width = self._want_table(page_table, seq_lens, cu_new, "cu_new")
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, min(width * self.page, 1 << 30))
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        B.moe_kv_append(self.dims, self.pool, seqs, k, v, stride, cu_new, T, stream)
+        _call("moe_kv_append", B.lib().moe_kv_append(
+            self._dims, self._pool, ctypes.byref(seqs), k.data_ptr(), v.data_ptr(), stride, cu_new.data_ptr(), T,
+            _current(self._dev) if stream is None else B.handle(stream)))
 
-    def workspace(self, need: int, stream) -> torch.Tensor:
-        """The stream's workspace, of at least `need` bytes, zero-filled when
-        allocated (the library keeps its counters zero from call to call)."""
-        key = B.handle(stream)
+    def workspace(self, need: int, stream=None) -> torch.Tensor:
+        """The stream's workspace (default: the current stream's), of at least
+        `need` bytes, zero-filled when allocated (the library keeps its counters
+        zero from call to call)."""
+        key = _current(self._dev) if stream is None else B.handle(stream)
         ws = self._ws.get(key)
         if ws is None or ws.numel() < need:
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):
                 ws = self._ws[key] = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
         return ws
 
@@ -103,13 +125,12 @@ class KVCache8:
             _want("q", q, torch.bfloat16, 3, self.device, shape, rows=True)
         n, width = self._want_table(page_table, seq_lens, cu_q, "cu_q")
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, max_len)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-            if out is None:
+        if out is None:
+            if stream is None:
                 out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        elif out is None:
-            with torch.cuda.stream(stream):
-                out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            else:
+                with torch.cuda.stream(stream):
+                    out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         if not _is(out, torch.bfloat16, dev, shape):
             _want("out", out, torch.bfloat16, 3, self.device, shape)
         if lse is not None and not _is(lse, torch.float32, dev, (T, Hq)):
@@ -119,10 +140,15 @@ class KVCache8:
             w_stride = weights.shape[-1]
             if not _is(weights, torch.float32, dev, (n, self.kv_heads, w_stride)):
                 _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
-        need = B.moe_kv_attention_workspace_bytes(self.dims, Hq, n, T, max_q, max_len, weights is not None)
-        ws = self.workspace(need, stream)
-        B.moe_kv_attention(self.dims, self.pool, seqs, q, q.stride(0) if T > 1 else Hq * D, Hq, cu_q, T, max_q,
-                           D ** -0.5 if scale is None else scale, out, lse, weights, w_stride, ws, ws.numel(), stream)
+        sizes = (Hq, n, T, max_q, max_len, weights is not None)
+        if self._need[0] != sizes:
+            self._need = (sizes, B.moe_kv_attention_workspace_bytes(self.dims, *sizes))
+        ws = self.workspace(self._need[1], stream)
+        _call("moe_kv_attention", B.lib().moe_kv_attention(
+            self._dims, self._pool, ctypes.byref(seqs), q.data_ptr(), q.stride(0) if T > 1 else Hq * D, Hq,
+            cu_q.data_ptr(), T, max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), None if weights is None else weights.data_ptr(), w_stride,
+            ws.data_ptr(), ws.numel(), _current(dev) if stream is None else B.handle(stream)))
         return out
 
     def evict(self, weights: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int, budget: int,
@@ -134,8 +160,8 @@ class KVCache8:
         Returns (lengths int32 [B], the kept weights fp32 [B, Hkv, budget], the
         kept positions int32 [B, Hkv, budget])."""
         dst = self if dst is None else dst
-        if dst.k.shape[1:] != self.k.shape[1:]:
-            raise ValueError(f"dst holds pages of {tuple(dst.k.shape[1:])}, not {tuple(self.k.shape[1:])}")
+        if dst._shape != self._shape:
+            raise ValueError(f"dst holds pages of {dst._shape}, not {self._shape}")
         n, width = self._want_table(page_table, seq_lens, None, "")
         w_stride, dst_width = weights.shape[-1], dst_table.shape[-1]
         if not (_is(weights, torch.float32, self._dev, (n, self.kv_heads, w_stride)) and
@@ -143,14 +169,15 @@ class KVCache8:
             _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
             _want("dst_table", dst_table, torch.int32, 2, self.device, (n, dst_width))
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
             made = self._evict_outputs(n, budget)
         else:
             with torch.cuda.stream(stream):
                 made = self._evict_outputs(n, budget)
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, max_len)
-        B.moe_kv_evict(self.dims, self.pool, seqs, weights, w_stride, budget, sink, recent, dst.pool, dst_table,
-                       dst_width, *made, stream)
+        _call("moe_kv_evict", B.lib().moe_kv_evict(
+            self._dims, self._pool, ctypes.byref(seqs), weights.data_ptr(), w_stride, budget, sink, recent, dst._pool,
+            dst_table.data_ptr(), dst_width, made[0].data_ptr(), made[1].data_ptr(), made[2].data_ptr(),
+            _current(self._dev) if stream is None else B.handle(stream)))
         return made
 
     def _evict_outputs(self, n, budget):
