@@ -22,8 +22,8 @@ constexpr int kAppendThreads = 128;
 // run of n > 0 tokens touches at most floor((n - 1) / page) + 2 pages, and the
 // next sequence's first number lies at least floor(n / page) + 2 further, so
 // the numbers never meet and need no prefix sum.
-__device__ __forceinline__ long long first_item(const int32_t* cu, int b, int page) {
-  return cu[b] / page + 2ll * b;
+__device__ __forceinline__ long long first_item(const int32_t* cu, int b, int shift) {
+  return (cu[b] >> shift) + 2ll * b;
 }
 
 __device__ __forceinline__ uint32_t absmax_bits(const uint4& v) {
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
   int b = 0;
   for (int left = s.B; left > 1;) {
     const int step = (left + 31) / 32, i = (threadIdx.x & 31) * step;
-    const uint32_t below = __ballot_sync(0xFFFFFFFFu, i < left && first_item(cu, b + min(i, left - 1), d.page) <= item);
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, i < left && first_item(cu, b + min(i, left - 1), d.shift) <= item);
     const int k = below ? 31 - __clz(below) : 0;
     b += k * step;
     left = min(step, left - k * step);
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
     set_status(status, MOE_ERR_DEVICE_CHECK);
     return;
   }
-  const long long p = start / d.page + (item - first_item(cu, b, d.page));   // page of the sequence
-  if (n == 0 || item < first_item(cu, b, d.page) || p * d.page >= len) return;
+  const long long p = (start >> d.shift) + (item - first_item(cu, b, d.shift));   // page of the sequence
+  if (n == 0 || item < first_item(cu, b, d.shift) || p * d.page >= len) return;
   const int page_id = s.table[static_cast<size_t>(b) * s.width + p];
   if (page_id < 0 || page_id >= pool.num_pages) {
     set_status(status, MOE_ERR_DEVICE_CHECK);
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
                              static_cast<long long>(h) * d.D;
   uint8_t* codes = (is_v ? pool.v : pool.k) + kv_row(page_id, d.Hkv, h, d.page, 0, d.D);
   float* scale = (is_v ? pool.v_scale : pool.k_scale) + static_cast<size_t>(page_id) * d.Hkv + h;
-  const int per_row = d.D / 8, vecs = (s1 - s0) * per_row;
+  const int row_shift = d.D == 128 ? 4 : 3, vecs = (s1 - s0) << row_shift;   // vectors of a row: 16 or 8
   uint4 x[kVecs];
   uint32_t m = 0;
   bool odd = false;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
   for (int i = 0; i < kVecs; ++i) {
     const int j = threadIdx.x + i * kAppendThreads;
     if (j >= vecs) break;
-    x[i] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(j / per_row) * kv_stride + j % per_row * 8);
+    x[i] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(j >> row_shift) * kv_stride + (j & ((1 << row_shift) - 1)) * 8);
   }
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
@@ -136,17 +136,29 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
   }
   const bool exact = (__float_as_uint(now) & 0x7FFFFFu) == 0;
   const float inv = __fdiv_rn(1.f, now);
+  uint8_t* to = codes + static_cast<size_t>(s0) * d.D;
+  if (exact && !odd) {   // a power of two and finite values: one multiplication each
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int j = threadIdx.x + i * kAppendThreads;
-    if (j >= vecs) break;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    for (int i = 0; i < kVecs; ++i) {
+      const int j = threadIdx.x + i * kAppendThreads;
+      if (j >= vecs) break;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = e4m3x2_of(bf16_lo(w[e]) * inv, bf16_hi(w[e]) * inv);
+      *reinterpret_cast<uint2*>(to + j * 8) = make_uint2(prmt(c[0], c[1], 0x5410u), prmt(c[2], c[3], 0x5410u));
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int j = threadIdx.x; j < vecs; j += kAppendThreads) {   // (read again: seldom taken)
+    const uint4 v = *reinterpret_cast<const uint4*>(src + static_cast<long long>(j >> row_shift) * kv_stride + (j & ((1 << row_shift) - 1)) * 8);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t c[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       c[e] = e4m3x2_of(quotient(bf16_lo(w[e]), now, inv, exact), quotient(bf16_hi(w[e]), now, inv, exact));
-    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(s0) * d.D + j * 8) =
-        make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    *reinterpret_cast<uint2*>(to + j * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
   }
 }
 
@@ -324,14 +336,14 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvP
   __syncthreads();
   if (tid < n) {
     const int t = kept[tid];
-    const int q = t / d.page;
+    const int q = t >> d.shift;
     int id = q < s.width ? s.table[static_cast<size_t>(b) * s.width + q] : -1;
     if (id < 0 || id >= src.num_pages) {
       set_status(status, MOE_ERR_DEVICE_CHECK);
       from[tid] = ~static_cast<size_t>(0);
       scale[0][tid] = scale[1][tid] = 0.f;
     } else {
-      from[tid] = kv_row(id, d.Hkv, h, d.page, t % d.page, d.D);
+      from[tid] = kv_row(id, d.Hkv, h, d.page, t & (d.page - 1), d.D);
       const float a = src.k_scale[static_cast<size_t>(id) * d.Hkv + h], c = src.v_scale[static_cast<size_t>(id) * d.Hkv + h];
       scale[0][tid] = a;
       scale[1][tid] = c;
@@ -341,7 +353,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvP
     }
   }
   __syncthreads();
-  const int per_row = d.D / 16, chunks = n * per_row;
+  const int row_shift = d.D == 128 ? 3 : 2, chunks = n << row_shift;   // 16-byte chunks of a row: 8 or 4
   const float big[2] = {__uint_as_float(top[0]), __uint_as_float(top[1])};
   const size_t to = kv_row(to_id, d.Hkv, h, d.page, 0, d.D);
   if (tid < 2) (tid ? dst.v_scale : dst.k_scale)[static_cast<size_t>(to_id) * d.Hkv + h] = big[tid];
@@ -350,9 +362,9 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvP
     uint4 c[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int j = j0 + i * kGatherThreads, r = j / per_row;
+      const int j = j0 + i * kGatherThreads, r = j >> row_shift;
       const bool in = j < chunks && from[min(r, n - 1)] != ~static_cast<size_t>(0);
-      const size_t at = in ? from[r] + j % per_row * 16 : 0;
+      const size_t at = in ? from[r] + (j & ((1 << row_shift) - 1)) * 16 : 0;
       c[0][i] = in ? __ldg(reinterpret_cast<const uint4*>(src.k + at)) : make_uint4(0, 0, 0, 0);
       c[1][i] = in ? __ldg(reinterpret_cast<const uint4*>(src.v + at)) : make_uint4(0, 0, 0, 0);
     }
@@ -360,7 +372,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvP
     for (int i = 0; i < 4; ++i) {
       const int j = j0 + i * kGatherThreads;
       if (j >= chunks) break;
-      const int r = j / per_row;
+      const int r = j >> row_shift;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         if (scale[kv][r] != big[kv]) c[kv][i] = e4m3x16_scaled(c[kv][i], __fdiv_rn(scale[kv][r], big[kv]));
