@@ -189,8 +189,8 @@ __device__ __forceinline__ void scores(float (&s)[kTok / 8][2 * R], const QueryT
 struct Tile {
   int first, n, len, rows, row0, seen;   // seen: tokens that the tile's last real row sees
   __device__ __forceinline__ bool find(const KvSeqs& s, const KvAttention& at, int b, int g, int mt, int tile_rows,
-                                       int page, int* status) {
-    if (!kv_sequence(s, at.cu_q, at.T_q, b, page, status, &first, &n, &len)) return false;
+                                       const KvDims& d, int* status) {
+    if (!kv_sequence(s, at.cu_q, at.T_q, b, d, status, &first, &n, &len)) return false;
     if (n > at.max_q) {
       set_status(status, MOE_ERR_DEVICE_CHECK);
       return false;
@@ -431,7 +431,7 @@ struct Cursor {
                                            int* status) {
     tiles = 0;
     steps = 1;
-    if (!kv_sequence(s, at.cu_q, at.T_q, b, d.page, status, &first, &n, &len)) return;
+    if (!kv_sequence(s, at.cu_q, at.T_q, b, d, status, &first, &n, &len)) return;
     if (n > at.max_q) {
       set_status(status, MOE_ERR_DEVICE_CHECK);
       return;
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kGainThreads) kv_gain_kept_kernel(KvDims d, Kv
   ChainReleaseAtExit release;
   const int h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv, t = blockIdx.x * kGainThreads + threadIdx.x;
   Tile tile;
-  if (!tile.find(s, at, b, g, 0, 8, d.page, status) || t >= tile.len) return;
+  if (!tile.find(s, at, b, g, 0, 8, d, status) || t >= tile.len) return;
   float sum = 0.f;
 #pragma unroll 8
   for (int r = 0; r < tile.rows; ++r) {
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(128) kv_lay_kernel(KvDims d, KvSeqs s, KvAtten
   const int lane = threadIdx.x & 31, mt = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
   const int g = at.Hq / d.Hkv;
   Tile tile;
-  if (!tile.find(s, at, b, g, mt, 16, d.page, status)) return;
+  if (!tile.find(s, at, b, g, mt, 16, d, status)) return;
   QueryTile<D, 2> q;
   q.load(at, tile.first, h, g, tile.row0, tile.rows, lane);
   const size_t slot = laid_tile(at, tile.first, b, g, mt, d.Hkv, h);
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPo
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv;
   const int first = blockIdx.x * 8 * kTok, t0 = first + (warp & 7) * kTok, part = warp >> 3, n = lane >> 2, c = lane & 3;
   Tile tile;
-  if (!tile.find(s, at, b, g, 0, 16, d.page, status) || first >= tile.len) return;
+  if (!tile.find(s, at, b, g, 0, 16, d, status) || first >= tile.len) return;
   uint2 k[kTok / 8][D / 16];
   float ks[2];
 #pragma unroll

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvP
     left = min(step, left - k * step);
   }
   int first, n, len;
-  if (!kv_sequence(s, cu, T, b, d.page, status, &first, &n, &len)) return;
+  if (!kv_sequence(s, cu, T, b, d, status, &first, &n, &len)) return;
   const int start = len - n;
   if (start < 0) {
     set_status(status, MOE_ERR_DEVICE_CHECK);

@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   const int heads = a.s.B * a.d.Hkv, unit = blockIdx.x % heads, pair = pairs - 1 - blockIdx.x / heads;
   const int b = unit / a.d.Hkv, h = unit % a.d.Hkv, g = a.at.Hq / a.d.Hkv;
   int first, n, len;
-  if (!kv_sequence(a.s, a.at.cu_q, a.at.T_q, b, a.d.page, a.status, &first, &n, &len)) return;
+  if (!kv_sequence(a.s, a.at.cu_q, a.at.T_q, b, a.d, a.status, &first, &n, &len)) return;
   if (n > a.at.max_q) {
     set_status(a.status, MOE_ERR_DEVICE_CHECK);
     return;
