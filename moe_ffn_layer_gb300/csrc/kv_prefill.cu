@@ -30,11 +30,12 @@ namespace {
 constexpr int kTile = 128;              // rows of a tile
 constexpr int kStep = 64;               // tokens of a step
 constexpr int kRing = 4;                // steps of K and of V in shared memory
-// Warps: 0 and 1 issue the tiles' MMAs (one warp for both spent half its time
-// between waits and MMAs: PLACEHOLDER2), 2 to 5 and 6 to 9 are
-// the tiles' softmax, 10 to 13 convert.
-constexpr int kThreads = 448;
-constexpr int kSoftmaxWarp = 2, kConvertWarp = 10;
+// Warps: 0 and 1 issue the tiles' score MMAs, 2 and 3 their output MMAs (a warp's
+// next barrier test waits behind the MMAs that it has issued, so the two kinds
+// have warps of their own: PLACEHOLDER2), 4 to 7 and 8 to 11
+// are the tiles' softmax, 12 to 15 convert.
+constexpr int kThreads = 512;
+constexpr int kSoftmaxWarp = 4, kConvertWarp = 12;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kLarge = 0x4400u;    // 2^9 in bf16: where a weight passes it, the maximum that they are taken against follows
 
@@ -68,8 +69,8 @@ struct Smem {
 
 constexpr int kGroupRing = 8;   // steps whose groups are kept: a step's are read until the step four later is converted
 struct Ctrl {
-  uint64_t q_full[2], k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing], s_full[2][2], p_full[2][2], o_full[2],
-      scale_full[kGroupRing], drain[2];
+  uint64_t q_full[2], k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing], s_full[2][2], p_full[2][2], o_full[2][2],
+      scale_full[kGroupRing], drain[4];
   uint32_t tmem;
   int abort;
   Group group[kGroupRing][kStep / 16];
@@ -276,71 +277,76 @@ __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32
   }
 }
 
-// A tile's MMA warp: per step the scores of the step after, then the output of
-// this one.  The whole warp runs it, so that descriptors and addresses stay in
-// uniform registers; one elected lane issues.
+// The MMA warps of a tile.  The whole warp runs each, so that descriptors and
+// addresses stay in uniform registers; one elected lane issues.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const PrefillArgs& a, Ctrl* ctrl) {
+  if (__all_sync(0xFFFFFFFFu, test(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, wait_on(bar, parity, &ctrl->abort, a.status, a.wait_ns)) != 0;
+}
+
+// Scores: S of step j takes the place of step j - 2's weights, once their product is done.
 template <int D>
-__device__ __forceinline__ void multiply(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int t,
-                                         int steps) {
+__device__ __forceinline__ void multiply_scores(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int t,
+                                                int steps) {
   using S = Smem<D>;
-  constexpr uint32_t kScores = idesc_f32(kTile, kStep, false, false), kOut = idesc_f32(kTile, D, true, true);
-  volatile int* abort = &ctrl->abort;
+  constexpr uint32_t kScores = idesc_f32(kTile, kStep, false, false);
   const bool one = elect_one();
-  const auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (__all_sync(0xFFFFFFFFu, test(bar, parity))) return true;
-    return __all_sync(0xFFFFFFFFu, wait_on(bar, parity, abort, a.status, a.wait_ns)) != 0;
-  };
-  const uint32_t k_full = smem_u32(ctrl->k_full), v_full = smem_u32(ctrl->v_full), o_full = smem_u32(&ctrl->o_full[t]),
-                 p_full = smem_u32(ctrl->p_full[t]);
-  if (!wait(smem_u32(&ctrl->q_full[t]), 0)) return;
-  const uint64_t dq = smem_desc_k128(smem + S::q + t * S::kQ), k0 = smem_desc_k128(smem + S::k),
-                 v0 = smem_desc_n128(smem + S::v, S::kBlock);
-  const uint32_t s_t = tmem + t * 2 * kStep, o = tmem + 4 * kStep + t * D;
-  // j: the step whose output is due; the scores are those of step j + 1
-  int stage = 0, stage_next = 0;          // of step j and of step j + 1
-  uint32_t phase = 0, phase_next = 0;     // and their rings' parities
-  for (int j = -1; j < steps; ++j) {
-    const uint32_t buf = j & 1;   // of step j
-    if (j + 1 < steps) {
-      if (!wait(k_full + 8 * stage_next, phase_next)) return;
-      // these scores take the place of step j - 1's weights: once their product is done
-      if (j > 0 && !wait(o_full, buf ^ 1u)) return;
-      tc_fence_after();
-      const uint32_t to = s_t + (buf ^ 1u) * kStep;
-      const uint64_t dk = k0 + stage_next * (S::kOperand >> 4);
-      if (one) {
+  const uint32_t k_full = smem_u32(ctrl->k_full), o_full = smem_u32(ctrl->o_full[t]);
+  if (!warp_wait(smem_u32(&ctrl->q_full[t]), 0, a, ctrl)) return;
+  const uint64_t dq = smem_desc_k128(smem + S::q + t * S::kQ), k0 = smem_desc_k128(smem + S::k);
+  uint32_t stage = 0, phase = 0;
+  for (int j = 0; j < steps; ++j) {
+    const uint32_t buf = j & 1, to = tmem + t * 2 * kStep + buf * kStep;
+    if (!warp_wait(k_full + 8 * stage, phase, a, ctrl)) return;
+    if (j > 1 && !warp_wait(o_full + 8 * buf, ((j >> 1) - 1) & 1, a, ctrl)) return;
+    tc_fence_after();
+    const uint64_t dk = k0 + stage * (S::kOperand >> 4);
+    if (one) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          umma_bf16(to, dq + (i >> 2) * (S::kQBlock >> 4) + 2 * (i & 3), dk + (i >> 2) * (S::kBlock >> 4) + 2 * (i & 3),
-                    kScores, i > 0);
-        umma_commit(&ctrl->s_full[t][buf ^ 1u]);
-        umma_commit(&ctrl->k_empty[stage_next]);
-      }
-      __syncwarp();
+      for (int i = 0; i < D / 16; ++i)
+        umma_bf16(to, dq + (i >> 2) * (S::kQBlock >> 4) + 2 * (i & 3), dk + (i >> 2) * (S::kBlock >> 4) + 2 * (i & 3),
+                  kScores, i > 0);
+      umma_commit(&ctrl->s_full[t][buf]);
+      umma_commit(&ctrl->k_empty[stage]);
     }
-    if (j >= 0) {
-      if (!wait(v_full + 8 * stage, phase)) return;
-      if (!wait(p_full + 8 * buf, (j >> 1) & 1)) return;
-      tc_fence_after();
-      const uint32_t p = s_t + buf * kStep;
-      const uint64_t dv = v0 + stage * (S::kOperand >> 4);
-      if (one) {
+    __syncwarp();
+    if (++stage == kRing) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void multiply_out(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int t,
+                                             int steps) {
+  using S = Smem<D>;
+  constexpr uint32_t kOut = idesc_f32(kTile, D, true, true);
+  const bool one = elect_one();
+  const uint32_t v_full = smem_u32(ctrl->v_full), p_full = smem_u32(ctrl->p_full[t]);
+  const uint64_t v0 = smem_desc_n128(smem + S::v, S::kBlock);
+  const uint32_t o = tmem + 4 * kStep + t * D;
+  uint32_t stage = 0, phase = 0;
+  for (int j = 0; j < steps; ++j) {
+    const uint32_t buf = j & 1, p = tmem + t * 2 * kStep + buf * kStep;
+    if (!warp_wait(v_full + 8 * stage, phase, a, ctrl)) return;
+    if (!warp_wait(p_full + 8 * buf, (j >> 1) & 1, a, ctrl)) return;
+    tc_fence_after();
+    const uint64_t dv = v0 + stage * (S::kOperand >> 4);
+    if (one) {
 #pragma unroll
-        for (int i = 0; i < kStep / 16; ++i) {
-          const uint32_t hi = p + 32 * (i >> 1) + 8 * (i & 1);
-          umma_bf16_ts(o, hi, dv + i * (2048 >> 4), kOut, j + i > 0);
-          umma_bf16_ts(o, hi + 16, dv + i * (2048 >> 4), kOut, 1);
-        }
-        umma_commit(&ctrl->o_full[t]);
-        umma_commit(&ctrl->v_empty[stage]);
+      for (int i = 0; i < kStep / 16; ++i) {
+        const uint32_t hi = p + 32 * (i >> 1) + 8 * (i & 1);
+        umma_bf16_ts(o, hi, dv + i * (2048 >> 4), kOut, j + i > 0);
+        umma_bf16_ts(o, hi + 16, dv + i * (2048 >> 4), kOut, 1);
       }
-      __syncwarp();
+      umma_commit(&ctrl->o_full[t][buf]);
+      umma_commit(&ctrl->v_empty[stage]);
     }
-    stage = stage_next;
-    phase = phase_next;
-    if (++stage_next == kRing) {
-      stage_next = 0;
-      phase_next ^= 1u;
+    __syncwarp();
+    if (++stage == kRing) {
+      stage = 0;
+      phase ^= 1u;
     }
   }
 }
@@ -464,10 +470,10 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
         const float r = to == m ? 1.f : ex2(m - to);   // (0 for the first)
         m = to;
         l *= r;
-        // O so far: once the last step's product is in it (the one before was, ahead
-        // of these scores; the next one waits for these weights)
+        // O so far: once the last step's product is in it (products of a tile end in
+        // order, and the next one waits for these weights)
         if (j > 0) {
-          failed |= !__all_sync(0xFFFFFFFFu, wait_for(&ctrl->o_full[t], (j - 1) & 1, abort, a.status, a.wait_ns));
+          failed |= !__all_sync(0xFFFFFFFFu, wait_for(&ctrl->o_full[t][(j - 1) & 1], ((j - 1) >> 1) & 1, abort, a.status, a.wait_ns));
           __syncwarp();   // (the tensor-memory accesses below want the whole warp)
           tc_fence_after();
         }
@@ -509,10 +515,9 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
     mbar_arrive(&ctrl->p_full[t][j & 1]);
     if (__any_sync(0xFFFFFFFFu, failed)) return;
   }
-  // The last scores followed the third last product, so up to two are still to
-  // come: a wait for each, or its parity would be taken for the one before.
-  for (int j = max(steps - 2, 0); j < steps; ++j)
-    if (!__all_sync(0xFFFFFFFFu, wait_for(&ctrl->o_full[t], j & 1, abort, a.status, a.wait_ns))) return;
+  if (steps > 0 && !__all_sync(0xFFFFFFFFu, wait_for(&ctrl->o_full[t][(steps - 1) & 1], ((steps - 1) >> 1) & 1, abort,
+                                                    a.status, a.wait_ns)))
+    return;
   __syncwarp();
   tc_fence_after();
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -569,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctrl->q_full[i], kTile);
-      mbar_init(&ctrl->o_full[i], 1);
       for (int k = 0; k < 2; ++k) {
+        mbar_init(&ctrl->o_full[i][k], 1);
         mbar_init(&ctrl->s_full[i][k], 1);
         mbar_init(&ctrl->p_full[i][k], kTile);
       }
@@ -582,8 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
       mbar_init(&ctrl->v_empty[i], tiles);
     }
     for (int i = 0; i < kGroupRing; ++i) mbar_init(&ctrl->scale_full[i], 2);
-    mbar_init(&ctrl->drain[0], 1);
-    mbar_init(&ctrl->drain[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&ctrl->drain[i], 1);
     ctrl->abort = 0;
     fence_barrier_init();
   }
@@ -597,8 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ctrl->tmem, 0);
   if (warp < kSoftmaxWarp) {
-    if (warp < tiles && steps > 0) {
-      multiply<D>(a, ctrl, smem, tmem, warp, steps);
+    if ((warp & 1) < tiles && steps > 0) {
+      if (warp < 2)
+        multiply_scores<D>(a, ctrl, smem, tmem, warp, steps);
+      else
+        multiply_out<D>(a, ctrl, smem, tmem, warp & 1, steps);
       // whatever was issued is done before the tensor memory goes
       __syncwarp();
       if (elect_one()) {
