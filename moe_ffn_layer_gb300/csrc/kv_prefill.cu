@@ -37,7 +37,7 @@ constexpr int kRing = 4;                // steps of K and of V in shared memory
 constexpr int kThreads = 512;
 constexpr int kSoftmaxWarp = 4, kConvertWarp = 12;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kLarge = 0x4400u;    // 2^9 in bf16: where a weight passes it, the maximum that they are taken against follows
+constexpr float kLarge = 512.f;         // where 32 weights pass it together, the maximum that they are taken against follows
 
 struct PrefillArgs {
   KvDims d;
@@ -401,7 +401,7 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
   const uint32_t o = tmem + lanes + 4 * kStep + t * D;
   // m: what the exponents are taken against, a whole number, so that a change
   // of it scales l, O and the weights already written exactly.  It follows the
-  // scores only where a weight comes out above kLarge.
+  // scores only where weights come out above kLarge.
   float m = -INFINITY, l = 0.f;
   for (int j = 0; j < steps; ++j) {
     const uint32_t groups = smem_u32(ctrl->group[j % kGroupRing]);
@@ -439,7 +439,6 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
       float sum[4];
       bool raised = false;
       for (;;) {
-        uint32_t most = 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float add = lv[e] - (m == -INFINITY ? 0.f : m);
@@ -452,15 +451,14 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
             part[1] += w1;
             const uint32_t u0 = __float_as_uint(w0), u1 = __float_as_uint(w1);
             hi[8 * e + i] = prmt(u0, u1, 0x7632u);
-            most = __vmaxu2(most, hi[8 * e + i]);
             lo[8 * e + i] = pack_bf16x2(w0 - __uint_as_float(u0 & 0xFFFF0000u), w1 - __uint_as_float(u1 & 0xFFFF0000u));
           }
           sum[2 * e] = part[0];
           sum[2 * e + 1] = part[1];
         }
-        // Too large a weight (or a first one, or a NaN, which stays): m is raised
-        // to the scores' maximum and everything so far scaled down to it.
-        const bool large = max(most & 0xFFFFu, most >> 16) > kLarge || m == -INFINITY;
+        // Too large a sum (or a first one, or a NaN, which stays): m is raised to
+        // the scores' maximum and everything so far scaled down to it.
+        const bool large = !(sum[0] + sum[1] + sum[2] + sum[3] <= kLarge) || m == -INFINITY;
         if (raised || !__any_sync(0xFFFFFFFFu, large)) break;
         raised = true;
         float top = -INFINITY;
