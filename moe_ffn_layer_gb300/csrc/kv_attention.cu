@@ -521,13 +521,13 @@ __device__ __forceinline__ void join_parts(const Parts& parts, int c0, int n, co
   }
 }
 
-// CTAs an SM holds, and stages of a warp's ring.  Tiles of 8 rows: two CTAs of
-// three stages (64 sequences of 513 to 16384 tokens: 206 us) against three of
-// two (227 us: 168 registers, spilled); tiles of 16 rows have 8 KB more to meet
-// in, so two of two stages (57 us on 4 queries each of 16 sequences, 83 us at
-// one CTA of three).
-template <int R>
-constexpr int ctas_per_sm() { return 2; }
+// CTAs an SM holds, and stages of a warp's ring.  Tiles of 8 rows, D = 128: two
+// CTAs of three stages (64 sequences of 513 to 16384 tokens: 206 us) against
+// three of two (227 us: 168 registers, spilled); D = 64 fits three of three.
+// Tiles of 16 rows have 8 KB more to meet in, so two of two stages (57 us on 4
+// queries each of 16 sequences, 83 us at one CTA of three).
+template <int D, int R>
+constexpr int ctas_per_sm() { return D == 64 && R == 1 ? 3 : 2; }
 template <int R>
 constexpr int ring_stages() { return R == 1 ? 3 : 2; }
 
@@ -536,7 +536,7 @@ constexpr int ring_stages() { return R == 1 ? 3 : 2; }
 // asynchronous copies and a running softmax of its own; the ring runs on
 // across units.  At a unit's end the warps' states meet in shared memory.
 template <int D, int R>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kernel(KvDims d, KvPool pool, KvSeqs s,
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<D, R>()) kv_decode_kernel(KvDims d, KvPool pool, KvSeqs s,
                                                                                  KvAttention at, Parts parts,
                                                                                  int* status) {
   constexpr int kRows = 8 * R, kPitch = D + 4, kStages = ring_stages<R>();
@@ -736,25 +736,37 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm<R>()) kv_decode_kerne
 // weights[b][h][t] += sum over the rows of (b, h) of exp(s_t - lse), the rows
 // in order, so that the sums do not depend on scheduling.
 
-// From the scores that the decode kernel kept (8-row tiles): a thread per token.
+// From the scores that the decode kernel kept (8-row tiles): four tokens a thread.
 // Writing and reading 4 bytes per row and token beats reading K again (D bytes)
 // up to these 8 rows.  Bound: HBM and L2, 4 rows + 8 bytes per token.
-constexpr int kGainThreads = 256;
+constexpr int kGainThreads = 128, kGainTokens = 4 * kGainThreads;
 __global__ void __launch_bounds__(kGainThreads) kv_gain_kept_kernel(KvDims d, KvSeqs s, KvAttention at,
                                                                     const float* __restrict__ scores, int pitch,
                                                                     int* status) {
   chain_wait();
   ChainReleaseAtExit release;
-  const int h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv, t = blockIdx.x * kGainThreads + threadIdx.x;
+  const int h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv, t = (blockIdx.x * kGainThreads + threadIdx.x) * 4;
   Tile tile;
   if (!tile.find(s, at, b, g, 0, 8, d, status) || t >= tile.len) return;
-  float sum = 0.f;
-#pragma unroll 8
-  for (int r = 0; r < tile.rows; ++r) {
-    const size_t at_row = static_cast<size_t>(tile.first + r / g) * at.Hq + h * g + r % g;
-    if (t < tile.sees(r, g)) sum += exp2_approx(scores[at_row * pitch + t] - at.lse[at_row] * kLog2e);
+  float sum[4] = {};
+  for (int i = 0; i < tile.n; ++i) {
+    const int sees = tile.len - tile.n + i + 1;   // tokens that query i sees
+    if (t >= sees) continue;
+    const size_t row0 = static_cast<size_t>(tile.first + i) * at.Hq + h * g;
+#pragma unroll 4
+    for (int r = 0; r < g; ++r) {
+      const float lse = at.lse[row0 + r] * kLog2e;
+      const float4 v = *reinterpret_cast<const float4*>(scores + (row0 + r) * pitch + t);   // (pitch holds whole steps)
+      sum[0] += exp2_approx(v.x - lse);
+      sum[1] += t + 1 < sees ? exp2_approx(v.y - lse) : 0.f;
+      sum[2] += t + 2 < sees ? exp2_approx(v.z - lse) : 0.f;
+      sum[3] += t + 3 < sees ? exp2_approx(v.w - lse) : 0.f;
+    }
   }
-  at.weights[(static_cast<long long>(b) * d.Hkv + h) * at.w_stride + t] += sum;
+  float* w = at.weights + (static_cast<long long>(b) * d.Hkv + h) * at.w_stride + t;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (t + e < tile.len) w[e] += sum[e];
 }
 
 // More rows: the scores again, from K and the queries as MMA operands, which a
@@ -940,9 +952,11 @@ struct Layout {
 };
 bool few_rows(int Hq, int Hkv, int max_q) { return static_cast<long long>(max_q) * (Hq / Hkv) <= 8; }
 Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights) {
-  constexpr size_t slots = static_cast<size_t>(kSMs) * ctas_per_sm<2>() * 2 * 16;
-  static_assert(slots >= static_cast<size_t>(kSMs) * ctas_per_sm<1>() * 2 * 8, "slots of 8-row tiles");
-  static_assert(kSMs * ctas_per_sm<1>() <= kMostCtas && kSMs * ctas_per_sm<2>() <= kMostCtas, "tickets");
+  constexpr size_t slots = static_cast<size_t>(kSMs) * ctas_per_sm<128, 2>() * 2 * 16;
+  static_assert(ctas_per_sm<64, 2>() <= ctas_per_sm<128, 2>() && ctas_per_sm<128, 1>() <= ctas_per_sm<64, 1>() &&
+                    slots >= static_cast<size_t>(kSMs) * ctas_per_sm<64, 1>() * 2 * 8,
+                "slots of either tile size");
+  static_assert(kSMs * ctas_per_sm<64, 1>() <= kMostCtas && kSMs * ctas_per_sm<128, 2>() <= kMostCtas, "tickets");
   Layout w{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -976,7 +990,7 @@ int launch_decode(const KvDims& d, const KvPool& pool, const KvSeqs& s, const Kv
   const long long tiles = (static_cast<long long>(a.max_q) * (a.Hq / d.Hkv) + 8 * R - 1) / (8 * R);
   const double steps = static_cast<double>(s.B) * d.Hkv * tiles * ((static_cast<long long>(s.max_len) + kSpan - 1) / kSpan + 1);
   if (steps > INT_MAX) return MOE_ERR_UNSUPPORTED;
-  const int ctas = steps < kSMs * ctas_per_sm<R>() ? static_cast<int>(steps) : kSMs * ctas_per_sm<R>();
+  const int ctas = steps < kSMs * ctas_per_sm<D, R>() ? static_cast<int>(steps) : kSMs * ctas_per_sm<D, R>();
   if (launch_chained(kv_decode_kernel<D, R>, dim3(ctas), dim3(kWarps * 32), smem, stream, d, pool, s, a, parts,
                      status) != cudaSuccess)
     return MOE_ERR_CUDA;
@@ -1000,7 +1014,7 @@ int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, 
                                     : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
   if (rc || !a.weights || s.max_len == 0) return rc;
   if (few) {
-    const unsigned blocks = (static_cast<unsigned>(s.max_len) + kGainThreads - 1) / kGainThreads;
+    const unsigned blocks = (static_cast<unsigned>(s.max_len) + kGainTokens - 1) / kGainTokens;
     if (launch_chained(kv_gain_kept_kernel, dim3(blocks, d.Hkv, s.B), dim3(kGainThreads), 0, stream, d, s, a,
                        parts.scores, parts.pitch, status) != cudaSuccess)
       return MOE_ERR_CUDA;
