@@ -23,6 +23,8 @@
 // never turns a masked product into a NaN.
 #include <limits.h>
 
+#include <algorithm>
+
 #include "kv_cache.cuh"
 
 namespace moe {
@@ -813,21 +815,35 @@ __global__ void __launch_bounds__(128) kv_lay_kernel(KvDims d, KvSeqs s, KvAtten
 // tokens' codes in registers and runs over the row tiles that see them, the
 // even ones in warps 0 to 7, the odd ones in 8 to 15; the two sums are added at
 // the end.  The tiles come through a ring in shared memory that all warps read.
-constexpr int kGainWarps = 16, kGainStages = 4;
+// With few such CTAs `parts` of them share the row tiles of the same tokens (a
+// prompt of 4096 with weights: 650 us without, 477 with), and the last to end adds
+// their sums in order.  Measured: half the f16 MMA rate of mma.sync (a quarter of
+// tcgen05's), 0.22 ms for 247 M pairs of row and token.
+// A stage is four pairs: with a barrier at each pair the warps' MMAs and
+// exponentials fell into step.
+constexpr int kGainWarps = 16, kGainStages = 3, kGainPairs = 4, kGainBlock = 256, kGainTickets = 4096;
+struct GainParts {
+  int parts;       // 1: no tickets
+  int* ticket;     // [B][Hkv][blocks], zero between calls
+  float* sums;     // [B][Hkv][blocks][parts][kGainBlock]
+};
 template <int D>
 struct GainStage {
-  uint4 a[2][D / 16][32];   // a pair of tiles
-  float2 info[2][16];
+  uint4 a[kGainPairs][2][D / 16][32];
+  float2 info[kGainPairs][2][16];
 };
 template <int D>
 __global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPool pool, KvSeqs s, KvAttention at,
-                                                                  Laid laid, int* status) {
+                                                                  Laid laid, GainParts gp, int* status) {
+  __shared__ int last;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float half[8][32];
-  __shared__ __align__(16) GainStage<D> ring[kGainStages];
+  GainStage<D>* ring = reinterpret_cast<GainStage<D>*>(smem);
   chain_wait();
   ChainReleaseAtExit release;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, b = blockIdx.z, g = at.Hq / d.Hkv;
-  const int first = blockIdx.x * 8 * kTok, t0 = first + (warp & 7) * kTok, part = warp >> 3, n = lane >> 2, c = lane & 3;
+  const int block = blockIdx.x / gp.parts, row_part = blockIdx.x % gp.parts;
+  const int first = block * kGainBlock, t0 = first + (warp & 7) * kTok, part = warp >> 3, n = lane >> 2, c = lane & 3;
   Tile tile;
   if (!tile.find(s, at, b, g, 0, 16, d, status) || first >= tile.len) return;
   uint2 k[kTok / 8][D / 16];
@@ -856,70 +872,70 @@ __global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPo
   // Row r sees token t where r >= (t - (len - n)) g.  Pairs of row tiles, from
   // the first that sees the CTA's first token.
   const int base = tile.len - tile.n, tiles = (tile.rows + 15) / 16, pairs = (tiles + 1) / 2;
-  const int pair0 = first > base ? (first - base) * g / 32 : 0;
+  const int pair0 = (first > base ? (first - base) * g / 32 : 0) + row_part * kGainPairs;
+  const int stride = gp.parts * kGainPairs;   // the parts take stages in turn
   const int need_any = t0 < tile.len ? max(t0 - base, 0) * g : INT_MAX;
   const int need_all = max(min(t0 + kTok, tile.len) - 1 - base, 0) * g;
   const bool gone = no_page(ks[0]) || no_page(ks[1]);
-  const auto fetch = [&](int pair) {
-    if (pair < pairs) {
-      GainStage<D>& st = ring[pair % kGainStages];
-#pragma unroll
-      for (int i = threadIdx.x; i < 2 * (D / 16) * 32; i += kGainWarps * 32) {
-        const int mt = 2 * pair + i / (D / 16 * 32), j = i % (D / 16 * 32);
-        if (mt < tiles)
-          cp_async16(smem_u32(&st.a[0][0][0] + i), laid.a + laid_tile(at, tile.first, b, g, mt, d.Hkv, h) * (D / 16 * 32) + j);
-      }
-      if (threadIdx.x < 16) {
-        const int mt = 2 * pair + threadIdx.x / 8;
-        if (mt < tiles)
-          cp_async16(smem_u32(&st.info[0][0] + 2 * threadIdx.x),
-                     laid.info + laid_tile(at, tile.first, b, g, mt, d.Hkv, h) * 16 + threadIdx.x % 8 * 2);
-      }
-    }
+  const auto fetch = [&](int pair, int stage) {   // kGainPairs pairs from `pair` on
+    GainStage<D>& st = ring[stage];
+    constexpr int kVecs = D / 16 * 32;   // of a tile
+    const int left = min(2 * kGainPairs, tiles - 2 * pair);
+    for (int i = threadIdx.x; i < left * kVecs; i += kGainWarps * 32)
+      cp_async16(smem_u32(&st.a[0][0][0][0] + i),
+                 laid.a + laid_tile(at, tile.first, b, g, 2 * pair + i / kVecs, d.Hkv, h) * kVecs + i % kVecs);
+    for (int i = threadIdx.x; i < left * 8; i += kGainWarps * 32)
+      cp_async16(smem_u32(&st.info[0][0][0] + 2 * i),
+                 laid.info + laid_tile(at, tile.first, b, g, 2 * pair + i / 8, d.Hkv, h) * 16 + i % 8 * 2);
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kGainStages - 1; ++i) fetch(pair0 + i);
+  for (int i = 0; i < kGainStages - 1; ++i) fetch(pair0 + i * stride, i);
   float sum[kTok / 8][2] = {};
-  for (int pair = pair0; pair < pairs; ++pair) {
+  int stage = 0;
+  for (int pair = pair0; pair < pairs; pair += stride) {
     cp_async_wait<kGainStages - 2>();
-    __syncthreads();   // everybody's copies of this pair are there; everybody is done with the one before
-    fetch(pair + kGainStages - 1);
-    const int mt = 2 * pair + part;
-    if (mt >= tiles || mt * 16 + 15 < need_any) continue;
-    const GainStage<D>& st = ring[pair % kGainStages];
-    float x[kTok / 8][4] = {};
+    __syncthreads();   // everybody's copies of this stage are there; everybody is done with the one before
+    fetch(pair + (kGainStages - 1) * stride, stage == 0 ? kGainStages - 1 : stage - 1);
+    const GainStage<D>& st = ring[stage];
+    stage = stage + 1 == kGainStages ? 0 : stage + 1;
+#pragma unroll 1
+    for (int q = 0; q < kGainPairs; ++q) {
+      const int mt = 2 * (pair + q) + part;
+      if (mt >= tiles || mt * 16 + 15 < need_any) continue;
+      float x[kTok / 8][4] = {};
 #pragma unroll
-    for (int f = 0; f < D / 16; ++f) {
-      uint32_t a[4];
-      *reinterpret_cast<uint4*>(a) = lds_u4(smem_u32(&st.a[part][f][lane]));
+      for (int f = 0; f < D / 16; ++f) {
+        uint32_t a[4];
+        *reinterpret_cast<uint4*>(a) = lds_u4(smem_u32(&st.a[q][part][f][lane]));
 #pragma unroll
-      for (int nt = 0; nt < kTok / 8; ++nt) mma_f16(x[nt], a, k[nt][f].x, k[nt][f].y);
-    }
-    const float2 r0 = st.info[part][n], r1 = st.info[part][8 + n];
-#pragma unroll
-    for (int nt = 0; nt < kTok / 8; ++nt) {
-      const float f0 = ks[nt >> 1] * r0.x, f1 = ks[nt >> 1] * r1.x;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x[nt][e] = exp2_approx(fmaf(x[nt][e], f0, -r0.y));
-        x[nt][2 + e] = exp2_approx(fmaf(x[nt][2 + e], f1, -r1.y));
+        for (int nt = 0; nt < kTok / 8; ++nt) mma_f16(x[nt], a, k[nt][f].x, k[nt][f].y);
       }
-    }
-    if (mt * 16 < need_all || gone) {
+      const float2 r0 = st.info[q][part][n], r1 = st.info[q][part][8 + n];
+#pragma unroll
+      for (int nt = 0; nt < kTok / 8; ++nt) {
+        const float f0 = ks[nt >> 1] * r0.x, f1 = ks[nt >> 1] * r1.x;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[nt][e] = exp2_approx(fmaf(x[nt][e], f0, -r0.y));
+          x[nt][2 + e] = exp2_approx(fmaf(x[nt][2 + e], f1, -r1.y));
+        }
+      }
+      if (mt * 16 < need_all || gone) {
+#pragma unroll
+        for (int nt = 0; nt < kTok / 8; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int need = (t0 + nt * 8 + 2 * c + e - base) * g;
+            if (mt * 16 + n < need || no_page(ks[nt >> 1])) x[nt][e] = 0.f;
+            if (mt * 16 + 8 + n < need || no_page(ks[nt >> 1])) x[nt][2 + e] = 0.f;
+          }
+      }
 #pragma unroll
       for (int nt = 0; nt < kTok / 8; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int need = (t0 + nt * 8 + 2 * c + e - base) * g;
-          if (mt * 16 + n < need || no_page(ks[nt >> 1])) x[nt][e] = 0.f;
-          if (mt * 16 + 8 + n < need || no_page(ks[nt >> 1])) x[nt][2 + e] = 0.f;
-        }
+        for (int e = 0; e < 2; ++e) sum[nt][e] += x[nt][e] + x[nt][2 + e];
     }
-#pragma unroll
-    for (int nt = 0; nt < kTok / 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) sum[nt][e] += x[nt][e] + x[nt][2 + e];
   }
   cp_async_wait<0>();
 #pragma unroll
@@ -931,23 +947,59 @@ __global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPo
       if (part == 1 && n == 0) half[warp & 7][nt * 8 + 2 * c + e] = sum[nt][e];
     }
   __syncthreads();
+  float* w = at.weights + (static_cast<long long>(b) * d.Hkv + h) * at.w_stride + first;
+  if (gp.parts == 1) {
+    if (part == 0 && n == 0) {
+#pragma unroll
+      for (int nt = 0; nt < kTok / 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = nt * 8 + 2 * c + e;
+          if (t0 + i < tile.len) w[t0 - first + i] += sum[nt][e] + half[warp][i];
+        }
+    }
+    return;
+  }
+  const size_t slot = (static_cast<size_t>(b) * d.Hkv + h) * (gridDim.x / gp.parts) + block;
+  float* sums = gp.sums + slot * gp.parts * kGainBlock;
   if (part == 0 && n == 0) {
-    float* w = at.weights + (static_cast<long long>(b) * d.Hkv + h) * at.w_stride;
 #pragma unroll
     for (int nt = 0; nt < kTok / 8; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = nt * 8 + 2 * c + e;
-        if (t0 + i < tile.len) w[t0 + i] += sum[nt][e] + half[warp][i];
+        sums[row_part * kGainBlock + t0 - first + i] = sum[nt][e] + half[warp][i];
       }
   }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(gp.ticket + slot, 1) == gp.parts - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
+  if (threadIdx.x == 0) gp.ticket[slot] = 0;
+  if (threadIdx.x < kGainBlock && first + static_cast<int>(threadIdx.x) < tile.len) {
+    float v = 0.f;
+    for (int p = 0; p < gp.parts; ++p) v += __ldcg(sums + p * kGainBlock + threadIdx.x);
+    w[threadIdx.x] += v;
+  }
+}
+
+// How many CTAs share a block of tokens: enough for four on every SM, each with two stages at least.
+int gain_parts(int B, int Hkv, int max_len, long long rows) {
+  const long long blocks = static_cast<long long>(B) * Hkv * ((static_cast<long long>(max_len) + kGainBlock - 1) / kGainBlock);
+  if (blocks > kGainTickets || blocks == 0) return 1;
+  const long long parts = std::min<long long>({8, (4 * kSMs + blocks - 1) / blocks, rows / (2 * kGainPairs * 32)});
+  return parts > 1 ? static_cast<int>(parts) : 1;
 }
 
 // Workspace: the tickets first, at the same place for every call, then the
 // parts, the log-sum-exps, and for the weights the kept scores or the laid out
 // queries.
 struct Layout {
-  size_t o, ml, lse, scores, laid, info, total;
+  size_t gain_ticket, o, ml, lse, scores, laid, info, gain, total;
   int pitch;
 };
 bool few_rows(int Hq, int Hkv, int max_q) { return static_cast<long long>(max_q) * (Hq / Hkv) <= 8; }
@@ -965,6 +1017,7 @@ Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, b
     return r;
   };
   take(kMostCtas * sizeof(int));
+  w.gain_ticket = take(kGainTickets * sizeof(int));
   const size_t rows = static_cast<size_t>(T_q) * Hq;
   w.o = take(slots * d.D * sizeof(float));
   w.ml = take(slots * sizeof(float2));
@@ -976,6 +1029,9 @@ Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, b
     const size_t tiles = laid_tiles(Hq, d.Hkv, B, T_q);
     w.laid = take(tiles * 32 * d.D);
     w.info = take(tiles * 16 * sizeof(float2));
+    const int parts = gain_parts(B, d.Hkv, max_len, static_cast<long long>(max_q) * (Hq / d.Hkv));
+    const size_t blocks = static_cast<size_t>(B) * d.Hkv * ((static_cast<size_t>(max_len) + kGainBlock - 1) / kGainBlock);
+    if (parts > 1) w.gain = take(blocks * parts * kGainBlock * sizeof(float));
   }
   w.total = at;
   return w;
@@ -1022,11 +1078,15 @@ int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, 
     return MOE_OK;
   }
   const Laid laid{reinterpret_cast<uint4*>(base + w.laid), reinterpret_cast<float2*>(base + w.info)};
-  const unsigned tiles = static_cast<unsigned>((rows + 15) / 16), blocks = (static_cast<unsigned>(s.max_len) + 255) / 256;
+  const unsigned tiles = static_cast<unsigned>((rows + 15) / 16);
+  const unsigned blocks = (static_cast<unsigned>(s.max_len) + kGainBlock - 1) / kGainBlock;
+  const GainParts gp{gain_parts(s.B, d.Hkv, s.max_len, rows), reinterpret_cast<int*>(base + w.gain_ticket),
+                     reinterpret_cast<float*>(base + w.gain)};
   if (launch_chained(kv_lay_kernel<D>, dim3((tiles + 3) / 4, d.Hkv, s.B), dim3(128), 0, stream, d, s, a, laid,
                      status) != cudaSuccess ||
-      launch_chained(kv_gain_kernel<D>, dim3(blocks, d.Hkv, s.B), dim3(kGainWarps * 32), 0, stream, d, pool, s, a, laid,
-                     status) != cudaSuccess)
+      kv_allow_smem<kv_gain_kernel<D>>(kGainStages * sizeof(GainStage<D>)) != cudaSuccess ||
+      launch_chained(kv_gain_kernel<D>, dim3(blocks * gp.parts, d.Hkv, s.B), dim3(kGainWarps * 32),
+                     kGainStages * sizeof(GainStage<D>), stream, d, pool, s, a, laid, gp, status) != cudaSuccess)
     return MOE_ERR_CUDA;
   *launches += 2;
   return MOE_OK;

@@ -6,15 +6,27 @@
 // that they see, 64 at a time:
 //  - four warps convert the tokens' codes into shared memory, K to f16 and V to
 //    bf16 (both exact), in the 128-byte swizzle of the MMA's operands;
-//  - one thread issues the MMAs: S = Q K^T (f16, accumulator in tensor memory),
-//    then O += P V (bf16, P from tensor memory, V with its head dimension
-//    contiguous);
+//  - two warps a tile issue the MMAs: S = Q K^T (f16, accumulator in tensor
+//    memory), and O += P V (bf16, P from tensor memory, V with its head
+//    dimension contiguous);
 //  - a warpgroup for each tile turns S into the weights P, a row per thread.
 //    P takes the tensor memory of S: the 32 columns of 32 tokens' scores become
 //    16 of their weights' high bf16 terms and 16 of the low ones (16 bits in
 //    all, at any size, as in the decode kernel), so PV is two MMAs per step.
 // A tile's S has two buffers, so that the scores of the next step are there when
 // a softmax ends, and neither it nor the MMAs wait for each other's last piece.
+//
+// Bound: instruction issue of the softmax and the converters, in step with the
+// MMAs.  One prompt of 8192 (32 heads of 128, 8 kv heads): 789 us, 0.70 PFLOP/s of
+// the definition's operations, where the two-term weights alone cost half as many
+// MMAs again; the tensor pipe is active 43% of the time, the issue slots 55%.
+// What got it there from 1097 us (all same prompt): MMA operands in uniform
+// registers and waits tested inline (the MMA warp's own instructions between two
+// waits were the longest chain), 64-token steps with two S buffers, the running
+// maximum followed only where weights grow (no pass over S for it).  Tried and
+// slower: steps of 128 tokens with S in one buffer (815 us: both tiles' softmaxes
+// run at once and the tensor cores wait), the same with the tiles taking turns
+// (838 us).
 //
 // A page's V scale is 2^e times a mantissa in [1, 2): 2^e goes into the V
 // operand (exact), the mantissa into the weights' exponent, and the row's sum
@@ -31,8 +43,7 @@ constexpr int kTile = 128;              // rows of a tile
 constexpr int kStep = 64;               // tokens of a step
 constexpr int kRing = 4;                // steps of K and of V in shared memory
 // Warps: 0 and 1 issue the tiles' score MMAs, 2 and 3 their output MMAs (a warp's
-// next barrier test waits behind the MMAs that it has issued, so the two kinds
-// have warps of their own: PLACEHOLDER2), 4 to 7 and 8 to 11
+// next barrier test waits behind the MMAs that it has issued), 4 to 7 and 8 to 11
 // are the tiles' softmax, 12 to 15 convert.
 constexpr int kThreads = 512;
 constexpr int kSoftmaxWarp = 4, kConvertWarp = 12;
