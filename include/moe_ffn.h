@@ -261,9 +261,9 @@ MOE_API int moe_forward_w8(const moe_dims* d, const moe_weights_w8* w, const voi
  * Pools hold pages of `page` tokens; each page holds, per kv head, the e4m3
  * codes of K and of V (row-major [page][D]) and one fp32 scale for each:
  *   K[t] = k_scale[id][h] * e4m3(k[id][h][t % page]),  id = page_table[b][t / page]
- * and V likewise.  Scales are finite and not negative; the codes 0x7f and 0xff
- * (NaN) are never stored by these calls and read as +-480 (as elsewhere in
- * this library).  Slots at or beyond a sequence's length may hold anything.
+ * and V likewise.  Scales are finite and not negative; the NaN codes 0x7f and
+ * 0xff are never stored by these calls and may not lie among a sequence's
+ * tokens.  Slots at or beyond a sequence's length may hold anything.
  * Supported: D 64 or 128; page 16, 32, 64 or 128. */
 typedef struct {
   int Hkv, D, page;
@@ -284,6 +284,7 @@ typedef struct {
  *             (entries beyond a sequence's length are not read)
  *  seq_lens   int32 [B] on the device (never read by the host)
  *  max_len    host upper bound on seq_lens
+ * Supported: B <= 65535, max_len <= 2^30.
  * A length outside [0, max_len] or beyond width * page, packed boundaries that
  * are not ascending or exceed the stated total, and page ids outside the pool
  * are device-checked: a sequence that fails is skipped, a page that fails is
