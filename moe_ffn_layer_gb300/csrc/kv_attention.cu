@@ -34,9 +34,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kTok = 32;          // tokens of a warp's step
 constexpr int kWarps = 4;
 constexpr int kSpan = kWarps * kTok;   // tokens of a CTA's step: one step of each warp
-constexpr int kDecodeRows = 64;        // query rows of a kv head up to which the decode kernel is taken
+constexpr int kDecodeRows = 64;        // query rows of a kv head up to which the decode kernel is taken (on_prefill)
 constexpr float kSlack = 8.f;
-constexpr int kSMs = 152;         // of a GB300: the plan of a call depends on its sizes alone
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -1003,10 +1002,26 @@ int gain_parts(int B, int Hkv, int max_len, long long rows) {
 // parts, the log-sum-exps, and for the weights the kept scores or the laid out
 // queries.
 struct Layout {
-  size_t gain_ticket, o, ml, lse, scores, laid, info, gain, total;
+  size_t gain_ticket, o, ml, lse, scores, laid, info, gain, part_o, part_ml, total;
   int pitch;
 };
+
+// Tiles of 8 rows where every sequence's rows fit one, else of 16: 4 rows over 16
+// sequences of 8192 (8 kv heads of 128) 57 us, 63 with tiles of 16.
 bool few_rows(int Hq, int Hkv, int max_q) { return static_cast<long long>(max_q) * (Hq / Hkv) <= 8; }
+
+// The tensor-memory kernel for more than kDecodeRows rows of a kv head.  Decode
+// against it, us, 8 kv heads of 128: 64 rows over one sequence of 32768 tokens 68
+// and 65, 128 rows 114 and 67; over four of 32768, 64 rows 185 and 244, 128 rows
+// 323 and 246; over 16 of 2048, 64 rows 64 and 65, 96 rows 86 and 65.  But where
+// no decode CTA would have more than one step, its launch is the shorter one: a
+// prompt of 128, 512 rows, 8.3 and 12.8; (one of 256, two steps and more: 21 and 16).
+bool on_prefill(const KvDims& d, int Hq, int B, int max_q, int max_len) {
+  const long long rows = static_cast<long long>(max_q) * (Hq / d.Hkv);
+  const double steps = static_cast<double>(B) * d.Hkv * ((rows + 15) / 16) * ((static_cast<long long>(max_len) + kSpan - 1) / kSpan);
+  return rows > kDecodeRows && steps > kSMs * ctas_per_sm<128, 2>();
+}
+
 Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights) {
   constexpr size_t slots = static_cast<size_t>(kSMs) * ctas_per_sm<128, 2>() * 2 * 16;
   static_assert(ctas_per_sm<64, 2>() <= ctas_per_sm<128, 2>() && ctas_per_sm<128, 1>() <= ctas_per_sm<64, 1>() &&
@@ -1026,6 +1041,11 @@ Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, b
   w.o = take(slots * d.D * sizeof(float));
   w.ml = take(slots * sizeof(float2));
   w.lse = take(rows * sizeof(float));
+  if (on_prefill(d, Hq, B, max_q, max_len)) {
+    const size_t part_rows = kv_prefill_part_rows(d, Hq, B, max_q, max_len);
+    w.part_o = take(part_rows * d.D * sizeof(float));
+    w.part_ml = take(part_rows * sizeof(float2));
+  }
   if (weights && few_rows(Hq, d.Hkv, max_q)) {
     w.pitch = static_cast<int>((static_cast<long long>(max_len) + kTok - 1) / kTok * kTok);
     w.scores = take(rows * w.pitch * sizeof(float));
@@ -1064,12 +1084,14 @@ int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, 
   const Layout w = layout(d, a.Hq, s.B, a.T_q, a.max_q, s.max_len, a.weights != nullptr);
   uint8_t* base = static_cast<uint8_t*>(ws);
   if (a.weights && !a.lse) a.lse = reinterpret_cast<float*>(base + w.lse);
-  const bool few = few_rows(a.Hq, d.Hkv, a.max_q);   // tiles of 8 rows where every sequence's rows fit one, else of 16
+  const bool few = few_rows(a.Hq, d.Hkv, a.max_q);
   const Parts parts{reinterpret_cast<int*>(base), reinterpret_cast<float*>(base + w.o),
                     reinterpret_cast<float2*>(base + w.ml),
                     a.weights && few ? reinterpret_cast<float*>(base + w.scores) : nullptr, w.pitch};
   const long long rows = static_cast<long long>(a.max_q) * (a.Hq / d.Hkv);
-  const int rc = rows > kDecodeRows ? kv_prefill_launch(d, pool, s, a, status, stream, launches)   // tcgen05
+  const int rc = on_prefill(d, a.Hq, s.B, a.max_q, s.max_len)
+                     ? kv_prefill_launch(d, pool, s, a, reinterpret_cast<float*>(base + w.part_o),
+                                         reinterpret_cast<float2*>(base + w.part_ml), status, stream, launches)
                  : few              ? launch_decode<D, 1>(d, pool, s, a, parts, status, stream, launches)
                                     : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
   if (rc || !a.weights || s.max_len == 0) return rc;

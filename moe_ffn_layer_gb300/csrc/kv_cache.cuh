@@ -9,6 +9,8 @@
 
 namespace moe {
 
+constexpr int kSMs = 152;   // of a GB300: the plan of a call depends on its sizes alone
+
 // Allows a kernel its dynamic shared memory, once per device and kernel.
 template <auto kKernel>
 inline cudaError_t kv_allow_smem(size_t bytes) {

@@ -28,11 +28,16 @@
 // run at once and the tensor cores wait), the same with the tiles taking turns
 // (838 us).
 //
+// Where there are fewer CTAs than half the SMs the key axis is cut in parts, and
+// kv_prefill_join_kernel adds what they leave in the workspace.
+//
 // A page's V scale is 2^e times a mantissa in [1, 2): 2^e goes into the V
 // operand (exact), the mantissa into the weights' exponent, and the row's sum
 // takes it out again, w / mantissa; for power-of-two scales it is 1.
 #include <limits.h>
 #include <stddef.h>
+
+#include <algorithm>
 
 #include "kv_cache.cuh"
 
@@ -57,7 +62,15 @@ struct PrefillArgs {
   KvAttention at;
   int* status;
   uint64_t wait_ns;
+  // The key axis cut in `parts`, at steps: a part's O (relative to its maximum),
+  // its maxima and sums, by [part][pair][sequence, head][row of the pair].
+  int pairs, parts;
+  float* part_o;     // rows of D
+  float2* part_ml;
 };
+
+// Steps of a part of a unit of `steps`: the same in the kernel and in the join.
+__device__ __forceinline__ int part_steps(int steps, int parts) { return (steps + parts - 1) / parts; }
 
 // What the softmax needs of a step's 16-token groups.
 struct alignas(16) Group {   // (one 16-byte access)
@@ -171,8 +184,8 @@ __device__ __forceinline__ bool v_is_zero(float vs) { return (__float_as_uint(vs
 
 // The converters' part: K and V of every step, each into a ring of its own.
 template <int D>
-__device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, int b, int h, int end,
-                                        int steps) {
+__device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, int b, int h, int from,
+                                        int end, int steps) {
   using S = Smem<D>;
   constexpr int kHalves = D / 64, kRows = kStep / 32;   // a thread has a chunk of each half of kRows rows
   const int tid = threadIdx.x - kConvertWarp * 32;
@@ -223,13 +236,13 @@ __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32
   uint4 kx[kRows * kHalves], vx[kRows * kHalves];
   float ks[kRows], vs[kRows], ks_next[kRows], vs_next[kRows];
   int id[kRows], id_next[kRows];
-  look(id, 0);
-  look(id_next, kStep);
-  check(id, 0);
-  load(kx, a.pool.k, id, 0);
+  look(id, from);
+  look(id_next, from + kStep);
+  check(id, from);
+  load(kx, a.pool.k, id, from);
   scales(ks, vs, id);
   for (int j = 0; j < steps; ++j) {
-    const int t0 = j * kStep, st = j % kRing;
+    const int t0 = from + j * kStep, st = j % kRing;
     const uint32_t parity = (j / kRing) & 1;
     load(vx, a.pool.v, id, t0);
     if (writes) {
@@ -365,7 +378,8 @@ __device__ __forceinline__ void multiply_out(const PrefillArgs& a, Ctrl* ctrl, u
 // A softmax warpgroup's part: a row per thread.
 template <int D>
 __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int t, int b,
-                                        int h, int g, int first, int n, int len, int row0, int steps) {
+                                        int h, int g, int first, int n, int len, int row0, int from,
+                                        int steps) {
   using S = Smem<D>;
   const KvAttention& at = a.at;
   volatile int* abort = &ctrl->abort;
@@ -422,7 +436,7 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
     if (!__all_sync(0xFFFFFFFFu, ok)) return;
     __syncwarp();
     tc_fence_after();
-    const int t0 = j * kStep;
+    const int t0 = from + j * kStep;
     bool failed = false;
     // 32 tokens (two groups): their scores s to weights, in place
     const auto weigh = [&](int c, uint32_t (&s)[32]) {
@@ -529,7 +543,11 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
     return;
   __syncwarp();
   tc_fence_after();
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const bool cut = a.parts > 1;
+  const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
+  // (in the grid's order)
+  const size_t slot = static_cast<size_t>(blockIdx.x) * 2 * kTile + t * kTile + in_tile;
+  float4* part = reinterpret_cast<float4*>(a.part_o + slot * D);
   uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D);
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) {
@@ -541,7 +559,12 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0;
     }
-    if (real) {
+    if (real && cut) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        part[8 * c + i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                      __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+    } else if (real) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t w[4];
@@ -553,11 +576,14 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
     }
     __syncwarp();
   }
-  if (real && at.lse) at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (real && cut)
+    a.part_ml[slot] = make_float2(m, l);
+  else if (real && at.lse)
+    at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, int pairs) {
+__global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a) {
   using S = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -566,7 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   chain_wait();
   ChainReleaseAtExit release;
   // the rows that see most first: the last CTAs to start are the shortest
-  const int heads = a.s.B * a.d.Hkv, unit = blockIdx.x % heads, pair = pairs - 1 - blockIdx.x / heads;
+  const int heads = a.s.B * a.d.Hkv, unit = blockIdx.x % heads;
+  const int pair = a.pairs - 1 - blockIdx.x / heads % a.pairs, part = blockIdx.x / heads / a.pairs;
   const int b = unit / a.d.Hkv, h = unit % a.d.Hkv, g = a.at.Hq / a.d.Hkv;
   int first, n, len;
   if (!kv_sequence(a.s, a.at.cu_q, a.at.T_q, b, a.d, a.status, &first, &n, &len)) return;
@@ -577,8 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   const int rows = n * g, row0 = pair * 2 * kTile;
   if (row0 >= rows) return;
   const int tiles = row0 + kTile < rows ? 2 : 1;
-  const int end = max(len - n + (min(row0 + 2 * kTile, rows) - 1) / g + 1, 0);   // what the last row sees
-  const int steps = (end + kStep - 1) / kStep;
+  const int seen = max(len - n + (min(row0 + 2 * kTile, rows) - 1) / g + 1, 0);   // by the last row
+  const int all = (seen + kStep - 1) / kStep, per = part_steps(all, a.parts);
+  if (part > 0 && part * per >= all) return;   // (the join does not ask for it)
+  const int from = part * per * kStep, steps = min(per, all - part * per), end = min(seen, from + steps * kStep);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -625,9 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
     }
   } else if (warp < kConvertWarp) {
     const int t = (warp - kSoftmaxWarp) / 4;
-    if (t < tiles) softmax<D>(a, ctrl, smem, tmem, t, b, h, g, first, n, len, row0, steps);
+    if (t < tiles) softmax<D>(a, ctrl, smem, tmem, t, b, h, g, first, n, len, row0, from, steps);
   } else {
-    convert<D>(a, ctrl, smem, b, h, end, steps);
+    convert<D>(a, ctrl, smem, b, h, from, end, steps);
   }
   tc_fence_before();
   __syncthreads();
@@ -637,25 +666,100 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a, 
   }
 }
 
+// The parts of a row, in order: a warp per row, D / 32 columns a lane.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_prefill_join_kernel(PrefillArgs a) {
+  constexpr int kPer = D / 32;
+  chain_wait();
+  ChainReleaseAtExit release;
+  const int heads = a.s.B * a.d.Hkv, unit = blockIdx.y, b = unit / a.d.Hkv, h = unit % a.d.Hkv, g = a.at.Hq / a.d.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x * kJoinWarps + warp;
+  int first, n, len;
+  if (!kv_sequence(a.s, a.at.cu_q, a.at.T_q, b, a.d, a.status, &first, &n, &len)) return;
+  if (n > a.at.max_q || row >= n * g) return;   // (the first is recorded by the parts)
+  const int pair = row / (2 * kTile), rows = n * g;
+  const int seen = max(len - n + (min((pair + 1) * 2 * kTile, rows) - 1) / g + 1, 0);
+  const int all = (seen + kStep - 1) / kStep, per = part_steps(all, a.parts);
+  const int used = max((all + max(per, 1) - 1) / max(per, 1), 1);
+  const auto slot = [&](int p) {
+    return ((static_cast<size_t>(p) * a.pairs + (a.pairs - 1 - pair)) * heads + unit) * 2 * kTile + row % (2 * kTile);
+  };
+  float m = -INFINITY;
+  for (int p = lane; p < used; p += 32) m = fmaxf(m, a.part_ml[slot(p)].x);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
+  float l = 0.f, acc[kPer] = {};
+#pragma unroll 4
+  for (int p = 0; p < used; ++p) {
+    const float2 ml = a.part_ml[slot(p)];
+    const float r = ml.x == m ? 1.f : ex2(ml.x - m);   // (a power of two: maxima are whole numbers)
+    const float* o = a.part_o + slot(p) * D + lane * kPer;
+    float v[kPer];
+    if constexpr (kPer == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(o);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(o);
+      v[0] = x.x, v[1] = x.y;
+    }
+    l = fmaf(ml.y, r, l);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(v[e], r, acc[e]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t at_row = static_cast<size_t>(first + row / g) * a.at.Hq + h * g + row % g;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.at.out) + at_row * D + lane * kPer);
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && a.at.lse) a.at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 template <int D>
 int launch(const PrefillArgs& a, cudaStream_t stream, int* launches) {
   if (kv_allow_smem<kv_prefill_kernel<D>>(Smem<D>::total) != cudaSuccess) return MOE_ERR_CUDA;
-  const long long rows = static_cast<long long>(a.at.max_q) * (a.at.Hq / a.d.Hkv);
-  const long long pairs = (rows + 2 * kTile - 1) / (2 * kTile);
-  const double ctas = static_cast<double>(pairs) * a.s.B * a.d.Hkv;
+  const double ctas = static_cast<double>(a.pairs) * a.s.B * a.d.Hkv * a.parts;
   if (ctas > INT_MAX) return MOE_ERR_UNSUPPORTED;
-  if (launch_chained(kv_prefill_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Smem<D>::total, stream, a,
-                     static_cast<int>(pairs)) != cudaSuccess)
+  if (launch_chained(kv_prefill_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Smem<D>::total, stream,
+                     a) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  ++*launches;
+  if (a.parts == 1) return MOE_OK;
+  const unsigned rows = static_cast<unsigned>(a.pairs) * 2 * kTile;
+  if (launch_chained(kv_prefill_join_kernel<D>, dim3(rows / kJoinWarps, a.s.B * a.d.Hkv), dim3(kJoinWarps * 32), 0,
+                     stream, a) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++*launches;
   return MOE_OK;
 }
 
+long long pairs_of(const KvDims& d, int Hq, int max_q) {
+  return (static_cast<long long>(max_q) * (Hq / d.Hkv) + 2 * kTile - 1) / (2 * kTile);
+}
+
+// Parts of the key axis: as many as give each SM a CTA, of eight steps at least.
+// 128 rows on 8 kv heads over one sequence of 32768 tokens: 931 us uncut, 67 in 19
+// parts; 512 rows 1028 and 136 (9 parts); four of 2048, 512 rows: 64 and 55 (2).
+int parts_of(const KvDims& d, int Hq, int B, int max_q, int max_len) {
+  const long long ctas = pairs_of(d, Hq, max_q) * B * d.Hkv;
+  if (ctas == 0) return 1;
+  const long long parts = std::min<long long>(kSMs / ctas, max_len / (8 * kStep));
+  return parts > 1 ? static_cast<int>(parts) : 1;
+}
+
 }  // namespace
 
-int kv_prefill_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& at, int* status,
-                      cudaStream_t stream, int* launches) {
-  const PrefillArgs a{d, pool, s, at, status, wait_limit_ns()};
+size_t kv_prefill_part_rows(const KvDims& d, int Hq, int B, int max_q, int max_len) {
+  const int parts = parts_of(d, Hq, B, max_q, max_len);
+  return parts == 1 ? 0 : static_cast<size_t>(pairs_of(d, Hq, max_q)) * B * d.Hkv * parts * 2 * kTile;
+}
+
+int kv_prefill_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& at, float* part_o,
+                      float2* part_ml, int* status, cudaStream_t stream, int* launches) {
+  const long long pairs = pairs_of(d, at.Hq, at.max_q);
+  if (pairs > INT_MAX) return MOE_ERR_UNSUPPORTED;
+  const PrefillArgs a{d, pool, s, at, status, wait_limit_ns(), static_cast<int>(pairs),
+                      parts_of(d, at.Hq, s.B, at.max_q, s.max_len), part_o, part_ml};
   return d.D == 128 ? launch<128>(a, stream, launches) : launch<64>(a, stream, launches);
 }
 
