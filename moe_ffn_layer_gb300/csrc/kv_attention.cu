@@ -820,8 +820,8 @@ __global__ void __launch_bounds__(128) kv_lay_kernel(KvDims d, KvSeqs s, KvAtten
 // the end.  The tiles come through a ring in shared memory that all warps read.
 // With few such CTAs `parts` of them share the row tiles of the same tokens (a
 // prompt of 4096 with weights: 650 us without, 477 with), and the last to end adds
-// their sums in order.  Measured: half the f16 MMA rate of mma.sync (a quarter of
-// tcgen05's), 0.22 ms for 247 M pairs of row and token.
+// their sums in order.  Measured: 206 us for 247 M pairs of row and
+// token (D = 128), the tensor pipe active 51% of the time.
 // A stage is four pairs: with a barrier at each pair the warps' MMAs and
 // exponentials fell into step.
 constexpr int kGainWarps = 16, kGainStages = 3, kGainPairs = 4, kGainBlock = 256, kGainTickets = 4096;

@@ -51,7 +51,7 @@ __device__ __forceinline__ float quotient(float x, float s, float inv, bool exac
 }
 
 // Bound: the bf16 rows read once and their codes written once (3 bytes a
-// value): 16k tokens of 8 heads of 128 in 18 us, 4.7 TB/s; a decode step's single
+// value): 13.9k tokens of 8 heads of 128 in 18 us, 4.7 TB/s; a decode step's single
 // rows are launch latency, 4.5 us.  The rows stay in
 // registers between the maximum and the rounding: kVecs vectors a thread, as
 // many as a page has (4 to 16), so that small pages leave room for more CTAs
