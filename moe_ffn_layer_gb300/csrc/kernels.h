@@ -145,13 +145,14 @@ struct KvAttention {
   float* lse;
   float* weights;
   long long w_stride;
+  int few;   // both kernels run: the sequences of up to so many query rows of a kv head are the decode kernel's; 0: one runs
 };
 size_t kv_attention_ws_bytes(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights);
 int kv_attention_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, void* ws,
                         int* status, cudaStream_t stream, int* launches);
 // The attention for many query rows per sequence (tcgen05): out, and lse where given.
 // Rows of partial results (0: the key axis is not cut), and the launch, which keeps O and (maximum, sum) of each.
-size_t kv_prefill_part_rows(const KvDims& d, int Hq, int B, int max_q, int max_len);
+size_t kv_prefill_part_rows(const KvDims& d, int Hq, int B, int T_q, int few, int max_len);
 int kv_prefill_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& a, float* part_o,
                       float2* part_ml, int* status, cudaStream_t stream, int* launches);
 struct KvEvict {

@@ -91,7 +91,7 @@ int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv
   int* status = nullptr;
   int sms = 0, n = 0;
   if ((rc = moe::current_device_info(&status, &sms))) return rc;
-  const moe::KvAttention a{q, q_stride, Hq, cu_q, T_q, max_q, scale, out, lse, weights, w_stride};
+  const moe::KvAttention a{q, q_stride, Hq, cu_q, T_q, max_q, scale, out, lse, weights, w_stride, 0};
   rc = moe::kv_attention_launch(kd, pool_of(pool), seqs_of(s), a, ws, status, stream, &n);
   moe::set_last_launches(n);
   return rc;

@@ -437,6 +437,7 @@ struct Cursor {
       set_status(status, MOE_ERR_DEVICE_CHECK);
       return;
     }
+    if (at.few && n * (at.Hq / d.Hkv) > at.few) return;   // the other kernel's
     tiles = (n * (at.Hq / d.Hkv) + tile_rows - 1) / tile_rows;
     steps = max((len + kSpan - 1) / kSpan, 1);
   }
@@ -1022,6 +1023,15 @@ bool on_prefill(const KvDims& d, int Hq, int B, int max_q, int max_len) {
   return rows > kDecodeRows && steps > kSMs * ctas_per_sm<128, 2>();
 }
 
+// Beside it the decode kernel takes the sequences of up to so many rows, where
+// there may be some (the shortest has T_q less the others' most); 0: it is not
+// launched.  64 sequences of 513 to 8192 tokens, 63 asking for one token and one
+// for 512 (8 kv heads of 128): 712 us with one kernel, 286 with both.
+int beside_prefill(const KvDims& d, int Hq, int B, int T_q, int max_q) {
+  const long long least = T_q - static_cast<long long>(B - 1) * max_q;
+  return B > 1 && least * (Hq / d.Hkv) <= kDecodeRows ? kDecodeRows : 0;
+}
+
 Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights) {
   constexpr size_t slots = static_cast<size_t>(kSMs) * ctas_per_sm<128, 2>() * 2 * 16;
   static_assert(ctas_per_sm<64, 2>() <= ctas_per_sm<128, 2>() && ctas_per_sm<128, 1>() <= ctas_per_sm<64, 1>() &&
@@ -1042,7 +1052,7 @@ Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, b
   w.ml = take(slots * sizeof(float2));
   w.lse = take(rows * sizeof(float));
   if (on_prefill(d, Hq, B, max_q, max_len)) {
-    const size_t part_rows = kv_prefill_part_rows(d, Hq, B, max_q, max_len);
+    const size_t part_rows = kv_prefill_part_rows(d, Hq, B, T_q, beside_prefill(d, Hq, B, T_q, max_q), max_len);
     w.part_o = take(part_rows * d.D * sizeof(float));
     w.part_ml = take(part_rows * sizeof(float2));
   }
@@ -1067,7 +1077,9 @@ int launch_decode(const KvDims& d, const KvPool& pool, const KvSeqs& s, const Kv
   constexpr size_t smem = kWarps * ring_stages<R>() * (Ring<D>::kStageBytes + 16) + 2 * 8 * R * (D + 4) * sizeof(float);
   if (kv_allow_smem<kv_decode_kernel<D, R>>(smem) != cudaSuccess) return MOE_ERR_CUDA;
   // no more CTAs than the longest call of these sizes gives steps to
-  const long long tiles = (static_cast<long long>(a.max_q) * (a.Hq / d.Hkv) + 8 * R - 1) / (8 * R);
+  long long rows = static_cast<long long>(a.max_q) * (a.Hq / d.Hkv);
+  if (a.few) rows = std::min<long long>(rows, a.few);
+  const long long tiles = (rows + 8 * R - 1) / (8 * R);
   const double steps = static_cast<double>(s.B) * d.Hkv * tiles * ((static_cast<long long>(s.max_len) + kSpan - 1) / kSpan + 1);
   if (steps > INT_MAX) return MOE_ERR_UNSUPPORTED;
   const int ctas = steps < kSMs * ctas_per_sm<D, R>() ? static_cast<int>(steps) : kSMs * ctas_per_sm<D, R>();
@@ -1089,11 +1101,16 @@ int launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, KvAttention a, 
                     reinterpret_cast<float2*>(base + w.ml),
                     a.weights && few ? reinterpret_cast<float*>(base + w.scores) : nullptr, w.pitch};
   const long long rows = static_cast<long long>(a.max_q) * (a.Hq / d.Hkv);
-  const int rc = on_prefill(d, a.Hq, s.B, a.max_q, s.max_len)
-                     ? kv_prefill_launch(d, pool, s, a, reinterpret_cast<float*>(base + w.part_o),
-                                         reinterpret_cast<float2*>(base + w.part_ml), status, stream, launches)
-                 : few              ? launch_decode<D, 1>(d, pool, s, a, parts, status, stream, launches)
-                                    : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
+  int rc = MOE_OK;
+  const bool prefill = on_prefill(d, a.Hq, s.B, a.max_q, s.max_len);
+  if (prefill) {
+    a.few = beside_prefill(d, a.Hq, s.B, a.T_q, a.max_q);
+    rc = kv_prefill_launch(d, pool, s, a, reinterpret_cast<float*>(base + w.part_o),
+                           reinterpret_cast<float2*>(base + w.part_ml), status, stream, launches);
+  }
+  if (rc == MOE_OK && (!prefill || a.few))
+    rc = few ? launch_decode<D, 1>(d, pool, s, a, parts, status, stream, launches)
+             : launch_decode<D, 2>(d, pool, s, a, parts, status, stream, launches);
   if (rc || !a.weights || s.max_len == 0) return rc;
   if (few) {
     const unsigned blocks = (static_cast<unsigned>(s.max_len) + kGainTokens - 1) / kGainTokens;

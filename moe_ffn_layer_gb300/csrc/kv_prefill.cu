@@ -62,12 +62,59 @@ struct PrefillArgs {
   KvAttention at;
   int* status;
   uint64_t wait_ns;
-  // The key axis cut in `parts`, at steps: a part's O (relative to its maximum),
-  // its maxima and sums, by [part][pair][sequence, head][row of the pair].
-  int pairs, parts;
+  // The key axis cut in parts, at steps: a part's O (relative to its maximum), its
+  // maxima and sums, by [part][unit][row of the unit].
+  int most_parts;    // 1: not cut
   float* part_o;     // rows of D
   float2* part_ml;
 };
+
+// A unit: two tiles of rows of a (sequence, kv head).  They count by sequence, in
+// it from the rows that see most, heads innermost: as many as the real sequences
+// have.  A converged warp finds unit u (sequences that fail their checks have
+// none) and returns whether there is one; `total`, if asked, is their number.
+struct Unit {
+  int b, h, pair, first, n, len;
+};
+__device__ __forceinline__ bool find_unit(const PrefillArgs& a, int u, Unit* unit, int* total) {
+  const int lane = threadIdx.x & 31, g = a.at.Hq / a.d.Hkv;
+  int before = 0;
+  bool found = false;
+  for (int base = 0; base < a.s.B && (total || !found); base += 32) {
+    const int b = base + lane;
+    int first = 0, n = 0, len = 0, pairs = 0;
+    if (b < a.s.B && kv_sequence(a.s, a.at.cu_q, a.at.T_q, b, a.d, a.status, &first, &n, &len)) {
+      if (n > a.at.max_q)
+        set_status(a.status, MOE_ERR_DEVICE_CHECK);
+      else if (n * g > a.at.few)
+        pairs = (n * g + 2 * kTile - 1) / (2 * kTile);
+    }
+    int upto = pairs * a.d.Hkv;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, i);
+      if (lane >= i) upto += v;
+    }
+    const int rel = u - before;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, rel < upto);
+    if (!found && hit) {
+      const int from = __ffs(hit) - 1;
+      const int p = __shfl_sync(0xFFFFFFFFu, pairs, from);
+      const int in = rel - (__shfl_sync(0xFFFFFFFFu, upto, from) - p * a.d.Hkv);
+      *unit = Unit{base + from, in % a.d.Hkv, p - 1 - in / a.d.Hkv, __shfl_sync(0xFFFFFFFFu, first, from),
+                   __shfl_sync(0xFFFFFFFFu, n, from), __shfl_sync(0xFFFFFFFFu, len, from)};
+      found = true;
+    }
+    before = min(before + __shfl_sync(0xFFFFFFFFu, upto, 31), 1 << 30);   // (boundaries that overlap: no overflow)
+  }
+  if (total) *total = before;
+  return found;
+}
+
+// Parts of `units` units: as many as give each SM a CTA.
+__device__ __forceinline__ int parts_of(const PrefillArgs& a, int units) {
+  return units == 0 ? 1 : max(1, min(kSMs / units, a.most_parts));
+}
 
 // Steps of a part of a unit of `steps`: the same in the kernel and in the join.
 __device__ __forceinline__ int part_steps(int steps, int parts) { return (steps + parts - 1) / parts; }
@@ -379,7 +426,7 @@ __device__ __forceinline__ void multiply_out(const PrefillArgs& a, Ctrl* ctrl, u
 template <int D>
 __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32_t smem, uint32_t tmem, int t, int b,
                                         int h, int g, int first, int n, int len, int row0, int from,
-                                        int steps) {
+                                        int steps, bool cut) {
   using S = Smem<D>;
   const KvAttention& at = a.at;
   volatile int* abort = &ctrl->abort;
@@ -543,9 +590,7 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
     return;
   __syncwarp();
   tc_fence_after();
-  const bool cut = a.parts > 1;
   const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
-  // (in the grid's order)
   const size_t slot = static_cast<size_t>(blockIdx.x) * 2 * kTile + t * kTile + in_tile;
   float4* part = reinterpret_cast<float4*>(a.part_o + slot * D);
   uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(at.out) + at_row * D);
@@ -591,21 +636,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a) 
   const uint32_t smem = smem_u32(base);
   chain_wait();
   ChainReleaseAtExit release;
-  // the rows that see most first: the last CTAs to start are the shortest
-  const int heads = a.s.B * a.d.Hkv, unit = blockIdx.x % heads;
-  const int pair = a.pairs - 1 - blockIdx.x / heads % a.pairs, part = blockIdx.x / heads / a.pairs;
-  const int b = unit / a.d.Hkv, h = unit % a.d.Hkv, g = a.at.Hq / a.d.Hkv;
-  int first, n, len;
-  if (!kv_sequence(a.s, a.at.cu_q, a.at.T_q, b, a.d, a.status, &first, &n, &len)) return;
-  if (n > a.at.max_q) {
-    set_status(a.status, MOE_ERR_DEVICE_CHECK);
-    return;
+  int u = blockIdx.x, part = 0, parts = 1;
+  Unit unit;
+  if (a.most_parts > 1) {
+    int units;
+    find_unit(a, 0, &unit, &units);
+    parts = parts_of(a, units);
+    if (u >= units * parts) return;
+    part = u / units;
+    u %= units;
   }
-  const int rows = n * g, row0 = pair * 2 * kTile;
-  if (row0 >= rows) return;
+  if (!find_unit(a, u, &unit, nullptr)) return;
+  const int b = unit.b, h = unit.h, first = unit.first, n = unit.n, len = unit.len, g = a.at.Hq / a.d.Hkv;
+  const int rows = n * g, row0 = unit.pair * 2 * kTile;
   const int tiles = row0 + kTile < rows ? 2 : 1;
   const int seen = max(len - n + (min(row0 + 2 * kTile, rows) - 1) / g + 1, 0);   // by the last row
-  const int all = (seen + kStep - 1) / kStep, per = part_steps(all, a.parts);
+  const int all = (seen + kStep - 1) / kStep, per = part_steps(all, parts);
   if (part > 0 && part * per >= all) return;   // (the join does not ask for it)
   const int from = part * per * kStep, steps = min(per, all - part * per), end = min(seen, from + steps * kStep);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
@@ -654,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(PrefillArgs a) 
     }
   } else if (warp < kConvertWarp) {
     const int t = (warp - kSoftmaxWarp) / 4;
-    if (t < tiles) softmax<D>(a, ctrl, smem, tmem, t, b, h, g, first, n, len, row0, from, steps);
+    if (t < tiles) softmax<D>(a, ctrl, smem, tmem, t, b, h, g, first, n, len, row0, from, steps, parts > 1);
   } else {
     convert<D>(a, ctrl, smem, b, h, from, end, steps);
   }
@@ -673,18 +719,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_prefill_join_kernel(Prefil
   constexpr int kPer = D / 32;
   chain_wait();
   ChainReleaseAtExit release;
-  const int heads = a.s.B * a.d.Hkv, unit = blockIdx.y, b = unit / a.d.Hkv, h = unit % a.d.Hkv, g = a.at.Hq / a.d.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x * kJoinWarps + warp;
-  int first, n, len;
-  if (!kv_sequence(a.s, a.at.cu_q, a.at.T_q, b, a.d, a.status, &first, &n, &len)) return;
-  if (n > a.at.max_q || row >= n * g) return;   // (the first is recorded by the parts)
-  const int pair = row / (2 * kTile), rows = n * g;
-  const int seen = max(len - n + (min((pair + 1) * 2 * kTile, rows) - 1) / g + 1, 0);
-  const int all = (seen + kStep - 1) / kStep, per = part_steps(all, a.parts);
-  const int used = max((all + max(per, 1) - 1) / max(per, 1), 1);
-  const auto slot = [&](int p) {
-    return ((static_cast<size_t>(p) * a.pairs + (a.pairs - 1 - pair)) * heads + unit) * 2 * kTile + row % (2 * kTile);
-  };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, in_unit = blockIdx.x * kJoinWarps + warp;
+  const int u = blockIdx.y, g = a.at.Hq / a.d.Hkv;
+  Unit unit;
+  int units;
+  if (!find_unit(a, u, &unit, &units)) return;
+  const int parts = parts_of(a, units), rows = unit.n * g, h = unit.h, first = unit.first;
+  const int row = unit.pair * 2 * kTile + in_unit;
+  if (parts == 1 || row >= rows) return;
+  const int seen = max(unit.len - unit.n + (min((unit.pair + 1) * 2 * kTile, rows) - 1) / g + 1, 0);
+  const int all = (seen + kStep - 1) / kStep, per = part_steps(all, parts), used = all ? (all + per - 1) / per : 1;
+  const auto slot = [&](int p) { return (static_cast<size_t>(p) * units + u) * 2 * kTile + in_unit; };
   float m = -INFINITY;
   for (int p = lane; p < used; p += 32) m = fmaxf(m, a.part_ml[slot(p)].x);
 #pragma unroll
@@ -715,51 +760,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv_prefill_join_kernel(Prefil
   if (lane == 0 && a.at.lse) a.at.lse[at_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// The units that a call can have, and the parts that they can be cut in: eight
+// steps at least, and none where there are too many units for certain.
+// 128 rows on 8 kv heads over one sequence of 32768 tokens: 931 us uncut, 67 in 19
+// parts; 512 rows 1028 and 136 (9 parts); four of 2048, 512 rows: 64 and 55 (2).
+long long most_units(const KvDims& d, int Hq, int B, int T_q, int max_q) {
+  const long long g = Hq / d.Hkv, each = (max_q * g + 2 * kTile - 1) / (2 * kTile);
+  return std::min(each * B, T_q * g / (2 * kTile) + B) * d.Hkv;
+}
+int most_parts(const KvDims& d, int Hq, int B, int T_q, int few, int max_len) {
+  const long long rows = static_cast<long long>(T_q) * (Hq / d.Hkv) - static_cast<long long>(B) * few;   // at least
+  return rows / (2 * kTile) * d.Hkv > kSMs / 2 ? 1 : std::max(1, std::min(kSMs, max_len / (8 * kStep)));
+}
+
 template <int D>
 int launch(const PrefillArgs& a, cudaStream_t stream, int* launches) {
   if (kv_allow_smem<kv_prefill_kernel<D>>(Smem<D>::total) != cudaSuccess) return MOE_ERR_CUDA;
-  const double ctas = static_cast<double>(a.pairs) * a.s.B * a.d.Hkv * a.parts;
-  if (ctas > INT_MAX) return MOE_ERR_UNSUPPORTED;
-  if (launch_chained(kv_prefill_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), Smem<D>::total, stream,
-                     a) != cudaSuccess)
+  const long long units = most_units(a.d, a.at.Hq, a.s.B, a.at.T_q, a.at.max_q);
+  if (units > INT_MAX) return MOE_ERR_UNSUPPORTED;
+  const bool cut = a.most_parts > 1;
+  if (launch_chained(kv_prefill_kernel<D>, dim3(static_cast<unsigned>(cut ? std::max<long long>(units, kSMs) : units)),
+                     dim3(kThreads), Smem<D>::total, stream, a) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++*launches;
-  if (a.parts == 1) return MOE_OK;
-  const unsigned rows = static_cast<unsigned>(a.pairs) * 2 * kTile;
-  if (launch_chained(kv_prefill_join_kernel<D>, dim3(rows / kJoinWarps, a.s.B * a.d.Hkv), dim3(kJoinWarps * 32), 0,
-                     stream, a) != cudaSuccess)
+  if (!cut) return MOE_OK;
+  const unsigned joins = static_cast<unsigned>(std::min<long long>(units, kSMs / 2));   // more are not cut
+  if (launch_chained(kv_prefill_join_kernel<D>, dim3(2 * kTile / kJoinWarps, joins), dim3(kJoinWarps * 32), 0, stream,
+                     a) != cudaSuccess)
     return MOE_ERR_CUDA;
   ++*launches;
   return MOE_OK;
 }
 
-long long pairs_of(const KvDims& d, int Hq, int max_q) {
-  return (static_cast<long long>(max_q) * (Hq / d.Hkv) + 2 * kTile - 1) / (2 * kTile);
-}
-
-// Parts of the key axis: as many as give each SM a CTA, of eight steps at least.
-// 128 rows on 8 kv heads over one sequence of 32768 tokens: 931 us uncut, 67 in 19
-// parts; 512 rows 1028 and 136 (9 parts); four of 2048, 512 rows: 64 and 55 (2).
-int parts_of(const KvDims& d, int Hq, int B, int max_q, int max_len) {
-  const long long ctas = pairs_of(d, Hq, max_q) * B * d.Hkv;
-  if (ctas == 0) return 1;
-  const long long parts = std::min<long long>(kSMs / ctas, max_len / (8 * kStep));
-  return parts > 1 ? static_cast<int>(parts) : 1;
-}
-
 }  // namespace
 
-size_t kv_prefill_part_rows(const KvDims& d, int Hq, int B, int max_q, int max_len) {
-  const int parts = parts_of(d, Hq, B, max_q, max_len);
-  return parts == 1 ? 0 : static_cast<size_t>(pairs_of(d, Hq, max_q)) * B * d.Hkv * parts * 2 * kTile;
+size_t kv_prefill_part_rows(const KvDims& d, int Hq, int B, int T_q, int few, int max_len) {
+  return most_parts(d, Hq, B, T_q, few, max_len) == 1 ? 0 : static_cast<size_t>(kSMs) * 2 * kTile;
 }
 
 int kv_prefill_launch(const KvDims& d, const KvPool& pool, const KvSeqs& s, const KvAttention& at, float* part_o,
                       float2* part_ml, int* status, cudaStream_t stream, int* launches) {
-  const long long pairs = pairs_of(d, at.Hq, at.max_q);
-  if (pairs > INT_MAX) return MOE_ERR_UNSUPPORTED;
-  const PrefillArgs a{d, pool, s, at, status, wait_limit_ns(), static_cast<int>(pairs),
-                      parts_of(d, at.Hq, s.B, at.max_q, s.max_len), part_o, part_ml};
+  const PrefillArgs a{d, pool, s, at, status, wait_limit_ns(), most_parts(d, at.Hq, s.B, at.T_q, at.few, s.max_len), part_o, part_ml};
   return d.D == 128 ? launch<128>(a, stream, launches) : launch<64>(a, stream, launches);
 }
 

@@ -32,6 +32,11 @@ SHAPES = [
     ([200] * 7, [150, 200, 1, 0, 129, 64, 200], 3, 7, 128, 32),   # enough rows to fill the GPU uncut
     ([130] * 24, [40] * 24, 4, 4, 64, 16),
     ([2, 1300], [600, 600], 2, 4, 128, 64),                # more queries than tokens
+    # single tokens, sequences that ask for nothing and chunks together
+    ([900, 1, 3000, 0, 64, 2100] + [33] * 30, [1, 1, 300, 1, 0, 16] + [1] * 30, 2, 4, 128, 64),
+    ([2000] + [70 + i for i in range(40)], [65] + [1 + i % 3 for i in range(40)], 1, 16, 64, 16),
+    ([500, 3000, 20], [17, 16, 1], 4, 4, 128, 32),         # 68 rows beside 64
+    ([1100, 5, 1500, 1500], [200, 5, 1, 1400], 2, 2, 64, 64),
 ]
 
 
@@ -164,3 +169,24 @@ def test_offsets_past_32_bits(n, L):
     ds = (D / 16) * 2.0 ** -22 * size + 2.0 ** -21 * size
     e = np.abs(out.double().cpu().numpy() - ref) - 2.0 ** -8 * np.abs(ref) - (2.0 ** -10 + 2 * ds.max()) * mass
     assert e.max() <= 0 and status() == 0
+
+
+@pytest.mark.parametrize("bad", [0, 2, 34])
+def test_sequences_of_a_mixed_batch_that_fail_their_checks_are_skipped(bad):
+    rng = np.random.default_rng(27)
+    lens, new = [1500, 40, 1200] + [50] * 32, [200, 1, 130] + [1] * 32
+    table, pages = make_table(rng, lens, 16)
+    cache = upload(make_pool(rng, pages, 2, 16, 128))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = torch.from_numpy(rng.standard_normal((cu[-1], 8, 128))).bfloat16().cuda()
+    run = lambda ls, **kw: cache.attend(q, i32(table), i32(ls), i32(cu), 200, 1500, **kw)
+    want = run(lens)
+    assert status() == 0
+    out = torch.full_like(want, 3.0)
+    run([-1 if b == bad else L for b, L in enumerate(lens)], out=out)
+    assert status() == -6 and status() == 0
+    rows = torch.arange(cu[-1], device="cuda")
+    gone = (rows >= int(cu[bad])) & (rows < int(cu[bad + 1]))
+    assert bool((out[gone] == 3).all())
+    # (the cut of the key axis goes by the units there are, so the sums' order may differ)
+    torch.testing.assert_close(out[~gone].float(), want[~gone].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
