@@ -35,6 +35,7 @@ constexpr int kTok = 32;          // tokens of a warp's step
 constexpr int kWarps = 4;
 constexpr int kSpan = kWarps * kTok;   // tokens of a CTA's step: one step of each warp
 constexpr int kDecodeRows = 64;        // query rows of a kv head up to which the decode kernel is taken (on_prefill)
+constexpr int kBesideRows = 32;        // the same beside the prefill kernel (beside_prefill)
 constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -1026,10 +1027,13 @@ bool on_prefill(const KvDims& d, int Hq, int B, int max_q, int max_len) {
 // Beside it the decode kernel takes the sequences of up to so many rows, where
 // there may be some (the shortest has T_q less the others' most); 0: it is not
 // launched.  64 sequences of 513 to 8192 tokens, 63 asking for one token and one
-// for 512 (8 kv heads of 128): 712 us with one kernel, 286 with both.
+// for 512 (8 kv heads of 128): 712 us with one kernel, 280 with both.  32 rows of
+// 16, 32 and 64: 48 times 20 rows beside a chunk of 512, all over 4096 tokens, 388,
+// 258 and 257 us; 16 sequences of 48 to 96 rows over 32768 945, 945 and 1198; but 12
+// times 48 rows beside a chunk, over 8192, 479, 479 and 272.
 int beside_prefill(const KvDims& d, int Hq, int B, int T_q, int max_q) {
   const long long least = T_q - static_cast<long long>(B - 1) * max_q;
-  return B > 1 && least * (Hq / d.Hkv) <= kDecodeRows ? kDecodeRows : 0;
+  return B > 1 && least * (Hq / d.Hkv) <= kBesideRows ? kBesideRows : 0;
 }
 
 Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, bool weights) {

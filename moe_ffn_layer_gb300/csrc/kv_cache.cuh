@@ -73,17 +73,21 @@ __device__ __forceinline__ uint4 e4m3x16_scaled(const uint4& v, float ratio) {
 // The packed cu_* boundaries and length of sequence b, checked: first row,
 // rows n >= 0 of T, length in [0, max_len] with its pages inside the table's
 // width.  False (and MOE_ERR_DEVICE_CHECK) where they are not.
+__device__ __forceinline__ bool kv_sequence_is(const KvSeqs& s, int T, const KvDims& d, int* status, int first, int n,
+                                               int len) {
+  if (first < 0 || n < 0 || n > T - first || len < 0 || len > s.max_len ||
+      (static_cast<long long>(len) + d.page - 1) >> d.shift > s.width) {
+    set_status(status, MOE_ERR_DEVICE_CHECK);
+    return false;
+  }
+  return true;
+}
 __device__ __forceinline__ bool kv_sequence(const KvSeqs& s, const int32_t* cu, int T, int b, const KvDims& d, int* status,
                                             int* first, int* n, int* len) {
   *first = cu[b];
   *n = cu[b + 1] - cu[b];
   *len = s.seq_lens[b];
-  if (*first < 0 || *n < 0 || *n > T - *first || *len < 0 || *len > s.max_len ||
-      (static_cast<long long>(*len) + d.page - 1) >> d.shift > s.width) {
-    set_status(status, MOE_ERR_DEVICE_CHECK);
-    return false;
-  }
-  return true;
+  return kv_sequence_is(s, T, d, status, *first, *n, *len);
 }
 
 }  // namespace moe
