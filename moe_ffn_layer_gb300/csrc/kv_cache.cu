@@ -55,7 +55,8 @@ __device__ __forceinline__ float quotient(float x, float s, float inv, bool exac
 // rows are launch latency, 4.5 us.  The rows stay in
 // registers between the maximum and the rounding: kVecs vectors a thread, as
 // many as a page has (4 to 16), so that small pages leave room for more CTAs
-// and their loads.
+// and their loads: 12000 tokens in pages of 16, 32 and 64 (D = 128)
+// 22, 17 and 17 us, with 16 for all 37, 24 and 19.
 template <int kVecs>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(KvDims d, KvPool pool, KvSeqs s,
                                                                    const __nv_bfloat16* __restrict__ kn,
@@ -182,7 +183,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // scheduling.  The weights are read five times; where the longest sequence's fit
 // (kStaged), the first pass leaves them in shared memory.  Latency of its passes:
 // 31 us for 256 (sequence, head) pairs of up to 16384.
-constexpr int kMostStaged = 24576;   // 96 KB: two CTAs on an SM
+// 192 KB.  With and without, selection and gathering, us: 32 sequences of 16384 120
+// and 126, of 32768 (one CTA an SM) 151 and 154, of 49152 179 and 181; one of 16384
+// 21 and 23, of 32768 32 and 34, of 49152 43 and 47.
+constexpr int kMostStaged = 49152;
 template <bool kStaged>
 __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvSeqs s, KvEvict e, int* status) {
   extern __shared__ float staged[];
@@ -317,7 +321,7 @@ constexpr int kGatherThreads = 128;
 // the largest of its rows' scales; a row from a page of another scale has its
 // codes rescaled (exact for powers of two, except into the subnormals).
 // Bound: the kept codes read and written once: 32 sequences of 3000 to 16384
-// tokens back to 4096 in 87 us, 5.6 TB/s of DRAM traffic.
+// tokens back to 4096 in 86 us, 5.6 TB/s of DRAM traffic.
 __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(KvDims d, KvPool src, KvSeqs s, KvPool dst,
                                                                    KvEvict e, int* status) {
   chain_wait();
