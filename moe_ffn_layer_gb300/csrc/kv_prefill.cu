@@ -564,6 +564,9 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
         const float r = to == m ? 1.f : ex2(m - to);   // (0 for the first)
         m = to;
         l *= r;
+        // What this step has stored so far (the weights of the tokens before these, O
+        // scaled for them) is read again below, and a load does not wait for a store.
+        tmem_st_wait();
         // O so far: once the last step's product is in it (products of a tile end in
         // order, and the next one waits for these weights)
         if (j > 0) {
