@@ -762,7 +762,8 @@ __global__ void __launch_bounds__(kGainThreads) kv_gain_kept_kernel(KvDims d, Kv
     const size_t row0 = static_cast<size_t>(tile.first + i) * at.Hq + h * g;
 #pragma unroll 4
     for (int r = 0; r < g; ++r) {
-      const float lse = at.lse[row0 + r] * kLog2e;
+      float lse = at.lse[row0 + r] * kLog2e;
+      if (lse == -INFINITY) lse = INFINITY;   // every page of the row's is missing: it adds nothing
       const float4 v = *reinterpret_cast<const float4*>(scores + (row0 + r) * pitch + t);   // (pitch holds whole steps)
       sum[0] += exp2_approx(v.x - lse);
       sum[1] += t + 1 < sees ? exp2_approx(v.y - lse) : 0.f;
