@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvS
   ChainReleaseAtExit release;
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   int len = s.seq_lens[b];
-  if (len < 0 || len > s.max_len) {
+  if (!kv_length_is(s, d, len)) {
     if (tid == 0) set_status(status, MOE_ERR_DEVICE_CHECK);
     len = 0;   // skipped: nothing is kept
   }

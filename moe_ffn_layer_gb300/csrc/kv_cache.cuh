@@ -70,13 +70,17 @@ __device__ __forceinline__ uint4 e4m3x16_scaled(const uint4& v, float ratio) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// A sequence's length, checked: in [0, max_len] with its pages inside the table's width.
+__device__ __forceinline__ bool kv_length_is(const KvSeqs& s, const KvDims& d, int len) {
+  return len >= 0 && len <= s.max_len && (static_cast<long long>(len) + d.page - 1) >> d.shift <= s.width;
+}
+
 // The packed cu_* boundaries and length of sequence b, checked: first row,
-// rows n >= 0 of T, length in [0, max_len] with its pages inside the table's
-// width.  False (and MOE_ERR_DEVICE_CHECK) where they are not.
+// rows n >= 0 of T, and the length.  False (and MOE_ERR_DEVICE_CHECK) where
+// they are not what they have to be.
 __device__ __forceinline__ bool kv_sequence_is(const KvSeqs& s, int T, const KvDims& d, int* status, int first, int n,
                                                int len) {
-  if (first < 0 || n < 0 || n > T - first || len < 0 || len > s.max_len ||
-      (static_cast<long long>(len) + d.page - 1) >> d.shift > s.width) {
+  if (first < 0 || n < 0 || n > T - first || !kv_length_is(s, d, len)) {
     set_status(status, MOE_ERR_DEVICE_CHECK);
     return false;
   }
