@@ -525,7 +525,7 @@ __device__ __forceinline__ void softmax(const PrefillArgs& a, Ctrl* ctrl, uint32
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int left = gone[e] ? 0 : sees - (t0 + 32 * c + 16 * e);
-          const bool flat = f[e] == 0.f || gone[e];   // (no -inf times 0)
+          const bool flat = f[e] == 0.f || left <= 0;   // (no -inf times 0, or times a row's NaN)
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[16 * e + i] = i >= left ? 0xFF800000u : flat ? 0u : s[16 * e + i];
           if (flat) f[e] = 1.f;

@@ -1,4 +1,5 @@
-"""Query rows that are left with nothing to see: every page of theirs missing."""
+"""Query rows that are left with nothing to see: every page of theirs missing, or
+more queries than tokens, whatever the row itself holds."""
 import numpy as np
 import pytest
 import torch
@@ -63,3 +64,32 @@ def test_a_prompt_whose_first_pages_are_missing(n):
     assert torch.equal(w[..., :blind], w0[..., :blind])
     gained = (w - w0).double().sum(-1).cpu()
     assert torch.allclose(gained, torch.full_like(gained, g * (n - blind)), rtol=1e-4, atol=1e-6)
+
+
+# lens, new, kv heads, heads of each, head size
+@pytest.mark.parametrize("lens,new,Hkv,g,D", [([3], [5], 2, 2, 128), ([3, 40], [9, 1], 1, 4, 64),
+                                              ([100, 3000], [200, 300], 2, 8, 128), ([70, 900], [100, 640], 2, 4, 64),
+                                              ([40, 8000], [90, 33], 1, 4, 128)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_row_that_sees_nothing_may_hold_anything(lens, new, Hkv, g, D, value):
+    """As rows that a program never filled do: they give 0 and -inf like any other that sees nothing."""
+    rng = np.random.default_rng(sum(lens))
+    table, pages = make_table(rng, lens, 16)
+    cache = upload(make_pool(rng, pages, Hkv, 16, D))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = torch.from_numpy(rng.standard_normal((cu[-1], Hkv * g, D))).bfloat16().cuda()
+
+    def run(q):
+        w, lse = torch.zeros(len(lens), Hkv, max(lens), device="cuda"), torch.empty(cu[-1], Hkv * g, device="cuda")
+        out = cache.attend(q, i32(table), i32(lens), i32(cu), max(new), max(lens), weights=w, lse=lse)
+        assert status() == 0
+        return out, lse, w
+
+    want = run(q)
+    bad = q.clone()
+    blind = new[0] - lens[0]                        # the first queries of sequence 0
+    bad[:blind, :, D // 2] = value
+    bad[blind - 1, 0] = value
+    got = run(bad)
+    assert not got[0][:blind].any() and bool(got[1][:blind].isneginf().all())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
