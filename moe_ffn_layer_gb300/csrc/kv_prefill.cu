@@ -246,12 +246,12 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t v, uint32_t unit) {
                     bf16x2_mul((prmt(v, 0u, 0xB3A2u) << 4) & 0x87F087F0u, unit));
 }
 
-// A V scale's power of two, bounded so that the bf16 operand and the rest stay in range.
+// A V scale's power of two, bounded so that the bf16 operand and the rest stay in
+// range (a smaller or subnormal scale's rest is below 1).
 __device__ __forceinline__ int v_exponent(float vs) {
   const int e = static_cast<int>(__float_as_uint(vs) >> 23 & 255u) - 127;
   return max(-100, min(e, 7));
 }
-__device__ __forceinline__ bool v_is_zero(float vs) { return (__float_as_uint(vs) & 0x7F800000u) == 0; }
 
 // The converters' part: K and V of every step, each into a ring of its own.
 template <int D>
@@ -320,7 +320,7 @@ __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         float lv = 0.f, inv = 1.f;
-        if (!v_is_zero(vs[i])) {
+        if (vs[i] != 0.f) {
           const float m = vs[i] * __uint_as_float(static_cast<uint32_t>(127 - v_exponent(vs[i])) << 23);
           lv = log2f(m);
           inv = 1.f / m;
@@ -349,7 +349,7 @@ __device__ __forceinline__ void convert(const PrefillArgs& a, Ctrl* ctrl, uint32
     if (!wait_for(&ctrl->v_empty[st], parity ^ 1u, abort, a.status, a.wait_ns)) return;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const uint32_t u = v_is_zero(vs[i]) ? 0u : static_cast<uint32_t>(v_exponent(vs[i]) + 247) << 7;
+      const uint32_t u = vs[i] == 0.f ? 0u : static_cast<uint32_t>(v_exponent(vs[i]) + 247) << 7;
       const uint32_t unit = u | u << 16;
 #pragma unroll
       for (int f = 0; f < kHalves; ++f) {
