@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPo
         for (int nt = 0; nt < kTok / 8; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int need = (t0 + nt * 8 + 2 * c + e - base) * g;
+            const int need = max(t0 + nt * 8 + 2 * c + e - base, 0) * g;   // (far below `base` the product would not fit)
             if (mt * 16 + n < need || no_page(ks[nt >> 1])) x[nt][e] = 0.f;
             if (mt * 16 + 8 + n < need || no_page(ks[nt >> 1])) x[nt][2 + e] = 0.f;
           }
