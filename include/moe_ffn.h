@@ -325,16 +325,19 @@ MOE_API int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const m
  *          (sequence, kv head) gains sum p_t over the call's queries and the
  *          heads of that kv head; other entries keep their values
  *  ws      scratch of moe_kv_attention_workspace_bytes(...) bytes (weights: not 0
- *          for a call that has them), 256-byte aligned and zero-filled before its first use (calls leave its
- *          counters zero; they sit at the same place for every size, so calls
- *          of any sizes may use one buffer in turn); calls that share it must
- *          not overlap on the GPU
+ *          for a call that has them), 256-byte aligned, its first
+ *          MOE_KV_COUNTER_BYTES zero before its first use (counters, which calls
+ *          leave zero; they sit at the same place for every size, so calls
+ *          of any sizes may use one buffer in turn; nothing else is kept from
+ *          call to call); calls that share it must not overlap on the GPU, and
+ *          a captured graph uses it at every replay
  * A query that sees nothing (an empty sequence, or more queries than tokens)
  * gives out 0 and lse -inf; a query row that holds a NaN or an infinity gives
  * NaN.  Rows of q outside every sequence are neither read nor written.
  * Sums, maxima and outputs are held in fp32; the products' operands are exact
  * (q, K, V) or keep 16 bits (the softmax weights, at any size).  Results do not
  * depend on scheduling. */
+#define MOE_KV_COUNTER_BYTES 18432
 MOE_API size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int B, int T_q, int max_q,
                                                 int max_len, int weights);
 MOE_API int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, const moe_kv_seqs* s, const void* q,

@@ -59,6 +59,8 @@ class moe_kv_seqs(ctypes.Structure):
                 ("width", ctypes.c_int), ("max_len", ctypes.c_int)]
 
 
+KV_COUNTER_BYTES = 18432   # MOE_KV_COUNTER_BYTES: the part of an attention workspace that starts zero
+
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _L, _F, _R = ctypes.c_int64, ctypes.c_float, ctypes.POINTER
 _SIGS = {

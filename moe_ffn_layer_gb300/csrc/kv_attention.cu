@@ -1050,6 +1050,7 @@ Layout layout(const KvDims& d, int Hq, int B, int T_q, int max_q, int max_len, b
     at += align_up(bytes);
     return r;
   };
+  static_assert(align_up(kMostCtas * sizeof(int)) + align_up(kGainTickets * sizeof(int)) == MOE_KV_COUNTER_BYTES, "counters");
   take(kMostCtas * sizeof(int));
   w.gain_ticket = take(kGainTickets * sizeof(int));
   const size_t rows = static_cast<size_t>(T_q) * Hq;

@@ -26,6 +26,9 @@ def _current(device_index: int) -> int:
     return torch.cuda.current_stream(device_index).cuda_stream
 
 
+_capturing = torch.cuda.is_current_stream_capturing
+
+
 def _call(name: str, rc: int) -> None:
     if rc != 0:
         raise B.MoEError(name, rc)
@@ -63,7 +66,7 @@ class KVCache8:
         self._dims, self._pool = ctypes.byref(self.dims), ctypes.byref(self.pool)
         self._shape = tuple(k.shape[1:])
         self._need = (None, 0)   # the last call's sizes and the workspace bytes they need
-        self._ws = {}   # by stream: calls of different streams may overlap
+        self._ws = {}   # by stream: calls of different streams may overlap, and replays of graphs with any
 
     def _want_table(self, page_table, seq_lens, cu, cu_name):
         """Checks the sequences' tensors; returns the table's rows and width."""
@@ -99,14 +102,24 @@ class KVCache8:
             _current(self._dev) if stream is None else B.handle(stream)))
 
     def workspace(self, need: int, stream=None) -> torch.Tensor:
-        """The stream's workspace (default: the current stream's), of at least
-        `need` bytes, zero-filled when allocated (the library keeps its counters
-        zero from call to call)."""
-        key = _current(self._dev) if stream is None else B.handle(stream)
-        ws = self._ws.get(key)
+        """A workspace of at least `need` bytes for one call on `stream`
+        (default: the current stream): the stream's own, which its calls use in
+        turn.  A call that is being captured in a graph has one of its own,
+        allocated and its counters zeroed in the capture: its memory is the
+        graph's, whatever later calls need or other graphs are replayed."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._workspace(need, B.handle(stream))
+        return self._workspace(need, _current(self._dev))
+
+    def _workspace(self, need, key):
+        captured = _capturing()
+        ws = None if captured else self._ws.get(key)
         if ws is None or ws.numel() < need:
-            with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):
-                ws = self._ws[key] = torch.zeros(max(need, 256), dtype=torch.uint8, device=self.device)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            ws[:B.KV_COUNTER_BYTES].zero_()
+            if not captured:
+                self._ws[key] = ws
         return ws
 
     def attend(self, q: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor, max_q: int,

@@ -1,0 +1,92 @@
+"""Host logic of KVCache8 without a GPU: the C entry points are recorded, not called."""
+import contextlib
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from moe_ffn_layer_gb300 import binding as B
+from moe_ffn_layer_gb300 import build as build_mod
+from moe_ffn_layer_gb300 import kv_cache
+from moe_ffn_layer_gb300.kv_cache import KVCache8
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+class Recorder:
+    """Stands in for the library: the size query is the library's own, the launches are kept."""
+
+    def __init__(self, real):
+        self.calls = []
+        self.moe_kv_attention_workspace_bytes = real.moe_kv_attention_workspace_bytes
+        for name in ("moe_kv_append", "moe_kv_attention", "moe_kv_evict"):
+            setattr(self, name, lambda *args, name=name: self.keep(name, args))
+
+    def keep(self, name, args):
+        self.calls.append((name, args))
+        return 0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """A recorder in the library's place, on stream 0 of a machine that may have no GPU."""
+    build_mod.build()
+    rec = Recorder(B.lib())
+    monkeypatch.setattr(B, "_lib", rec)
+    monkeypatch.setattr(kv_cache, "_current", lambda device: 0)
+    monkeypatch.setattr(kv_cache, "_capturing", lambda: False, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    return rec
+
+
+def make(pages=8, Hkv=2, D=64, P=16):
+    return KVCache8(pages, Hkv, D, P, device="cpu")
+
+
+def attend(cache, max_len, Hq=4, B_=1, **kw):
+    q = torch.zeros(B_, Hq, cache.head_dim, dtype=torch.bfloat16)
+    width = -(-max_len // cache.page)
+    return cache.attend(q, torch.zeros(B_, width, dtype=torch.int32), torch.ones(B_, dtype=torch.int32),
+                        torch.arange(B_ + 1, dtype=torch.int32), 1, max_len, **kw)
+
+
+def ws_of(call):
+    """(address, bytes) of the workspace that an attention call was given."""
+    return call[1][14:16]
+
+
+def test_counter_bytes_are_the_headers():
+    header = open(os.path.join(ROOT, "include", "moe_ffn.h")).read()
+    assert int(re.search(r"#define MOE_KV_COUNTER_BYTES (\d+)", header).group(1)) == B.KV_COUNTER_BYTES
+    cache = make()
+    assert B.moe_kv_attention_workspace_bytes(cache.dims, 4, 1, 1, 1, 64, 0) >= B.KV_COUNTER_BYTES
+
+
+def test_captured_calls_have_workspaces_of_their_own(calls, monkeypatch):
+    """None is the stream's, none is kept for a later call, and each starts with its counters zero."""
+    cache = make()
+    attend(cache, 64)
+    warm = ws_of(calls.calls[-1])
+    held, zero = [], []
+
+    def keep(name, args):
+        held.append(args)
+        zero.append(ctypes.string_at(args[14], B.KV_COUNTER_BYTES).count(0) == B.KV_COUNTER_BYTES)
+        return 0
+
+    monkeypatch.setattr(kv_cache, "_capturing", lambda: True, raising=False)
+    monkeypatch.setattr(calls, "moe_kv_attention", lambda *args: keep("moe_kv_attention", args))
+    attend(cache, 64)
+    attend(cache, 64)
+    assert all(args[14] != warm[0] for args in held) and all(zero)
+    monkeypatch.setattr(kv_cache, "_capturing", lambda: False, raising=False)
+    attend(cache, 64)
+    assert held[-1][14] == warm[0]                     # the stream's own again
+
+    cold = make()
+    monkeypatch.setattr(kv_cache, "_capturing", lambda: True, raising=False)
+    attend(cold, 64)
+    assert not cold._ws                                # the first call of a stream, captured: nothing to hand on
