@@ -331,6 +331,9 @@ MOE_API int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const m
  *          of any sizes may use one buffer in turn; nothing else is kept from
  *          call to call); calls that share it must not overlap on the GPU, and
  *          a captured graph uses it at every replay
+ *          (about 5 MB of parts, 25 where many rows may be few for the card; with
+ *          weights and up to 8 rows of a kv head 4 bytes for each row of q, head and token of max_len,
+ *          with more rows 2 D bytes for each row and head)
  * A query that sees nothing (an empty sequence, or more queries than tokens)
  * gives out 0 and lse -inf; a query row that holds a NaN or an infinity gives
  * NaN.  Rows of q outside every sequence are neither read nor written.

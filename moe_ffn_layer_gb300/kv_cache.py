@@ -116,7 +116,9 @@ class KVCache8:
         captured = _capturing()
         ws = None if captured else self._ws.get(key)
         if ws is None or ws.numel() < need:
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            # (a stream's own has some to spare: decoding with weights asks for more every 32 tokens)
+            spare = 0 if captured else min(need // 4, 64 << 20)
+            ws = torch.empty(max(need + spare, 256), dtype=torch.uint8, device=self.device)
             ws[:B.KV_COUNTER_BYTES].zero_()
             if not captured:
                 self._ws[key] = ws

@@ -90,3 +90,20 @@ def test_captured_calls_have_workspaces_of_their_own(calls, monkeypatch):
     monkeypatch.setattr(kv_cache, "_capturing", lambda: True, raising=False)
     attend(cold, 64)
     assert not cold._ws                                # the first call of a stream, captured: nothing to hand on
+
+
+def test_a_growing_length_seldom_allocates(calls):
+    """A decode loop with weights, max_len one more each step: the workspace holds scores by max_len."""
+    cache = make(Hkv=8, D=128, P=64)
+    w = torch.zeros(2, 8, 5000)
+    for L in range(1, 4001):
+        attend(cache, L, Hq=32, B_=2, weights=w)
+        assert ws_of(calls.calls[-1])[1] >= B.moe_kv_attention_workspace_bytes(cache.dims, 32, 2, 2, 1, L, 1)
+    given = [ws_of(c) for c in calls.calls]
+    assert sum(a != b for a, b in zip(given, given[1:])) <= 3      # the parts' fixed 5 MB cover most of the growth
+    big = torch.zeros(2, 8, 1 << 20)
+    del calls.calls[:]
+    for L in range(100_000, 110_000, 10):
+        attend(cache, L, Hq=32, B_=2, weights=big)
+    given = [ws_of(c) for c in calls.calls]
+    assert sum(a != b for a, b in zip(given, given[1:])) <= 1
