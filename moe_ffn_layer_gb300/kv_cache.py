@@ -156,9 +156,10 @@ class KVCache8:
             if not _is(weights, torch.float32, dev, (n, self.kv_heads, w_stride)):
                 _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
         sizes = (Hq, n, T, max_q, max_len, weights is not None)
-        if self._need[0] != sizes:
-            self._need = (sizes, B.moe_kv_attention_workspace_bytes(self.dims, *sizes))
-        ws = self.workspace(self._need[1], stream)
+        need = self._need   # (read once: another thread's call may put other sizes there)
+        if need[0] != sizes:
+            need = self._need = (sizes, B.moe_kv_attention_workspace_bytes(self.dims, *sizes))
+        ws = self.workspace(need[1], stream)
         _call("moe_kv_attention", B.lib().moe_kv_attention(
             self._dims, self._pool, ctypes.byref(seqs), q.data_ptr(), q.stride(0) if T > 1 else Hq * D, Hq,
             cu_q.data_ptr(), T, max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),

@@ -107,3 +107,20 @@ def test_a_growing_length_seldom_allocates(calls):
         attend(cache, L, Hq=32, B_=2, weights=big)
     given = [ws_of(c) for c in calls.calls]
     assert sum(a != b for a, b in zip(given, given[1:])) <= 1
+
+
+def test_calls_of_other_sizes_from_another_thread_in_between(calls):
+    """Whatever another thread's call leaves in the cache between this call's steps, its workspace is its own size's."""
+
+    class Interrupted(KVCache8):
+        @property
+        def _need(self):
+            return (None, 0)
+
+        @_need.setter
+        def _need(self, value):
+            pass                                       # another thread's sizes, smaller ones, take its place at once
+
+    cache = Interrupted(8, 2, 64, 16, device="cpu")
+    attend(cache, 64)
+    assert ws_of(calls.calls[-1])[1] >= B.moe_kv_attention_workspace_bytes(cache.dims, 4, 1, 1, 1, 64, 0)
