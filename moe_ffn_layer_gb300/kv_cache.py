@@ -178,6 +178,8 @@ class KVCache8:
         dst = self if dst is None else dst
         if dst._shape != self._shape:
             raise ValueError(f"dst holds pages of {dst._shape}, not {self._shape}")
+        if dst._dev != self._dev:
+            raise ValueError(f"dst: want pools on {self.device}, got {dst.device}")
         n, width = self._want_table(page_table, seq_lens, None, "")
         w_stride, dst_width = weights.shape[-1], dst_table.shape[-1]
         if not (_is(weights, torch.float32, self._dev, (n, self.kv_heads, w_stride)) and

@@ -124,3 +124,15 @@ def test_calls_of_other_sizes_from_another_thread_in_between(calls):
     cache = Interrupted(8, 2, 64, 16, device="cpu")
     attend(cache, 64)
     assert ws_of(calls.calls[-1])[1] >= B.moe_kv_attention_workspace_bytes(cache.dims, 4, 1, 1, 1, 64, 0)
+
+
+def test_evict_refuses_a_destination_on_another_device(calls):
+    cache, dst = make(), make()
+    args = (torch.zeros(1, 2, 16), torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32), 16, 4, 0, 0,
+            torch.zeros(1, 1, dtype=torch.int32))
+    cache.evict(*args, dst=dst)
+    assert len(calls.calls) == 1
+    dst.device, dst._dev = torch.device("cuda", 1), 1
+    with pytest.raises(ValueError, match="dst"):
+        cache.evict(*args, dst=dst)
+    assert len(calls.calls) == 1
