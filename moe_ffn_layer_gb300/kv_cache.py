@@ -8,6 +8,7 @@ sequence is the caller's: ``page_table`` int32 [B, width] and ``seq_lens`` int32
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -27,6 +28,8 @@ def _current(device_index: int) -> int:
 
 
 _capturing = torch.cuda.is_current_stream_capturing
+_device = torch.cuda.current_device
+_as_it_is = contextlib.nullcontext()
 
 
 def _call(name: str, rc: int) -> None:
@@ -68,6 +71,10 @@ class KVCache8:
         self._need = (None, 0)   # the last call's sizes and the workspace bytes they need
         self._ws = {}   # by stream: calls of different streams may overlap, and replays of graphs with any
 
+    def _here(self):
+        """The context of a call: the library works on the current device, which has to be the cache's."""
+        return _as_it_is if _device() == self._dev else torch.cuda.device(self._dev)
+
     def _want_table(self, page_table, seq_lens, cu, cu_name):
         """Checks the sequences' tensors; returns the table's rows and width."""
         n, width = page_table.shape
@@ -97,9 +104,10 @@ class KVCache8:
             raise ValueError(f"k and v rows lie {stride} and {v.stride(0)} elements apart")
         n, width = self._want_table(page_table, seq_lens, cu_new, "cu_new")
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, min(width * self.page, 1 << 30))
-        _call("moe_kv_append", B.lib().moe_kv_append(
-            self._dims, self._pool, ctypes.byref(seqs), k.data_ptr(), v.data_ptr(), stride, cu_new.data_ptr(), T,
-            _current(self._dev) if stream is None else B.handle(stream)))
+        with self._here():
+            _call("moe_kv_append", B.lib().moe_kv_append(
+                self._dims, self._pool, ctypes.byref(seqs), k.data_ptr(), v.data_ptr(), stride, cu_new.data_ptr(), T,
+                _current(self._dev) if stream is None else B.handle(stream)))
 
     def workspace(self, need: int, stream=None) -> torch.Tensor:
         """A workspace of at least `need` bytes for one call on `stream`
@@ -159,12 +167,13 @@ class KVCache8:
         need = self._need   # (read once: another thread's call may put other sizes there)
         if need[0] != sizes:
             need = self._need = (sizes, B.moe_kv_attention_workspace_bytes(self.dims, *sizes))
-        ws = self.workspace(need[1], stream)
-        _call("moe_kv_attention", B.lib().moe_kv_attention(
-            self._dims, self._pool, ctypes.byref(seqs), q.data_ptr(), q.stride(0) if T > 1 else Hq * D, Hq,
-            cu_q.data_ptr(), T, max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), None if weights is None else weights.data_ptr(), w_stride,
-            ws.data_ptr(), ws.numel(), _current(dev) if stream is None else B.handle(stream)))
+        with self._here():
+            ws = self.workspace(need[1], stream)
+            _call("moe_kv_attention", B.lib().moe_kv_attention(
+                self._dims, self._pool, ctypes.byref(seqs), q.data_ptr(), q.stride(0) if T > 1 else Hq * D, Hq,
+                cu_q.data_ptr(), T, max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
+                None if lse is None else lse.data_ptr(), None if weights is None else weights.data_ptr(), w_stride,
+                ws.data_ptr(), ws.numel(), _current(dev) if stream is None else B.handle(stream)))
         return out
 
     def evict(self, weights: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int, budget: int,
@@ -192,10 +201,11 @@ class KVCache8:
             with torch.cuda.stream(stream):
                 made = self._evict_outputs(n, budget)
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, max_len)
-        _call("moe_kv_evict", B.lib().moe_kv_evict(
-            self._dims, self._pool, ctypes.byref(seqs), weights.data_ptr(), w_stride, budget, sink, recent, dst._pool,
-            dst_table.data_ptr(), dst_width, made[0].data_ptr(), made[1].data_ptr(), made[2].data_ptr(),
-            _current(self._dev) if stream is None else B.handle(stream)))
+        with self._here():
+            _call("moe_kv_evict", B.lib().moe_kv_evict(
+                self._dims, self._pool, ctypes.byref(seqs), weights.data_ptr(), w_stride, budget, sink, recent, dst._pool,
+                dst_table.data_ptr(), dst_width, made[0].data_ptr(), made[1].data_ptr(), made[2].data_ptr(),
+                _current(self._dev) if stream is None else B.handle(stream)))
         return made
 
     def _evict_outputs(self, n, budget):

@@ -19,14 +19,22 @@ class Recorder:
     """Stands in for the library: the size query is the library's own, the launches are kept."""
 
     def __init__(self, real):
-        self.calls = []
+        self.calls, self.at = [], []                   # and the device that each was called on
+        self.device = -1                               # the current one; the caches' is a CPU tensor's, -1
         self.moe_kv_attention_workspace_bytes = real.moe_kv_attention_workspace_bytes
         for name in ("moe_kv_append", "moe_kv_attention", "moe_kv_evict"):
             setattr(self, name, lambda *args, name=name: self.keep(name, args))
 
     def keep(self, name, args):
         self.calls.append((name, args))
+        self.at.append(self.device)
         return 0
+
+    @contextlib.contextmanager
+    def on(self, device):
+        was, self.device = self.device, device
+        yield
+        self.device = was
 
 
 @pytest.fixture
@@ -37,6 +45,8 @@ def calls(monkeypatch):
     monkeypatch.setattr(B, "_lib", rec)
     monkeypatch.setattr(kv_cache, "_current", lambda device: 0)
     monkeypatch.setattr(kv_cache, "_capturing", lambda: False, raising=False)
+    monkeypatch.setattr(kv_cache, "_device", lambda: rec.device, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", rec.on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
     monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
     return rec
@@ -136,3 +146,17 @@ def test_evict_refuses_a_destination_on_another_device(calls):
     with pytest.raises(ValueError, match="dst"):
         cache.evict(*args, dst=dst)
     assert len(calls.calls) == 1
+
+
+@pytest.mark.parametrize("device", [-1, 0, 3])
+def test_calls_are_made_on_the_caches_device(calls, device):
+    """Whatever device is current; it is current again afterwards."""
+    cache = make()
+    calls.device = device
+    new = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    table, one = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    cache.append(new, new, table, one, torch.arange(2, dtype=torch.int32))
+    attend(cache, 16)
+    cache.evict(torch.zeros(1, 2, 16), table, one, 16, 4, 0, 0, table)
+    assert [name for name, _ in calls.calls] == ["moe_kv_append", "moe_kv_attention", "moe_kv_evict"]
+    assert calls.at == [-1, -1, -1] and calls.device == device
