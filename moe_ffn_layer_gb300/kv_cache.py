@@ -75,6 +75,10 @@ class KVCache8:
         """The context of a call: the library works on the current device, which has to be the cache's."""
         return _as_it_is if _device() == self._dev else torch.cuda.device(self._dev)
 
+    def _on(self, stream):
+        """The context of what a call on `stream` (torch's, or a handle) allocates."""
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream)
+
     def _want_table(self, page_table, seq_lens, cu, cu_name):
         """Checks the sequences' tensors; returns the table's rows and width."""
         n, width = page_table.shape
@@ -116,7 +120,7 @@ class KVCache8:
         allocated and its counters zeroed in the capture: its memory is the
         graph's, whatever later calls need or other graphs are replayed."""
         if stream is not None:
-            with torch.cuda.stream(stream):
+            with self._on(stream):
                 return self._workspace(need, B.handle(stream))
         return self._workspace(need, _current(self._dev))
 
@@ -152,7 +156,7 @@ class KVCache8:
             if stream is None:
                 out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
             else:
-                with torch.cuda.stream(stream):
+                with self._on(stream):
                     out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         if not _is(out, torch.bfloat16, dev, shape):
             _want("out", out, torch.bfloat16, 3, self.device, shape)
@@ -198,7 +202,7 @@ class KVCache8:
         if stream is None:
             made = self._evict_outputs(n, budget)
         else:
-            with torch.cuda.stream(stream):
+            with self._on(stream):
                 made = self._evict_outputs(n, budget)
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, max_len)
         with self._here():

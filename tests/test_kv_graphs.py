@@ -130,3 +130,14 @@ def test_several_calls_and_streams_of_one_capture():
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[1]) and torch.equal(outs[1], want[3]) and torch.equal(outs[2], want[1])
     assert torch.equal(w, once + once) and torch.equal(w2, w) and status() == 0
+
+
+def test_stream_given_by_handle():
+    c, side = Calls(), new_stream()
+    want, w = c(3, c.out(3)), torch.rand_like(c.w)
+    dst, to = i32([[0, 1]]), upload(make_pool(np.random.default_rng(1), 2, 2, 64, 128))
+    torch.cuda.synchronize()
+    got = c.cache.attend(c.q[:3], c.table, c.lens, c.cu[3], 3, c.L, stream=side.cuda_stream)
+    lens, _, kept = c.cache.evict(w, c.table, c.lens, c.L, 100, 4, 16, dst, dst=to, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got, want) and int(lens) == 100 and bool((kept >= 0).all()) and status() == 0

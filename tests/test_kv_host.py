@@ -3,6 +3,7 @@ import contextlib
 import ctypes
 import os
 import re
+import types
 
 import pytest
 import torch
@@ -19,6 +20,7 @@ class Recorder:
     """Stands in for the library: the size query is the library's own, the launches are kept."""
 
     def __init__(self, real):
+        self.entered = []
         self.calls, self.at = [], []                   # and the device that each was called on
         self.device = -1                               # the current one; the caches' is a CPU tensor's, -1
         self.moe_kv_attention_workspace_bytes = real.moe_kv_attention_workspace_bytes
@@ -29,6 +31,10 @@ class Recorder:
         self.calls.append((name, args))
         self.at.append(self.device)
         return 0
+
+    def on_stream(self, stream):
+        self.entered.append(stream.cuda_stream)        # as torch does: a stream object, no handle
+        return contextlib.nullcontext()
 
     @contextlib.contextmanager
     def on(self, device):
@@ -48,7 +54,8 @@ def calls(monkeypatch):
     monkeypatch.setattr(kv_cache, "_device", lambda: rec.device, raising=False)
     monkeypatch.setattr(torch.cuda, "device", rec.on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
-    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "stream", rec.on_stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: types.SimpleNamespace(cuda_stream=handle))
     return rec
 
 
@@ -160,3 +167,14 @@ def test_calls_are_made_on_the_caches_device(calls, device):
     cache.evict(torch.zeros(1, 2, 16), table, one, 16, 4, 0, 0, table)
     assert [name for name, _ in calls.calls] == ["moe_kv_append", "moe_kv_attention", "moe_kv_evict"]
     assert calls.at == [-1, -1, -1] and calls.device == device
+
+
+@pytest.mark.parametrize("stream", [77, types.SimpleNamespace(cuda_stream=77)])
+def test_streams_are_given_as_objects_or_handles(calls, stream):
+    """What a call allocates is allocated on its stream, however that is named."""
+    cache = make()
+    attend(cache, 16, stream=stream)
+    table, one = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    cache.evict(torch.zeros(1, 2, 16), table, one, 16, 4, 0, 0, table, stream=stream)
+    assert [args[-1] for _, args in calls.calls] == [77, 77]
+    assert calls.entered == [77, 77, 77] and list(cache._ws) == [77]   # out, the workspace, the eviction's outputs
