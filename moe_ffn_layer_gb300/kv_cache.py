@@ -8,7 +8,6 @@ sequence is the caller's: ``page_table`` int32 [B, width] and ``seq_lens`` int32
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -27,9 +26,8 @@ def _current(device_index: int) -> int:
     return torch.cuda.current_stream(device_index).cuda_stream
 
 
-_capturing = torch.cuda.is_current_stream_capturing
-_device = torch.cuda.current_device
-_as_it_is = contextlib.nullcontext()
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name: str, rc: int) -> None:
@@ -71,10 +69,6 @@ class KVCache8:
         self._need = (None, 0)   # the last call's sizes and the workspace bytes they need
         self._ws = {}   # by stream: calls of different streams may overlap, and replays of graphs with any
 
-    def _here(self):
-        """The context of a call: the library works on the current device, which has to be the cache's."""
-        return _as_it_is if _device() == self._dev else torch.cuda.device(self._dev)
-
     def _on(self, stream):
         """The context of what a call on `stream` (torch's, or a handle) allocates."""
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, self.device) if isinstance(stream, int) else stream)
@@ -108,10 +102,12 @@ class KVCache8:
             raise ValueError(f"k and v rows lie {stride} and {v.stride(0)} elements apart")
         n, width = self._want_table(page_table, seq_lens, cu_new, "cu_new")
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, min(width * self.page, 1 << 30))
-        with self._here():
-            _call("moe_kv_append", B.lib().moe_kv_append(
-                self._dims, self._pool, ctypes.byref(seqs), k.data_ptr(), v.data_ptr(), stride, cu_new.data_ptr(), T,
-                _current(self._dev) if stream is None else B.handle(stream)))
+        if _device() != self._dev:   # (the library works on the current device)
+            with torch.cuda.device(self._dev):
+                return self.append(k, v, page_table, seq_lens, cu_new, stream)
+        _call("moe_kv_append", B.lib().moe_kv_append(
+            self._dims, self._pool, ctypes.byref(seqs), k.data_ptr(), v.data_ptr(), stride, cu_new.data_ptr(), T,
+            _current(self._dev) if stream is None else B.handle(stream)))
 
     def workspace(self, need: int, stream=None) -> torch.Tensor:
         """A workspace of at least `need` bytes for one call on `stream`
@@ -167,17 +163,20 @@ class KVCache8:
             w_stride = weights.shape[-1]
             if not _is(weights, torch.float32, dev, (n, self.kv_heads, w_stride)):
                 _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
+        if _device() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self.attend(q, page_table, seq_lens, cu_q, max_q, max_len, scale, weights, out, lse, stream)
         sizes = (Hq, n, T, max_q, max_len, weights is not None)
         need = self._need   # (read once: another thread's call may put other sizes there)
         if need[0] != sizes:
             need = self._need = (sizes, B.moe_kv_attention_workspace_bytes(self.dims, *sizes))
-        with self._here():
-            ws = self.workspace(need[1], stream)
-            _call("moe_kv_attention", B.lib().moe_kv_attention(
-                self._dims, self._pool, ctypes.byref(seqs), q.data_ptr(), q.stride(0) if T > 1 else Hq * D, Hq,
-                cu_q.data_ptr(), T, max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
-                None if lse is None else lse.data_ptr(), None if weights is None else weights.data_ptr(), w_stride,
-                ws.data_ptr(), ws.numel(), _current(dev) if stream is None else B.handle(stream)))
+        handle = _current(dev) if stream is None else B.handle(stream)
+        ws = self._workspace(need[1], handle) if stream is None else self.workspace(need[1], stream)
+        _call("moe_kv_attention", B.lib().moe_kv_attention(
+            self._dims, self._pool, ctypes.byref(seqs), q.data_ptr(), q.stride(0) if T > 1 else Hq * D, Hq,
+            cu_q.data_ptr(), T, max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), None if weights is None else weights.data_ptr(), w_stride,
+            ws.data_ptr(), ws.numel(), handle))
         return out
 
     def evict(self, weights: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, max_len: int, budget: int,
@@ -199,17 +198,19 @@ class KVCache8:
                 _is(dst_table, torch.int32, self._dev, (n, dst_width))):
             _want("weights", weights, torch.float32, 3, self.device, (n, self.kv_heads, w_stride))
             _want("dst_table", dst_table, torch.int32, 2, self.device, (n, dst_width))
+        if _device() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self.evict(weights, page_table, seq_lens, max_len, budget, sink, recent, dst_table, dst, stream)
         if stream is None:
             made = self._evict_outputs(n, budget)
         else:
             with self._on(stream):
                 made = self._evict_outputs(n, budget)
         seqs = B.moe_kv_seqs(page_table.data_ptr(), seq_lens.data_ptr(), n, width, max_len)
-        with self._here():
-            _call("moe_kv_evict", B.lib().moe_kv_evict(
-                self._dims, self._pool, ctypes.byref(seqs), weights.data_ptr(), w_stride, budget, sink, recent, dst._pool,
-                dst_table.data_ptr(), dst_width, made[0].data_ptr(), made[1].data_ptr(), made[2].data_ptr(),
-                _current(self._dev) if stream is None else B.handle(stream)))
+        _call("moe_kv_evict", B.lib().moe_kv_evict(
+            self._dims, self._pool, ctypes.byref(seqs), weights.data_ptr(), w_stride, budget, sink, recent, dst._pool,
+            dst_table.data_ptr(), dst_width, made[0].data_ptr(), made[1].data_ptr(), made[2].data_ptr(),
+            _current(self._dev) if stream is None else B.handle(stream)))
         return made
 
     def _evict_outputs(self, n, budget):
