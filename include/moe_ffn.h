@@ -338,8 +338,8 @@ MOE_API int moe_kv_append(const moe_kv_dims* d, const moe_kv_pool* pool, const m
  * gives out 0 and lse -inf; a query row that holds a NaN or an infinity gives
  * NaN.  Rows of q outside every sequence are neither read nor written.
  * Sums, maxima and outputs are held in fp32; the products' operands are exact
- * (q, K, V) or keep 16 bits (the softmax weights, at any size).  Results do not
- * depend on scheduling. */
+ * (q, K, V) or keep 16 bits (the softmax weights times V's scale, where that is
+ * 2^-117 at least).  Results do not depend on scheduling. */
 #define MOE_KV_COUNTER_BYTES 18432
 MOE_API size_t moe_kv_attention_workspace_bytes(const moe_kv_dims* d, int Hq, int B, int T_q, int max_q,
                                                 int max_len, int weights);
@@ -362,7 +362,9 @@ MOE_API int moe_kv_attention(const moe_kv_dims* d, const moe_kv_pool* pool, cons
  *  kept        int32 [B][Hkv][budget] (out): their positions, then -1
  * A destination page's scale is the largest of its rows' scales; a row from a
  * page of another scale becomes e4m3(code * (scale / scale')).  Slots beyond
- * dst_lens are not written. */
+ * dst_lens are not written.  A sequence that fails its checks keeps nothing
+ * (dst_lens 0); a kept row whose source page fails is stored as zeros, and a
+ * destination page that fails is not written. */
 MOE_API int moe_kv_evict(const moe_kv_dims* d, const moe_kv_pool* src, const moe_kv_seqs* s, const float* weights,
                          int64_t w_stride, int budget, int sink, int recent, const moe_kv_pool* dst,
                          const int32_t* dst_table, int dst_width, int32_t* dst_lens, float* dst_weights, int32_t* kept,

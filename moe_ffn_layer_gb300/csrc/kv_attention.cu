@@ -18,9 +18,11 @@
 //  - output: bf16, which has fp32's range.  A V code becomes bf16 exactly; a
 //    weight p * vs enters as two bf16 terms, so that it keeps 16 bits however
 //    far it lies below the row's largest (a long sequence's many small weights
-//    count as they should, whatever the pages' scales).
-// Any code byte reads as a finite value, so what lies beyond a sequence's end
-// never turns a masked product into a NaN.
+//    count as they should, whatever the pages' scales).  Below 2^-117, and so
+//    with V scales near fp32's least, bf16's own floor of 2^-133 takes bits.
+// What lies beyond a sequence's end is loaded as zeros, scores are masked by
+// being replaced, and V's conversion reads any code byte as a finite value: no
+// slot that a row does not see turns its result into a NaN.
 #include <limits.h>
 
 #include <algorithm>
@@ -204,8 +206,6 @@ struct Tile {
     seen = max(len - n + last / g + 1, 0);
     return true;
   }
-  // tokens that row r sees (rows beyond the last real one see what it sees)
-  __device__ __forceinline__ int sees(int r, int g) const { return max(len - n + min(r, rows - 1) / g + 1, 0); }
 };
 
 // One warp's ring of 32-token steps in shared memory.  A step is two halves of
@@ -535,8 +535,8 @@ template <int R>
 constexpr int ring_stages() { return R == 1 ? 3 : 2; }
 
 // Bound: HBM (2 D bytes per token and kv head, read once), behind it instruction
-// issue (about 900 instructions a warp for 32 tokens, 256 of them V's codes to
-// bf16): 64 sequences of 513 to 16384 tokens, 8 kv heads of 128: 206 us, 5.4 TB/s;
+// issue (V's codes to bf16 are 64 pairs of four instructions each for 32 tokens
+// of a warp): 64 sequences of 513 to 16384 tokens, 8 kv heads of 128: 206 us, 5.4 TB/s;
 // one of 131071: 59 us, 4.5 TB/s.  16-row tiles (drafted tokens, two tiles of 16
 // sequences) are bound by issue, 56 us for 68 MB.  Each of a CTA's
 // four warps takes a quarter of every 128-token span, with a ring of
@@ -842,7 +842,7 @@ template <int D>
 __global__ void __launch_bounds__(kGainWarps * 32) kv_gain_kernel(KvDims d, KvPool pool, KvSeqs s, KvAttention at,
                                                                   Laid laid, GainParts gp, int* status) {
   __shared__ int last;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float half[8][32];
   GainStage<D>* ring = reinterpret_cast<GainStage<D>*>(smem);
   chain_wait();

@@ -182,11 +182,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 // index order writes the kept indices, so the result does not depend on
 // scheduling.  The weights are read five times; where the longest sequence's fit
 // (kStaged), the first pass leaves them in shared memory.  Latency of its passes:
-// 31 us for 256 (sequence, head) pairs of up to 16384.
-// 192 KB.  With and without, selection and gathering, us: 32 sequences of 16384 120
-// and 126, of 32768 (one CTA an SM) 151 and 154, of 49152 179 and 181; one of 16384
-// 21 and 23, of 32768 32 and 34, of 49152 43 and 47.
-constexpr int kMostStaged = 49152;
+// 31 us for 256 (sequence, head) pairs of up to 16384.  With and without staging,
+// selection and gathering, us: 32 sequences of 16384 120 and 126, of 32768 (one CTA
+// an SM) 151 and 154, of 49152 179 and 181; one of 16384 21 and 23, of 32768 32 and
+// 34, of 49152 43 and 47.
+constexpr int kMostStaged = 49152;   // 192 KB
 template <bool kStaged>
 __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(KvDims d, KvSeqs s, KvEvict e, int* status) {
   extern __shared__ float staged[];

@@ -8,7 +8,8 @@ from __future__ import annotations
 
 import numpy as np
 
-# the value of each e4m3 code; the NaN codes 0x7f and 0xff as the library reads them, +-480
+# the value of each e4m3 code; the NaN codes 0x7f and 0xff, which the cache never holds, as V's conversion and the
+# rescaling of codes read them, +-480
 VALUE = np.array([(-1.0 if c & 0x80 else 1.0) *
                   ((c & 7) * 2.0 ** -9 if not c & 0x78 else (1 + (c & 7) / 8) * 2.0 ** ((c >> 3 & 15) - 7))
                   for c in range(256)])
