@@ -535,9 +535,9 @@ template <int R>
 constexpr int ring_stages() { return R == 1 ? 3 : 2; }
 
 // Bound: HBM (2 D bytes per token and kv head, read once), behind it instruction
-// issue (V's codes to bf16 are 64 pairs of four instructions each for 32 tokens
-// of a warp): 64 sequences of 513 to 16384 tokens, 8 kv heads of 128: 206 us, 5.4 TB/s;
-// one of 131071: 59 us, 4.5 TB/s.  16-row tiles (drafted tokens, two tiles of 16
+// issue (727 instructions a warp for 32 tokens, 256 of them V's codes to bf16, 64
+// pairs of four): 64 sequences of 513 to 16384 tokens, 8 kv heads of 128: 207 us, 5.4 TB/s;
+// one of 131071: 60 us, 4.5 TB/s.  16-row tiles (drafted tokens, two tiles of 16
 // sequences) are bound by issue, 56 us for 68 MB.  Each of a CTA's
 // four warps takes a quarter of every 128-token span, with a ring of
 // asynchronous copies and a running softmax of its own; the ring runs on

@@ -17,9 +17,9 @@
 // a softmax ends, and neither it nor the MMAs wait for each other's last piece.
 //
 // Bound: instruction issue of the softmax and the converters, in step with the
-// MMAs.  One prompt of 8192 (32 heads of 128, 8 kv heads): 785 us, 0.70 PFLOP/s of
+// MMAs.  One prompt of 8192 (32 heads of 128, 8 kv heads): 784 us, 0.70 PFLOP/s of
 // the definition's operations, where the two-term weights alone cost half as many
-// MMAs again; the tensor pipe is active 43% of the time, the issue slots 56%.
+// MMAs again; the tensor pipe is active 43% of the time, the issue slots 55%.
 // What got it there from 1097 us (all same prompt): MMA operands in uniform
 // registers and waits tested inline (the MMA warp's own instructions between two
 // waits were the longest chain), 64-token steps with two S buffers, the running
