@@ -370,6 +370,63 @@ MOE_API int moe_kv_evict(const moe_kv_dims* d, const moe_kv_pool* src, const moe
                          const int32_t* dst_table, int dst_width, int32_t* dst_lens, float* dst_weights, int32_t* kept,
                          cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Projections in 8 bits: the dense matmuls around the attention and the layer
+ * (the w8a8_dynamic configuration of the xLLM PR "FlashComm1 +
+ * matmul-reduce-scatter", configuration section: weights in 8 bits, activations
+ * quantised as they are made).
+ *
+ * A matrix in 8 bits is e4m3 codes [rows][K], row-major, `ld` bytes apart, and
+ * exponent bytes [..][ceil(K / 128)], row-major, `lds` apart: byte b stands for
+ * the scale 2^(b - 127), and 255 for NaN.  A row of activations has one scale per
+ * 128 values; weights have one per block of 128 rows x 128 values.  Blocks at the
+ * ends are smaller where the sizes are not multiples of 128.
+ * The calls below store scale = the least power of two with max|x| <= 448 scale
+ * over the block's finite values, 2^-126 at least, and code = e4m3(x / scale),
+ * to nearest even (one rounding of the fp32 value); an infinity or a NaN
+ * becomes the NaN code 0x7f.
+ * Supported: K % 16 == 0; codes 16-byte aligned, ld % 16 == 0; scales 4-byte
+ * aligned, lds % 4 == 0 (bytes of a row beyond ceil(K / 128) may be read, never
+ * used or written).  bf16 rows are 16-byte aligned, strides multiples of 8. */
+
+/* RMS norm of rows, with the residual's addition:
+ *   h[t] = bf16(x[t] + residual[t])  (residual NULL: h = x, and no h is stored)
+ *   y[t] = h[t] * rsqrt(mean(h[t]^2) + eps) * weight   in fp32, mean over the H values
+ *  x, residual, h, y  bf16 rows, *_stride elements apart
+ *  weight  bf16 [H], or NULL for ones;  eps >= 0
+ *  h       NULL if and only if residual is; may be x or residual (same pointer
+ *          and stride); no other operands may overlap
+ *  y       bf16(y), or NULL;  codes, scales: y in 8 bits, or both NULL; one of
+ *          the two forms at least
+ * A row that holds a NaN gives NaN; one whose sum of squares passes the fp32
+ * range gives zeros, and NaN where it holds an infinity.  Supported: H <= 65536. */
+MOE_API int moe_rms_norm8(const void* x, int64_t x_stride, const void* residual, int64_t r_stride, const void* weight,
+                          float eps, int T, int H, void* h, int64_t h_stride, void* y, int64_t y_stride, void* codes,
+                          int64_t ld, void* scales, int64_t lds, cudaStream_t stream);
+
+/* Rows in 8 bits.
+ *   act == 0: of x[t][0..K-1]
+ *   act == 1: of SiLU(x[t][0..K-1]) * x[t][K..2K-1], computed in fp32
+ *  x bf16 [T], rows x_stride elements apart; must not overlap codes or scales */
+MOE_API int moe_quantize8(const void* x, int64_t x_stride, int T, int K, int act, void* codes, int64_t ld, void* scales,
+                          int64_t lds, cudaStream_t stream);
+
+/* A weight bf16 [N][K] (rows w_stride elements apart) in 8 bits, in blocks of
+ * 128 x 128.  Supported: N <= 8388480. */
+MOE_API int moe_quantize8_weight(const void* w, int64_t w_stride, int N, int K, void* codes, int64_t ld, void* scales,
+                                 int64_t lds, cudaStream_t stream);
+
+/* out[t][n] = bf16( sum_k A[t][k] W[n][k] ), A and W in 8 bits:
+ *  a [T][K] with a scale per row and 128 values (las bytes between its rows)
+ *  w [N][K] with a scale per 128 x 128 (lws bytes between its rows)
+ *  out bf16, rows out_stride elements apart; any N
+ * Products are exact and summed in fp32; a NaN code or scale makes what it
+ * reaches NaN.  a, w and out must be device memory of the current device.
+ * Results do not depend on scheduling. */
+MOE_API int moe_linear8(const void* a, int64_t lda, const void* a_scales, int64_t las, const void* w, int64_t ldw,
+                        const void* w_scales, int64_t lws, int T, int N, int K, void* out, int64_t out_stride,
+                        cudaStream_t stream);
+
 /* Reads and clears the current device's status word (first device-side error
  * since the last read, MOE_OK if none).  Synchronises `stream`. */
 MOE_API int moe_last_device_error(cudaStream_t stream);

@@ -84,6 +84,10 @@ _SIGS = {
                               _P, _L, _P, _Z, _P]),
     "moe_kv_evict": (_I, [_R(moe_kv_dims), _R(moe_kv_pool), _R(moe_kv_seqs), _P, _L, _I, _I, _I, _R(moe_kv_pool), _P,
                           _I, _P, _P, _P, _P]),
+    "moe_rms_norm8": (_I, [_P, _L, _P, _L, _P, _F, _I, _I, _P, _L, _P, _L, _P, _L, _P, _L, _P]),
+    "moe_quantize8": (_I, [_P, _L, _I, _I, _I, _P, _L, _P, _L, _P]),
+    "moe_quantize8_weight": (_I, [_P, _L, _I, _I, _P, _L, _P, _L, _P]),
+    "moe_linear8": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _I, _I, _I, _P, _L, _P]),
     "moe_last_device_error": (_I, [_P]),
     "moe_last_launch_count": (_I, []),
     "moe_workspace_layout": (_I, [ctypes.POINTER(moe_dims), _I, ctypes.POINTER(moe_workspace_offsets)]),
@@ -232,6 +236,28 @@ def moe_kv_evict(dims: moe_kv_dims, src: moe_kv_pool, seqs: moe_kv_seqs, weights
                                                      ptr(weights), w_stride, budget, sink, recent,
                                                      ctypes.byref(dst), ptr(dst_table), dst_width, ptr(dst_lens),
                                                      ptr(dst_weights), ptr(kept), handle(stream)))
+
+
+def moe_rms_norm8(x, x_stride, residual, r_stride, weight, eps, T, H, h, h_stride, y, y_stride, codes, ld, scales, lds,
+                  stream) -> int:
+    return _check("moe_rms_norm8", lib().moe_rms_norm8(ptr(x), x_stride, ptr(residual), r_stride, ptr(weight), eps, T, H,
+                                                       ptr(h), h_stride, ptr(y), y_stride, ptr(codes), ld, ptr(scales),
+                                                       lds, handle(stream)))
+
+
+def moe_quantize8(x, x_stride, T, K, act, codes, ld, scales, lds, stream) -> int:
+    return _check("moe_quantize8", lib().moe_quantize8(ptr(x), x_stride, T, K, act, ptr(codes), ld, ptr(scales), lds,
+                                                       handle(stream)))
+
+
+def moe_quantize8_weight(w, w_stride, N, K, codes, ld, scales, lds, stream) -> int:
+    return _check("moe_quantize8_weight", lib().moe_quantize8_weight(ptr(w), w_stride, N, K, ptr(codes), ld, ptr(scales),
+                                                                     lds, handle(stream)))
+
+
+def moe_linear8(a, lda, a_scales, las, w, ldw, w_scales, lws, T, N, K, out, out_stride, stream) -> int:
+    return _check("moe_linear8", lib().moe_linear8(ptr(a), lda, ptr(a_scales), las, ptr(w), ldw, ptr(w_scales), lws, T,
+                                                   N, K, ptr(out), out_stride, handle(stream)))
 
 
 def moe_last_device_error(stream) -> int:

@@ -3,6 +3,7 @@
 // adds the number of kernels it launched to *launches.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -167,6 +168,52 @@ struct KvEvict {
 };
 int kv_evict_launch(const KvDims& d, const KvPool& src, const KvSeqs& s, const KvPool& dst, const KvEvict& e,
                     int* status, cudaStream_t stream, int* launches);
+
+// 8-bit projections: rows and weights of e4m3 codes with a power of two (its exponent byte) per block.
+struct Norm8 {
+  const void* x;
+  long long x_stride;
+  const void* r;   // null: no residual (and no h)
+  long long r_stride;
+  const void* w;   // null: ones
+  float eps;
+  int H;
+  void* h;
+  long long h_stride;
+  void* y;   // null: not wanted
+  long long y_stride;
+  uint8_t* codes;   // null: not wanted
+  long long ld;
+  uint8_t* scales;
+  long long lds;
+};
+int rms_norm8_launch(const Norm8& a, int T, cudaStream_t stream, int* launches);
+struct Quantize8 {
+  const void* x;
+  long long x_stride;
+  int K;
+  uint8_t* codes;
+  long long ld;
+  uint8_t* scales;
+  long long lds;
+};
+// act: SiLU(x[.., :K]) * x[.., K:2K]
+int quantize8_launch(const Quantize8& a, int T, int act, cudaStream_t stream, int* launches);
+int quantize8_weight_launch(const Quantize8& a, int N, cudaStream_t stream, int* launches);
+struct Linear8 {
+  const uint8_t* a;
+  long long lda;
+  const uint8_t* a_scales;
+  long long las;
+  const uint8_t* w;
+  long long ldw;
+  const uint8_t* w_scales;
+  long long lws;
+  int T, N, K;
+  __nv_bfloat16* out;
+  long long ldo;
+};
+int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches);
 
 // Status word and SM count of the current device (first use looks them up).
 int current_device_info(int** status, int* num_sms);

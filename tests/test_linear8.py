@@ -1,0 +1,374 @@
+"""The 8-bit projections on the GPU against float64.
+
+Tolerances, derived.  Quantising bf16 values is exact but for the one rounding,
+which the oracle makes as well: codes and scales are equal.  Where the value is
+computed in fp32 (the norm, SiLU * up), with a relative error of at most ERR, a
+code may fall to the other side of a rounding border: |value - exact| is then at
+most half a step of e4m3 (2^-4 of the value, or 2^-10 of the scale under the
+normal range) more than ERR of it; a scale may differ only where the block's
+largest lies within ERR of the border.  ERR: a sum of H squares in fp32 in at
+most 64 + 32 + 5 steps a thread and its tree (each 2^-24, under the square root
+half of it), the division, root and products: (0.5 * 101 + 6) * 2^-24 < 2^-18.
+The product's sums are in fp32: K / 32 additions of partial sums and 32 products
+to each, a step at most 2^-22 of the sum of magnitudes (a truncating adder that
+keeps 22 bits beside the largest), then bf16's half step 2^-8 of the result.
+"""
+import numpy as np
+import pytest
+import torch
+
+from moe_ffn_layer_gb300 import binding as B
+from moe_ffn_layer_gb300 import build as build_mod
+from moe_ffn_layer_gb300 import linear8 as L8
+from oracle import linear8_oracle as lo
+
+pytestmark = pytest.mark.gpu
+
+ERR = 2.0 ** -18
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build_mod.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    yield B.lib()
+    assert B.moe_last_device_error(torch.cuda.current_stream()) == 0
+
+
+def np64(t):
+    return t.double().cpu().numpy()
+
+
+def np8(t):
+    return t.cpu().numpy()
+
+
+def rows(T, K, gap=0, seed=0):
+    """bf16 rows `gap` elements apart, some channels and rows much larger, a block of zeros."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn(T, K + gap, generator=g, device="cuda")
+    x *= 1 + 31 * (torch.rand(K + gap, generator=g, device="cuda") < 0.02)
+    x *= torch.exp2(torch.randint(-20, 20, (T, 1), generator=g, device="cuda").float())
+    x[T // 2, :128] = 0
+    return x.bfloat16()[:, :K]
+
+
+def assert_near_codes(codes, scales, y, err=ERR):
+    """codes and scales stand for y [R, K] within half a step and err."""
+    want, s = lo.quantize(y)
+    codes, scales = np8(codes), np8(scales)
+    off = scales != s
+    if off.any():   # the block's largest lies at the border
+        i, j = np.nonzero(off)
+        top = np.array([np.abs(y[r, 128 * b:128 * b + 128]).max() for r, b in zip(i, j)])
+        border = 448 * 2.0 ** (np.minimum(scales, s)[off].astype(float) - 127)
+        assert (np.abs(top / border - 1) <= err).all()
+    unit = lo.spread(scales, 1, *y.shape)
+    got = lo.VALUES[codes] * unit
+    assert np.array_equal(np.isnan(got), ~np.isfinite(y))
+    fine = np.isfinite(y)
+    tol = np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * unit) + err * np.abs(y)
+    assert (np.abs(got - y)[fine] <= tol[fine]).all()
+    # the codes differ only where a rounding may fall either way: a border is at most 2^-4 of a value away
+    # from the next, so that 2 err / 2^-4 of the values lie within err of one (twice that, and a few, allowed)
+    same = fine & ~off.repeat(128, 1)[:, :y.shape[1]]
+    assert np.sum((codes != want)[same]) <= 4 + 64 * err * same.sum()
+
+
+# ---------------------------------------------------------------- quantising
+@pytest.mark.parametrize("T,K,gap", [(1, 16, 0), (1, 128, 8), (3, 144, 0), (7, 2048, 128), (257, 272, 24), (1021, 768, 0),
+                                     (64, 8208, 16), (5, 112, 0)])
+def test_quantize_rows_equal(T, K, gap):
+    x = rows(T, K, gap, T + K)
+    codes, scales = L8.quantize8(x)
+    want, s = lo.quantize(np64(x))
+    assert np.array_equal(np8(scales), s) and np.array_equal(np8(codes), want)
+
+
+@pytest.mark.parametrize("N,K,gap", [(1, 16, 0), (128, 128, 0), (129, 144, 8), (300, 2064, 0), (1000, 768, 40)])
+def test_quantize_weight_equal(N, K, gap):
+    w = rows(N, K, gap, N + K)
+    codes, scales = L8.quantize8_weight(w)
+    want, s = lo.quantize(np64(w), 128)
+    assert np.array_equal(np8(scales), s) and np.array_equal(np8(codes), want)
+
+
+def special_rows():
+    """Rows of one block each at the ends of bf16 and at the scales' borders."""
+    out = [torch.zeros(128)]
+    for e in (-133, -126, -118, -117, -30, 0, 100, 118, 119):
+        for top in (1.75, 1.7578125, 1.7421875):
+            r = torch.linspace(-1, 1, 128) * 2.0 ** e
+            r[17] = top * 2.0 ** e
+            out.append(r)
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        r = torch.linspace(-3, 3, 128)
+        r[5] = bad
+        out.append(r)
+        out.append(torch.full((128,), bad))
+    r = torch.full((128,), -0.0)
+    out.append(r)
+    return torch.stack(out).bfloat16().cuda()
+
+
+def test_quantize_special_values():
+    x = special_rows()
+    codes, scales = L8.quantize8(x)
+    want, s = lo.quantize(np64(x))
+    assert np.array_equal(np8(scales), s) and np.array_equal(np8(codes), want)
+    one = x.reshape(1, -1)
+    codes1, scales1 = L8.quantize8(one)   # and as the blocks of one row
+    assert torch.equal(codes1.view(-1), codes.view(-1)) and torch.equal(scales1.view(-1), scales.view(-1))
+    codes, scales = L8.quantize8_weight(x)   # one block for all
+    want, s = lo.quantize(np64(x), 128)
+    assert np.array_equal(np8(scales), s) and np.array_equal(np8(codes), want)
+
+
+@pytest.mark.parametrize("T,K,gap", [(1, 16, 0), (333, 768, 0), (9, 1040, 8), (130, 2048, 64)])
+def test_silu_mul(T, K, gap):
+    """exp and the quotient by the fast instructions: 2 + |gate| 2^-1 ulp and 2 ulp; gates here stay under 100."""
+    x = rows(T, 2 * K, gap, T + K).float().clamp(-100, 100).bfloat16()
+    codes, scales = L8.quantize8(x, silu_mul=True)
+    assert_near_codes(codes, scales, lo.silu_mul(np64(x)), err=64 * 2.0 ** -23)
+
+
+def test_silu_mul_far_gates():
+    """Gates whose exponential overflows give 0; an infinite gate or up gives what the formula gives."""
+    inf = float("inf")
+    gate = torch.tensor([-1e4, -90.0, 90.0, 1e4, inf, float("nan"), 3.0, 0.0] + [1.0] * 120)
+    up = torch.tensor([2.0, 2.0, 2.0, 2.0, 1.0, 1.0, inf, 5.0] + [1.0] * 120)
+    codes, scales = L8.quantize8(torch.cat([gate, up]).bfloat16().cuda()[None], silu_mul=True)
+    got = lo.values(np8(codes), np8(scales))[0]
+    assert got[0] == 0 and got[1] == 0 and got[7] == 0
+    assert np.isnan(got[4:7]).all() and abs(got[3] / 2e4 - 1) < 2.0 ** -4 + 2.0 ** -8
+
+
+# ---------------------------------------------------------------- the norm
+@pytest.mark.parametrize("T,H,gap,residual,weight,outputs", [
+    (1, 16, 0, True, True, "both"), (1, 2048, 0, True, True, "codes"), (3, 128, 8, False, False, "both"),
+    (7, 2064, 24, True, True, "both"), (300, 768, 0, True, False, "y"), (5, 4096, 128, False, True, "codes"),
+    (1030, 256, 0, True, True, "both"), (2, 8192, 0, True, True, "both"), (3, 16400, 0, True, True, "both"),
+    (2, 65536, 0, True, True, "codes"), (65, 112, 16, True, True, "both")])
+def test_norm(T, H, gap, residual, weight, outputs):
+    x = rows(T, H, gap, T + H)
+    r = rows(T, H, gap // 8 * 16, T + H + 1) if residual else None
+    w = (1 + 0.2 * torch.randn(H, device="cuda")).bfloat16() if weight else None
+    n = L8.rms_norm8(x, w, 1e-5, r, outputs)
+    h = x if r is None else (x.float() + r.float()).bfloat16()
+    assert n.h is None if r is None else torch.equal(n.h.view(torch.int16), h.view(torch.int16))
+    y = lo.rms_norm(np64(h), None if w is None else np64(w), 1e-5)
+    assert (n.y is None) == (outputs == "codes") and (n.codes is None) == (outputs == "y")
+    if n.y is not None:
+        assert (np.abs(np64(n.y) - y) <= (2.0 ** -8 + ERR) * np.abs(y)).all()
+    if n.codes is not None:
+        assert_near_codes(n.codes, n.scales, y)
+
+
+def test_norm_in_place_and_rows_behind():
+    """h over the residual itself and over x; rows and columns beyond stay as they were."""
+    H = 272
+    x, r = rows(9, H, 16, 1), rows(9, H, 16, 2)
+    want = L8.rms_norm8(x, None, 1e-6, r, "both")
+    for over in ("x", "residual"):
+        base = {"x": torch.full((12, H + 16), 7.0, device="cuda").bfloat16(), "residual": torch.full((12, H + 16), 7.0, device="cuda").bfloat16()}
+        a, b = base["x"][:9, :H].copy_(x), base["residual"][:9, :H].copy_(r)
+        codes = torch.full((12, 288), 9, dtype=torch.uint8, device="cuda")
+        scales = torch.full((12, 8), 9, dtype=torch.uint8, device="cuda")
+        y = torch.full((12, 280), 7.0, device="cuda").bfloat16()
+        into = L8.Norm8(codes[:9, :H], scales[:9, :3], a if over == "x" else b, y[:9, :H])
+        got = L8.rms_norm8(a, None, 1e-6, b, "both", into)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+        for t, n in ((codes, H), (scales, 3)):
+            assert (t[9:] == 9).all() and (t[:, n:] == 9).all()
+        assert (y[9:] == 7).all() and (y[:, H:] == 7).all()
+        assert (base[over][9:] == 7).all() and (base[over][:, H:] == 7).all()
+
+
+def test_norm_special_rows():
+    x = torch.zeros(4, 256, device="cuda")
+    x[1, 3] = float("nan")
+    x[2, 5] = float("inf")
+    x[3] = 2.0 ** 100   # the sum of squares passes fp32
+    n = L8.rms_norm8(x.bfloat16(), None, 1e-6, None, "both")
+    v = lo.values(np8(n.codes), np8(n.scales))
+    y = np64(n.y)
+    for got in (v, y):
+        assert (got[0] == 0).all() and np.isnan(got[1]).all() and (got[3] == 0).all()
+        assert np.isnan(got[2, 5]) and (np.delete(got[2], 5) == 0).all()
+
+
+# ---------------------------------------------------------------- the product
+def random8(R, K, high, seed, span=12):
+    """All 254 codes that are numbers, scales of some powers of two."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    codes = torch.randint(0, 254, (R, K), generator=g, device="cuda")
+    codes += codes >= 127
+    scales = torch.randint(127 - span, 127 + span, (-(-R // high), -(-K // 128)), generator=g, device="cuda")
+    return L8.rows8(codes.to(torch.uint8), scales.to(torch.uint8))
+
+
+def assert_linear(out, a, w, rows_of=None):
+    A, W = lo.values(np8(a.codes), np8(a.scales)), lo.values(np8(w.codes), np8(w.scales), 128)
+    ref, size = lo.linear(A if rows_of is None else A[rows_of], W)
+    got = np64(out)
+    assert got.shape == ref.shape and (np.isnan(got) == np.isnan(ref)).all()
+    fine = ~np.isnan(ref)
+    steps = W.shape[1] / 32 + 32
+    tol = 2.0 ** -8 * np.abs(ref) + steps * 2.0 ** -22 * size
+    assert (np.abs(got - ref)[fine] <= tol[fine]).all()
+
+
+SIZES = [(1, 1, 16), (1, 128, 128), (1, 4096, 2048), (2, 40, 144), (7, 129, 272), (8, 256, 4096), (15, 2500, 2000),
+         (16, 384, 640), (17, 128, 1024), (31, 513, 80), (33, 130, 528), (63, 2048, 768), (64, 1000, 128), (65, 64, 2064),
+         (127, 300, 256), (128, 256, 512), (129, 257, 1040), (200, 2500, 2000), (255, 77, 64), (256, 512, 2048),
+         (257, 1030, 384), (400, 255, 1536), (511, 8, 128), (513, 2049, 192), (1000, 640, 896), (1500, 3000, 1168),
+         (2049, 1025, 336), (4100, 264, 160)]
+
+
+@pytest.mark.parametrize("T,N,K", SIZES)
+def test_linear(T, N, K):
+    a, w = random8(T, K, 1, T + N), random8(N, K, 128, K + N)
+    out = L8.Linear8(*w)(*a)
+    assert_linear(out, a, w)
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 40, 64, 100, 128, 300, 1024])
+def test_linear_exact(T):
+    """Small whole numbers, whose sums fp32 holds: every bit, on every path."""
+    N, K = 520, 1040
+    g = torch.Generator("cuda").manual_seed(T)
+    x = torch.randint(-4, 5, (T, K), generator=g, device="cuda").float()
+    m = torch.randint(-4, 5, (N, K), generator=g, device="cuda").float()
+    e = lambda v: v.to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    sa = torch.randint(126, 129, (T, 9), generator=g, device="cuda", dtype=torch.uint8)
+    sw = torch.randint(126, 129, (5, 9), generator=g, device="cuda", dtype=torch.uint8)
+    a, w = L8.rows8(e(x), sa), L8.rows8(e(m), sw)
+    out = L8.Linear8(*w)(*a)
+    ref = lo.linear(lo.values(np8(a.codes), np8(a.scales)), lo.values(np8(w.codes), np8(w.scales), 128))[0]
+    assert torch.equal(out.cpu().view(torch.int16), torch.from_numpy(ref).float().bfloat16().view(torch.int16))
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 200, 272), (70, 136, 400), (600, 300, 272)])
+def test_linear_strides_and_rows_behind(T, N, K):
+    """Operands and outputs that lie in larger tensors; what is beyond them stays as it was."""
+    big = torch.randint(0, 120, (T + 3, K + 48), dtype=torch.uint8, device="cuda")
+    bs = torch.randint(120, 130, (T + 3, 12), dtype=torch.uint8, device="cuda")
+    wide = torch.randint(0, 120, (N, K + 16), dtype=torch.uint8, device="cuda")
+    ws = torch.randint(120, 130, (-(-N // 128), 8), dtype=torch.uint8, device="cuda")
+    nb = -(-K // 128)
+    a, w = L8.Block8(big[:T, 16:16 + K], bs[:T, 4:4 + nb]), L8.Block8(wide[:, :K], ws[:, :nb])
+    lin = L8.Linear8(*w)
+    assert lin.codes.data_ptr() == wide.data_ptr()   # not copied
+    for pad, at in ((8, 0), (7, 0), (8, 1), (0, 0)):   # 16-byte rows, odd rows, an odd start, its own rows
+        out = torch.full((T + 2, N + pad), 7.0, device="cuda").bfloat16()
+        view = out[:T, at:at + N]
+        assert lin(*a, out=view) is view
+        assert_linear(view, a, w)
+        assert (out[T:] == 7).all() and (out[:, :at] == 7).all() and (out[:, at + N:] == 7).all()
+
+
+@pytest.mark.parametrize("T", [2, 40, 200, 700])
+def test_linear_nan(T):
+    """A NaN code or scale reaches its row or column, and nothing else."""
+    N, K = 300, 528
+    a, w = random8(T, K, 1, 1, 4), random8(N, K, 128, 2, 4)
+    a.codes[1, 527], a.scales[T - 1, 2] = 127, 255
+    w.codes[5, 0], w.scales[2, 3] = 255, 255
+    out = np64(L8.Linear8(*w)(*a))
+    want = np.zeros((T, N), bool)
+    want[1] = want[T - 1] = True
+    want[:, 5] = want[:, 256:] = True
+    assert (np.isnan(out) == want).all()
+
+
+@pytest.mark.parametrize("T", [3, 50, 300])
+def test_linear_far_scales(T):
+    """Scales at both ends of their range, whose product is of ordinary size."""
+    N, K = 140, 256
+    a, w = random8(T, K, 1, 3, 1), random8(N, K, 128, 4, 1)
+    for la, lw in ((1, 240), (247, 10)):
+        a.scales.fill_(la)
+        w.scales.fill_(lw)
+        assert_linear(L8.Linear8(*w)(*a), a, w)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 4096, 2048), (60, 640, 4096), (500, 1000, 1024)])
+def test_same_bits_again(T, N, K):
+    a, w = random8(T, K, 1, 5), random8(N, K, 128, 6)
+    lin = L8.Linear8(*w)
+    first = lin(*a)
+    for _ in range(5):
+        assert torch.equal(lin(*a).view(torch.int16), first.view(torch.int16))
+
+
+# ---------------------------------------------------------------- streams, graphs, a run of them
+def chain(x, r, weight, lin1, lin2, stream=None):
+    """norm -> gate_up -> SiLU * up -> down, the dense FFN of a layer."""
+    n = L8.rms_norm8(x, weight, 1e-6, r, stream=stream)
+    gu = lin1(n.codes, n.scales, stream=stream)
+    q = L8.quantize8(gu, silu_mul=True, stream=stream)
+    return n, gu, q, lin2(*q, stream=stream)
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 256, 384), (37, 512, 272), (600, 256, 640)])
+def test_dense_ffn(T, H, I):
+    x, r = torch.randn(T, H, device="cuda").bfloat16(), torch.randn(T, H, device="cuda").bfloat16()
+    weight = torch.rand(H, device="cuda").bfloat16()
+    w1 = L8.quantize8_weight((torch.randn(2 * I, H, device="cuda") * H ** -0.5).bfloat16())
+    w2 = L8.quantize8_weight((torch.randn(H, I, device="cuda") * I ** -0.5).bfloat16())
+    lin1, lin2 = L8.Linear8(*w1), L8.Linear8(*w2)
+    n, gu, q, out = chain(x, r, weight, lin1, lin2)
+    assert_near_codes(n.codes, n.scales, lo.rms_norm(np64((x.float() + r.float()).bfloat16()), np64(weight), 1e-6))
+    assert_linear(gu, L8.Block8(n.codes, n.scales), w1)
+    assert_near_codes(*q, lo.silu_mul(np64(gu)), err=64 * 2.0 ** -23)
+    assert_linear(out, q, w2)
+    # against the unquantised layer: each of the four quantised operands is off by 2^-4 of a value at most,
+    # about 2^-5.3 in the root mean square, independently: 5 % of the output
+    h = np64(x) + np64(r)
+    full = lo.silu_mul(lo.rms_norm(h, np64(weight), 1e-6) @ lo.values(np8(w1.codes), np8(w1.scales), 128).T) \
+        @ lo.values(np8(w2.codes), np8(w2.scales), 128).T
+    assert np.linalg.norm(np64(out) - full) <= 0.1 * np.linalg.norm(full)
+
+    # on another stream, by object and by handle
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for s in (side, side.cuda_stream):
+        got = chain(x, r, weight, lin1, lin2, s)[3]
+        side.synchronize()
+        assert torch.equal(got, out)
+
+    # captured, then replayed over new inputs
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = chain(x, r, weight, lin1, lin2)[3]
+    x.copy_(torch.randn(T, H, device="cuda").bfloat16())
+    fresh = chain(x, r, weight, lin1, lin2)[3]
+    for _ in range(3):
+        captured.zero_()
+        graph.replay()
+        assert torch.equal(captured, fresh)
+
+
+def test_wrappers_refuse():
+    x = torch.zeros(4, 256, device="cuda").bfloat16()
+    q = L8.quantize8(x)
+    lin = L8.Linear8(*L8.quantize8_weight(torch.zeros(40, 256, device="cuda").bfloat16()))
+    for bad in (lambda: L8.quantize8(x.float()), lambda: L8.quantize8(x[0]), lambda: L8.quantize8(x.t()),
+                lambda: L8.quantize8(x[:, :255], silu_mul=True), lambda: L8.quantize8(x, into=L8.quantize8(x[:, :128])),
+                lambda: L8.rms_norm8(x, outputs="h"), lambda: L8.rms_norm8(x, torch.ones(256, device="cuda")),
+                lambda: L8.rms_norm8(x, residual=x[:3]), lambda: L8.rms_norm8(x, residual=x.cpu()),
+                lambda: L8.rms_norm8(x, into=L8.rms_norm8(x, outputs="y")),
+                lambda: L8.rms_norm8(x, residual=x, into=L8.rms_norm8(x)),
+                lambda: lin(x, q.scales), lambda: lin(q.codes[:, :128], q.scales), lambda: lin(q.codes, q.scales[:2]),
+                lambda: lin(*q, out=torch.empty(4, 39, device="cuda").bfloat16()), lambda: lin(*q, out=torch.empty(4, 40, device="cuda")),
+                lambda: L8.Linear8(q.codes, q.scales), lambda: L8.Linear8(x, q.scales)):
+        with pytest.raises(ValueError):
+            bad()
+    host = torch.empty(4, 40, dtype=torch.bfloat16)
+    for bad in (lambda: L8.quantize8(x[:, :40]), lambda: L8.quantize8(x[:, 4:20]),
+                lambda: B.moe_linear8(q.codes, 256, q.scales, 4, lin.codes, 256, lin.scales, 4, 4, 40, 256, host, 40, None)):
+        with pytest.raises(B.MoEError) as e:
+            bad()
+        assert e.value.code == -2
+    assert L8.quantize8(x[:0]).codes.shape == (0, 256) and lin(*L8.quantize8(x[:0])).shape == (0, 40)
+    assert L8.rms_norm8(x[:0], residual=x[:0], outputs="both").y.shape == (0, 256)
