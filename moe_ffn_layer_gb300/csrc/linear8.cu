@@ -1,66 +1,323 @@
-// Product of two 8-bit matrices with block scales: out[t][n] = sum over the
-// 128-wide blocks b of K of 2^(ea[t][b] + ew[n / 128][b]) * sum_{k in b} a[t][k] w[n][k].
-#include "common.cuh"
-#include "kernels.h"
+// Product of two 8-bit matrices with block scales, few rows of A: out[t][n] =
+// sum over the 128-wide blocks b of K of 2^(ea[t][b] + ew[n / 128][b] - 254) *
+// sum_{k in b} a[t][k] w[n][k].
+//
+// The weights are the MMA's A operand, 128 of their rows a tile, and the tokens
+// its B operand, 16 to 128 columns, so that few tokens waste little of the MMA.
+// K is cut between the CTAs of a cluster, enough of them to draw the weights'
+// stream over every SM; each then sums its share of the tokens' partial sums, which
+// the others store into its shared memory, in the order of the ranks.
+#include <mutex>
+
+#include "linear8.cuh"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ float value(uint32_t code) {
-  return (code & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FFFFFFFu) : e4m3_to_f32(code);
-}
+constexpr int kThreads = 128;
+constexpr int kWideM = 128;   // weight rows of a tile
 
-// 64 x 64 outputs a CTA, 4 x 4 a thread, fp32 FMAs; a block's sum takes its scales when the block is done.
-__global__ void __launch_bounds__(256) linear8_kernel(Linear8 a) {
+template <int kNT>
+struct Cfg {
+  static constexpr int kChains = kNT <= 32 ? 4 : 2;   // accumulators that the MMAs of a block take in turn
+  static constexpr int kStages = kNT == 16 ? 5 : kNT == 32 ? 4 : kNT == 64 ? 3 : 4;
+  static constexpr int kLog = kNT == 16 ? 4 : kNT == 32 ? 5 : kNT == 64 ? 6 : 7;
+  static constexpr int kSlots = 2;   // of scale words, four blocks of K each
+  static constexpr uint32_t kStageBytes = kWideM * kBlockK + kNT * kBlockK;
+  static constexpr uint32_t kRecv = kStages * kStageBytes;                   // partial sums [rank][token][128] fp32
+  static constexpr uint32_t kSf = kRecv + kNT * kWideM * 4;                  // scale words: weights, tokens
+  static constexpr uint32_t kCtl = kSf + kSlots * 2 * kSfBytes;
+  static constexpr uint32_t kSmem = kCtl + (2 * kStages + 2 * kSlots + 1) * 8 + 48 + 1024;   // (1024: the ring's alignment)
+  static constexpr int kCols = (kChains * kNT < 32 ? 32 : kChains * kNT) + kSlots * 2 * kSfCols;
+  static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static constexpr uint32_t kSfBase = kChains * kNT;
+};
+
+template <int kNT>
+__global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_constant__ CUtensorMap mw,
+                                                                  const __grid_constant__ CUtensorMap ma, Linear8 a, int split,
+                                                                  int* status, uint64_t wait_ns) {
+  using C = Cfg<kNT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kCtl);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* sf_full = empty + C::kStages;
+  uint64_t* sf_empty = sf_full + C::kSlots;
+  uint64_t* done = sf_empty + C::kSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* ok_of = reinterpret_cast<int*>(tmem_slot + 2);   // [8] whether each CTA of the cluster has its sums
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x % split;   // == rank in the cluster
+  const int n0 = blockIdx.x / split * kWideM, t0 = blockIdx.y * kNT;
+  const int blocks = (a.K + kBlockK - 1) / kBlockK;
+  const int kb0 = static_cast<int>(static_cast<long long>(blocks) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&sf_full[i], 1);
+      mbar_init(&sf_empty[i], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 3) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&mw);
+    tma_prefetch_desc(&ma);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (split > 1) cluster_arrive();   // (waited for before the first access to another CTA)
   chain_wait();
   ChainReleaseAtExit release;
-  __shared__ float sa[16][65], sw[16][65];
-  const int t0 = blockIdx.y * 64, n0 = blockIdx.x * 64, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  float acc[4][4] = {}, sub[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 16) {
-    __syncthreads();
-    const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 4;
-    const uint32_t va = t0 + r < a.T ? *reinterpret_cast<const uint32_t*>(a.a + (t0 + r) * a.lda + k0 + c) : 0u;
-    const uint32_t vw = n0 + r < a.N ? *reinterpret_cast<const uint32_t*>(a.w + (n0 + r) * a.ldw + k0 + c) : 0u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      sa[c + j][r] = value(va >> (8 * j) & 0xFFu);
-      sw[c + j][r] = value(vw >> (8 * j) & 0xFFu);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sub[i][j] = fmaf(sa[k][ty * 4 + i], sw[k][tx * 4 + j], sub[i][j]);
-    if ((k0 & 127) == 112 || k0 + 16 == a.K) {
-      const int b = k0 >> 7;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ea = t0 + ty * 4 + i < a.T ? a.a_scales[(t0 + ty * 4 + i) * a.las + b] : 127;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int ew = n0 + tx * 4 + j < a.N ? a.w_scales[((n0 + tx * 4 + j) >> 7) * a.lws + b] : 127;
-          acc[i][j] += ea == 255 || ew == 255 ? __uint_as_float(0x7FFFFFFFu) : ldexpf(sub[i][j], ea + ew - 254);
-          sub[i][j] = 0.f;
+
+  int issued = 0;   // blocks of K whose copies were started
+  if (warp == 0) {
+    if (lane == 0) {
+      // the weights are read once where one tile holds all tokens
+      const uint64_t pol_w = gridDim.y == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+      const uint64_t pol_a = l2_policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, status, wait_ns)) break;
+        mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
+        uint8_t* at = smem + stage * C::kStageBytes;
+        tma_load_2d(at, &mw, &full[stage], kb * kBlockK, n0, pol_w);
+        tma_load_2d(at + kWideM * kBlockK, &ma, &full[stage], kb * kBlockK, t0, pol_a);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, sf_phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t sfa = tmem + C::kSfBase + slot * 2 * kSfCols, sfb = sfa + kSfCols;
+        if (kb == kb0 || (kb & 3) == 0) {
+          if (!mbar_wait(&sf_full[slot], sf_phase, abort_flag, status, wait_ns)) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + C::kSf + slot * 2 * kSfBytes);
+          scales_to_tmem<1>(sfa, at);
+          scales_to_tmem<1>(sfb, at + kSfBytes);
+        }
+        if (!mbar_wait(&full[stage], phase, abort_flag, status, wait_ns)) break;
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + stage * C::kStageBytes);
+        const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + kWideM * kBlockK);
+        const uint32_t idesc = idesc_mx8(kWideM, kNT) | mx8_byte(kb & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
+          umma_mx8<1>(tmem + (k % C::kChains) * kNT, da + 2 * k, db + 2 * k, idesc, sfa, sfb, kb > kb0 || k >= C::kChains);
+        umma_commit(&empty[stage]);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if ((kb & 3) == 3) {
+          umma_commit(&sf_empty[slot]);
+          if (++slot == C::kSlots) {
+            slot = 0;
+            sf_phase ^= 1u;
+          }
+        }
+      }
+      umma_commit(done);   // (whatever was issued)
+    }
+  } else if (warp == 2) {
+    int slot = 0;
+    uint32_t phase = 0;
+    const int g1 = (kb1 + 3) >> 2;
+    for (int g = kb0 >> 2; g < g1; ++g) {
+      const uint4 tok = scale_words(a.a_scales, a.las, t0, a.T, g);
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(a.w_scales + static_cast<long long>(n0 >> 7) * a.lws + 4 * g);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], phase ^ 1u, abort_flag, status, wait_ns))) break;
+      const uint32_t at = smem_u32(smem + C::kSf + slot * 2 * kSfBytes) + lane * 16;
+      sts_u4(at, make_uint4(w, w, w, w));
+      sts_u4(at + kSfBytes, tok);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sf_full[slot]);
+      if (++slot == C::kSlots) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j)
-      if (t0 + ty * 4 + i < a.T && n0 + tx * 4 + j < a.N)
-        a.out[(t0 + ty * 4 + i) * a.ldo + n0 + tx * 4 + j] = __float2bfloat16_rn(acc[i][j]);
+  __syncwarp();
+
+  // every warp: its 32 weight rows of the accumulators
+  const bool in_time = mbar_wait(done, 0, abort_flag, status, wait_ns);
+  const bool ok = __syncthreads_and(in_time && !*abort_flag);
+  if (!ok && threadIdx.x == 0) {
+    // given up: the MMAs and copies in flight end before the CTA does (bounded waits)
+    mbar_wait_timed(done, 0, status);
+    for (int i = 0; i < C::kStages && i < issued; ++i)
+      mbar_wait_timed(&full[i], ((issued - 1 - i) / C::kStages) & 1, status);
+  }
+  tc_fence_after();
+  float acc[kNT];
+  if (ok) {
+    const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll
+    for (int c = 0; c < kNT; c += 16) {
+      uint32_t r[C::kChains][16];
+#pragma unroll
+      for (int i = 0; i < C::kChains; ++i) tmem_ld_16cols(at + i * kNT + c, r[i]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float s = __uint_as_float(r[0][j]);
+#pragma unroll
+        for (int i = 1; i < C::kChains; ++i) s += __uint_as_float(r[i][j]);
+        acc[c + j] = s;
+      }
+    }
+  }
+  tc_fence_before();
+  const bool pairs = (a.ldo & 1) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
+  if (split == 1) {
+    if (ok) {
+      const int n = n0 + warp * 32 + lane;
+      if (pairs) {
+        // neighbouring lanes trade, so that the even one has both rows' sums of one token and the odd one of the next
+        const int np = n & ~1;
+#pragma unroll
+        for (int j = 0; j < kNT; j += 2) {
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? acc[j] : acc[j + 1], 1);
+          const int t = t0 + j + (lane & 1);
+          const uint32_t v = (lane & 1) ? pack_bf16x2(other, acc[j + 1]) : pack_bf16x2(acc[j], other);
+          if (t < a.T && np < a.N) {
+            __nv_bfloat16* to = a.out + t * a.ldo + np;
+            if (np + 1 < a.N) *reinterpret_cast<uint32_t*>(to) = v;
+            else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(v);
+          }
+        }
+      } else if (n < a.N) {
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+          if (t0 + j < a.T) a.out[(t0 + j) * a.ldo + n] = __float2bfloat16_rn(acc[j]);
+      }
+    }
+  } else {
+    cluster_wait();
+    const int lg = __ffs(split) - 1, share = kNT >> lg;   // tokens of each CTA
+    if (threadIdx.x < split) {
+      const uint32_t to = cluster_addr(smem_u32(&ok_of[rank]), threadIdx.x);
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(ok ? 1 : 0) : "memory");
+    }
+    if (ok) {
+      const uint32_t mine = smem_u32(smem + C::kRecv) + (rank * share * kWideM + threadIdx.x) * 4;
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) {
+        const uint32_t to = cluster_addr(mine, j >> (C::kLog - lg)) + (j & (share - 1)) * kWideM * 4;
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(acc[j]) : "memory");
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    bool all = true;
+    for (int r = 0; r < split; ++r) all = all && ok_of[r];
+    const int n = n0 + (threadIdx.x & 63) * 2;
+    if (all && n < a.N)
+      for (int j = threadIdx.x >> 6; j < share; j += 2) {
+        const int t = t0 + static_cast<int>(rank) * share + j;
+        if (t >= a.T) break;
+        float2 s = make_float2(0.f, 0.f);
+        for (int r = 0; r < split; ++r) {
+          const float2 p = *reinterpret_cast<const float2*>(smem + C::kRecv + ((r * share + j) * kWideM + (threadIdx.x & 63) * 2) * 4);
+          s.x += p.x;
+          s.y += p.y;
+        }
+        __nv_bfloat16* to = a.out + t * a.ldo + n;
+        if (pairs && n + 1 < a.N) {
+          *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(s.x, s.y);
+        } else {
+          to[0] = __float2bfloat16_rn(s.x);
+          if (n + 1 < a.N) to[1] = __float2bfloat16_rn(s.y);
+        }
+      }
+  }
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int kNT>
+int launch_narrow(const Linear8& a, int split, int* status, cudaStream_t stream) {
+  using C = Cfg<kNT>;
+  static std::mutex mu;
+  static bool ready[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MOE_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(linear8_narrow_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        return MOE_ERR_CUDA;
+      ready[dev] = true;
+    }
+  }
+  CUtensorMap mw, ma;
+  if (!linear8_map(&mw, a.w, a.N, a.K, a.ldw, kWideM) || !linear8_map(&ma, a.a, a.T, a.K, a.lda, kNT)) return MOE_ERR_CUDA;
+  const dim3 grid((a.N + kWideM - 1) / kWideM * split, (a.T + kNT - 1) / kNT);
+  if (grid.y > 65535) return MOE_ERR_UNSUPPORTED;
+  return launch_chained_cluster(linear8_narrow_kernel<kNT>, grid, dim3(kThreads), C::kSmem, stream, split, mw, ma, a, split, status,
+                                wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
 
+bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+  });
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld};
+  const cuuint32_t box[2] = {kBlockK, box_rows}, one[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches) {
-  if (launch_chained(linear8_kernel, dim3((a.N + 63) / 64, (a.T + 63) / 64), dim3(256), 0, stream, a) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  ++*launches;
-  return MOE_OK;
+  const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
+  const int blocks = (a.K + kBlockK - 1) / kBlockK;
+  const long long tiles = static_cast<long long>((a.N + kWideM - 1) / kWideM) * ((a.T + nt - 1) / nt);
+  int split = 1;
+  while (split < 8 && tiles * split < sms && blocks >= 2 * split) split *= 2;
+  const int rc = nt == 16   ? launch_narrow<16>(a, split, status, stream)
+                 : nt == 32 ? launch_narrow<32>(a, split, status, stream)
+                 : nt == 64 ? launch_narrow<64>(a, split, status, stream)
+                            : launch_narrow<128>(a, split, status, stream);
+  if (rc == MOE_OK) ++*launches;
+  return rc;
 }
 
 }  // namespace moe

@@ -1,0 +1,93 @@
+// What the kernels of the 8-bit product share: block-scaled MMAs, their scales in
+// tensor memory, cluster addresses, tensor maps.
+//
+// The tensor cores' mxf8f6f4 MMA multiplies each row's product over 32 values of
+// K by two powers of two, A's and B's, that it takes as exponent bytes from
+// tensor memory, and adds the fp32 results into D.  The scales of 128 rows are
+// four columns: row r's 32-bit word in lane r % 32 of column r / 32, the same in
+// each quarter of the lanes; the instruction descriptor says which byte of the word
+// an MMA uses.  A word here is a row's scales of four neighbouring blocks of
+// 128, as they lie in memory, and all four MMAs of a block use its byte.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+constexpr int kBlockK = 128;          // values of K per scale, and per row of a staged tile (128 bytes, 128-byte swizzle)
+constexpr uint32_t kSfBytes = 512;    // scale words of 128 rows in shared memory: 32 rows of 16 bytes
+constexpr uint32_t kSfCols = 4;       // and in tensor memory
+
+// D[tmem] (+)= (A sfa) (B sfb)^T over 32 values of K.
+template <int kGroup>
+__device__ __forceinline__ void umma_mx8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+  if (kGroup == 1) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// Instruction descriptor of it: e4m3 A and B, both K-major, shape M x N, e8m0
+// scales; `byte` is added by mx8_byte.
+__host__ __device__ constexpr uint32_t idesc_mx8(int M, int N) {
+  return (static_cast<uint32_t>(N >> 3) << 17)      // N / 8
+         | (1u << 23)                               // scales are e8m0
+         | (static_cast<uint32_t>(M >> 7) << 27);   // M / 128
+}
+// The byte of the scale words that an MMA uses, A's and B's.
+__device__ __forceinline__ uint32_t mx8_byte(uint32_t byte) { return byte << 4 | byte << 29; }
+
+// 32 rows of 16 bytes in shared memory (scale words of 128 rows) to four
+// columns of tensor memory, the same in each quarter of the lanes.  Runs in the order
+// of issue with the MMAs.
+template <int kGroup>
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
+  // rows of 16 bytes, groups of eight rows 128 bytes apart, no swizzle
+  const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
+                        (static_cast<uint64_t>(1u) << 46);
+  if (kGroup == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// The address of `saddr` (shared memory of this CTA) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Scale words of rows row0 + lane + 32 c (c < 4) for the blocks 4 g .. 4 g + 3;
+// rows from `rows` on have 1.0 (their codes read as 0).
+__device__ __forceinline__ uint4 scale_words(const uint8_t* scales, long long lds, int row0, int rows, int g) {
+  uint32_t w[4];
+  const int r = row0 + static_cast<int>(threadIdx.x & 31);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    w[c] = r + 32 * c < rows ? *reinterpret_cast<const uint32_t*>(scales + (r + 32 * c) * lds + 4 * g) : 0x7F7F7F7Fu;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A byte matrix [rows][cols], rows `ld` bytes apart, in boxes of 128 bytes x
+// box_rows in the 128-byte swizzle; what lies outside reads as 0.
+bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
+
+int linear8_narrow_launch(const Linear8& a, int* status, int sms, cudaStream_t stream);
+
+}  // namespace moe

@@ -372,3 +372,24 @@ def test_wrappers_refuse():
         assert e.value.code == -2
     assert L8.quantize8(x[:0]).codes.shape == (0, 256) and lin(*L8.quantize8(x[:0])).shape == (0, 40)
     assert L8.rms_norm8(x[:0], residual=x[:0], outputs="both").y.shape == (0, 256)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 128, 256), (3, 300, 2048), (40, 520, 1024), (300, 2048, 512), (1100, 512, 640)])
+def test_expired_waits_write_nothing(T, N, K):
+    """With the wait limit at 0 a wait that is not complete at its first test expires: the product records it,
+    lets its copies and MMAs in flight end, and writes nothing; the next call is clean."""
+    a, w = random8(T, K, 1, 8), random8(N, K, 128, 9)
+    lin = L8.Linear8(*w)
+    fresh = lin(*a)
+    out = torch.full_like(fresh, 5.0)
+    s = torch.cuda.current_stream()
+    assert B.moe_last_device_error(s) == 0
+    try:
+        B.moe_debug_set_wait_limit_ns(0)
+        lin(*a, out=out)
+    finally:
+        B.moe_debug_set_wait_limit_ns(2_000_000_000)
+    assert B.moe_last_device_error(s) == -5
+    assert (out == 5.0).all()
+    assert torch.equal(lin(*a).view(torch.int16), fresh.view(torch.int16))
+    assert B.moe_last_device_error(s) == 0
