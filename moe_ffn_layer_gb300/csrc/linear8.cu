@@ -286,10 +286,14 @@ int launch_narrow(const Linear8& a, int split, int* status, cudaStream_t stream)
 
 }  // namespace
 
-bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
-  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+namespace {
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t cols, uint64_t ld_bytes,
+            uint32_t box_cols, uint32_t box_rows) {
   static EncodeFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -300,13 +304,28 @@ bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
       fn = reinterpret_cast<EncodeFn>(p);
   });
   if (!fn) return false;
-  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld};
-  const cuuint32_t box[2] = {kBlockK, box_rows}, one[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld_bytes};
+  const cuuint32_t box[2] = {box_cols, box_rows}, one[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rows, cols, ld, kBlockK, box_rows);
+}
+
+bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows) {
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.T, a.N, 2 * a.ldo, 64, box_rows);
+}
+
 int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches) {
+  if (a.T > 512) {
+    const int rc = linear8_wide_launch(a, status, stream);
+    if (rc == MOE_OK) ++*launches;
+    return rc;
+  }
   const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
   const int blocks = (a.K + kBlockK - 1) / kBlockK;
   const long long tiles = static_cast<long long>((a.N + kWideM - 1) / kWideM) * ((a.T + nt - 1) / nt);

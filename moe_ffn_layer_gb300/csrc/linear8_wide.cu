@@ -1,0 +1,375 @@
+// Product of two 8-bit matrices with block scales, many rows of A: tiles of 256
+// tokens x kBN weight rows, computed by pairs of CTAs (two-CTA MMAs, M = 256).
+//
+// Each CTA of a pair stages its 128 tokens and half of the tile's weight rows, and
+// holds its tokens' sums in tensor memory; the first one's MMA thread issues for
+// both.  So a CTA reads (128 + kBN / 2) rows a block of K for a 128 x kBN tile.
+#include <mutex>
+
+#include "linear8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;   // 4 warps: copies, MMAs, scales, tensor memory; 4 warps: the epilogue
+constexpr int kM = 256;         // tokens of a pair's tile
+
+template <int kBN>
+struct Cfg {
+  static constexpr int kBufs = 2 * kBN <= 480 ? 2 : 1;   // accumulators
+  static constexpr uint32_t kABytes = kM / 2 * kBlockK, kBBytes = kBN / 2 * kBlockK;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+  static constexpr int kSlots = 2;   // of scale words, four blocks of K each
+  static constexpr int kBCopies = (kBN + 127) / 128;
+  static constexpr uint32_t kSlotBytes = (1 + kBCopies) * kSfBytes;
+  static constexpr uint32_t kOutBytes = 4 * 32 * 128;   // an epilogue warp's 32 rows of 64 bf16
+  static constexpr int kStages = (232448 - 1024 - 512 - kOutBytes - kSlots * kSlotBytes) / kStageBytes;
+  static constexpr uint32_t kOut = kStages * kStageBytes;
+  static constexpr uint32_t kSf = kOut + kOutBytes;
+  static constexpr uint32_t kCtl = kSf + kSlots * kSlotBytes;
+  static constexpr uint32_t kSmem = kCtl + 512 + 1024;   // (1024: the ring's alignment)
+  static constexpr uint32_t kSfBase = kBufs * kBN;
+  static constexpr uint32_t kSlotCols = (1 + kBCopies) * kSfCols;
+  static_assert(kSfBase + kSlots * kSlotCols <= 512, "tensor memory");
+  static_assert((2 * kStages + 2 * kSlots + 2 * kBufs + 1) * 8 + 16 <= 512, "control region");
+  static_assert(kStageBytes % 1024 == 0 && kBN % 32 == 0, "swizzled tiles, scale words by 32 rows");
+};
+
+// mbar_wait for a barrier that threads of the other CTA arrive on.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+                                                  uint64_t limit_ns) {
+  // (the second test, of a phase that is complete, has the other CTA's writes acquired)
+  return mbar_wait(bar, parity, abort, status, limit_ns) && try_wait_cluster(bar, parity);
+}
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {   // on the first CTA's barrier
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(smem_u32(bar), 0)) : "memory");
+}
+
+// A box into this CTA's shared memory, its bytes counted on the first CTA's barrier.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs when the MMAs and copies issued so far by this thread are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Tiles in groups of eight rows of tiles, so that the tiles that run at once share operands in L2.
+struct Tiles {
+  int mt, nt;
+  __device__ __forceinline__ void at(int tile, int* m, int* n) const {
+    const int per = 8 * nt, g = tile / per, r = tile - g * per, high = min(8, mt - 8 * g);
+    *n = r / high;
+    *m = 8 * g + r - *n * high;
+  }
+};
+
+template <int kBN>
+__global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_constant__ CUtensorMap ma,
+                                                                   const __grid_constant__ CUtensorMap mw,
+                                                                   const __grid_constant__ CUtensorMap mo, Linear8 a, int tma_out,
+                                                                   int* status, uint64_t wait_ns) {
+  using C = Cfg<kBN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kCtl);   // (the first CTA's)
+  uint64_t* empty = full + C::kStages;
+  uint64_t* sf_full = empty + C::kStages;                         // (the first CTA's)
+  uint64_t* sf_empty = sf_full + C::kSlots;
+  uint64_t* acc_full = sf_empty + C::kSlots;
+  uint64_t* acc_empty = acc_full + C::kBufs;                      // (the first CTA's)
+  uint64_t* drained = acc_empty + C::kBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int blocks = (a.K + kBlockK - 1) / kBlockK;
+  const Tiles order{(a.T + kM - 1) / kM, (a.N + kBN - 1) / kBN};
+  const int tiles = order.mt * order.nt, step = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&sf_full[i], 2);
+      mbar_init(&sf_empty[i], 1);
+    }
+    for (int i = 0; i < C::kBufs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 3) {
+    // both CTAs of the pair, and only one CTA fits an SM: no other can hold the columns for good
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&ma);
+    tma_prefetch_desc(&mw);
+    if (tma_out) tma_prefetch_desc(&mo);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  chain_wait();
+  ChainReleaseAtExit release;
+
+  int issued = 0;   // blocks of K whose copies were started
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+        int m, n;
+        order.at(tile, &m, &n);
+        const int row_a = m * kM + rank * (kM / 2), row_b = n * kBN + rank * (kBN / 2);
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (!(ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, status, wait_ns))) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+          const uint32_t at = smem_u32(smem + stage * C::kStageBytes), bar = cluster_addr(smem_u32(&full[stage]), 0);
+          tma_load_pair(at, &ma, bar, kb * kBlockK, row_a, pol);
+          tma_load_pair(at + C::kABytes, &mw, bar, kb * kBlockK, row_b, pol);
+          ++issued;
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int stage = 0, slot = 0, buf = 0;
+      uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+        if (!(ok = mbar_wait_cluster(&acc_empty[buf], acc_phase ^ 1u, abort_flag, status, wait_ns))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kBN;
+        for (int kb = 0; kb < blocks; ++kb) {
+          const uint32_t sfa = tmem + C::kSfBase + slot * C::kSlotCols, sfb = sfa + kSfCols;
+          if ((kb & 3) == 0) {
+            if (!(ok = mbar_wait_cluster(&sf_full[slot], sf_phase, abort_flag, status, wait_ns))) break;
+            tc_fence_after();
+            const uint32_t at = smem_u32(smem + C::kSf + slot * C::kSlotBytes);
+#pragma unroll
+            for (int i = 0; i < 1 + C::kBCopies; ++i) scales_to_tmem<2>(sfa + i * kSfCols, at + i * kSfBytes);
+          }
+          if (!(ok = mbar_wait(&full[stage], phase, abort_flag, status, wait_ns))) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem + stage * C::kStageBytes);
+          const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + C::kABytes);
+          const uint32_t idesc = idesc_mx8(kM, kBN) | mx8_byte(kb & 3);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
+            umma_mx8<2>(d, da + 2 * k, db + 2 * k, idesc, sfa, sfb, kb > 0 || k > 0);
+          commit_pair(&empty[stage]);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if ((kb & 3) == 3 || kb == blocks - 1) {
+            commit_pair(&sf_empty[slot]);
+            if (++slot == C::kSlots) {
+              slot = 0;
+              sf_phase ^= 1u;
+            }
+          }
+        }
+        if (!ok) break;
+        commit_pair(&acc_full[buf]);
+        if (++buf == C::kBufs) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      commit_pair(drained);   // (whatever was issued)
+    }
+  } else if (warp == 2) {
+    int slot = 0;
+    uint32_t phase = 0;
+    const int groups = (blocks + 3) >> 2;
+    bool ok = true;
+    for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+      int m, n;
+      order.at(tile, &m, &n);
+      for (int g = 0; g < groups; ++g) {
+        const uint4 tok = scale_words(a.a_scales, a.las, m * kM + rank * (kM / 2), a.T, g);
+        uint32_t w[4 * C::kBCopies];
+#pragma unroll
+        for (int c = 0; c < 4 * C::kBCopies; ++c) {
+          const int row = n * kBN + 32 * c;
+          w[c] = c < kBN / 32 && row < a.N ? *reinterpret_cast<const uint32_t*>(a.w_scales + (row >> 7) * a.lws + 4 * g) : 0x7F7F7F7Fu;
+        }
+        if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], phase ^ 1u, abort_flag, status, wait_ns)))) break;
+        const uint32_t at = smem_u32(smem + C::kSf + slot * C::kSlotBytes) + lane * 16;
+        sts_u4(at, tok);
+#pragma unroll
+        for (int i = 0; i < C::kBCopies; ++i) sts_u4(at + (1 + i) * kSfBytes, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_first(&sf_full[slot]);
+        if (++slot == C::kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    const int quad = warp & 3;
+    const uint32_t stage_out = smem_u32(smem + C::kOut) + quad * 32 * 128;
+    int buf = 0;
+    uint32_t phase = 0;
+    for (int tile = blockIdx.x >> 1; tile < tiles; tile += step) {
+      int m, n;
+      order.at(tile, &m, &n);
+      const int row0 = m * kM + rank * (kM / 2) + quad * 32, col0 = n * kBN;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], phase, abort_flag, status, wait_ns))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * kBN + (static_cast<uint32_t>(quad * 32) << 16);
+      uint32_t v[kBN / 2];
+#pragma unroll
+      for (int c = 0; c < kBN; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32cols(acc + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[c / 2 + i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_first(&acc_empty[buf]);
+      if (++buf == C::kBufs) {
+        buf = 0;
+        phase ^= 1u;
+      }
+#pragma unroll
+      for (int c = 0; c < kBN; c += 64) {
+        if (col0 + c >= a.N || row0 >= a.T) break;
+        // the last chunk has left the staging rows
+        if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + 8 * j < kBN)
+            sts_u4(stage_out + lane * 128 + ((j ^ (lane & 7)) << 4),
+                   make_uint4(v[c / 2 + 4 * j], v[c / 2 + 4 * j + 1], v[c / 2 + 4 * j + 2], v[c / 2 + 4 * j + 3]));
+        if (tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                             reinterpret_cast<uint64_t>(&mo)), "r"(stage_out), "r"(col0 + c), "r"(row0)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {
+          __syncwarp();
+          const int cols = min(min(64, kBN - c), a.N - col0 - c);
+          for (int r = 0; r < 32 && row0 + r < a.T; ++r) {
+            __nv_bfloat16* to = a.out + (row0 + r) * a.ldo + col0 + c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = lane + 32 * h;
+              uint16_t x;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(stage_out + r * 128 + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2));
+              if (i < cols) *reinterpret_cast<uint16_t*>(to + i) = x;
+            }
+          }
+        }
+      }
+    }
+    if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0) mbar_wait_timed(drained, 0, status);   // nothing more arrives here from the MMAs
+  if (*abort_flag && threadIdx.x == 0) {
+    // given up: the copies in flight end before the CTAs do (bounded waits); what the other CTA has
+    // in flight is counted on the first one's barriers, in part perhaps: a while more for that
+    if (rank == 0)
+      for (int i = 0; i < C::kStages && i < issued; ++i)
+        mbar_wait_timed(&full[i], ((issued - 1 - i) / C::kStages) & 1, status);
+    const uint64_t from = globaltimer();
+    while (globaltimer() - from < 1000000) __nanosleep(1000);
+  }
+  // neither CTA leaves while the other may still reach its barriers or read its operands
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 3) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+template <int kBN>
+int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
+  using C = Cfg<kBN>;
+  static std::mutex mu;
+  static int pairs_of[64] = {};   // the pairs that fit a device at once
+  int dev = 0, pairs = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MOE_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!pairs_of[dev]) {
+      if (cudaFuncSetAttribute(linear8_wide_kernel<kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        return MOE_ERR_CUDA;
+      cudaLaunchConfig_t q = {};
+      q.gridDim = dim3(2);
+      q.blockDim = dim3(kThreads);
+      q.dynamicSmemBytes = C::kSmem;
+      cudaLaunchAttribute at;
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = 2;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      q.attrs = &at;
+      q.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&pairs, linear8_wide_kernel<kBN>, &q) != cudaSuccess || pairs < 1) return MOE_ERR_CUDA;
+      pairs_of[dev] = pairs;
+    }
+    pairs = pairs_of[dev];
+  }
+  const long long tiles = static_cast<long long>((a.T + kM - 1) / kM) * ((a.N + kBN - 1) / kBN);
+  if (tiles > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  CUtensorMap ma, mw, mo = {};
+  if (!linear8_map(&ma, a.a, a.T, a.K, a.lda, kM / 2) || !linear8_map(&mw, a.w, a.N, a.K, a.ldw, kBN / 2)) return MOE_ERR_CUDA;
+  // whole boxes by TMA where the rows lie as it takes them
+  const bool tma_out = a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && linear8_out_map(&mo, a, 32);
+  const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+  return launch_chained_cluster(linear8_wide_kernel<kBN>, dim3(grid), dim3(kThreads), C::kSmem, stream, 2, ma, mw, mo, a,
+                                tma_out ? 1 : 0, status, wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+int linear8_wide_launch(const Linear8& a, int* status, cudaStream_t stream) { return launch_wide<256>(a, status, stream); }
+
+}  // namespace moe
