@@ -105,41 +105,40 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, sf_phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const uint32_t sfa = tmem + C::kSfBase + slot * 2 * kSfCols, sfb = sfa + kSfCols;
-        if (kb == kb0 || (kb & 3) == 0) {
-          if (!mbar_wait(&sf_full[slot], sf_phase, abort_flag, status, wait_ns)) break;
-          tc_fence_after();
-          const uint32_t at = smem_u32(smem + C::kSf + slot * 2 * kSfBytes);
-          scales_to_tmem<1>(sfa, at);
-          scales_to_tmem<1>(sfb, at + kSfBytes);
+    const bool one = elect_one();
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, sf_phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const uint32_t sfa = tmem + C::kSfBase + slot * 2 * kSfCols, sfb = sfa + kSfCols;
+      const bool group = kb == kb0 || (kb & 3) == 0;
+      if (group && !warp_wait(&sf_full[slot], sf_phase, abort_flag, status, wait_ns)) break;
+      if (!warp_wait(&full[stage], phase, abort_flag, status, wait_ns)) break;
+      tc_fence_after();
+      const uint32_t sf_at = smem_u32(smem + C::kSf + slot * 2 * kSfBytes), at = smem_u32(smem + stage * C::kStageBytes);
+      const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + kWideM * kBlockK);
+      const uint32_t idesc = idesc_mx8(kWideM, kNT) | mx8_byte(kb & 3);
+      if (one) {
+        if (group) {
+          scales_to_tmem<1>(sfa, sf_at);
+          scales_to_tmem<1>(sfb, sf_at + kSfBytes);
         }
-        if (!mbar_wait(&full[stage], phase, abort_flag, status, wait_ns)) break;
-        tc_fence_after();
-        const uint32_t at = smem_u32(smem + stage * C::kStageBytes);
-        const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + kWideM * kBlockK);
-        const uint32_t idesc = idesc_mx8(kWideM, kNT) | mx8_byte(kb & 3);
 #pragma unroll
         for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
           umma_mx8<1>(tmem + (k % C::kChains) * kNT, da + 2 * k, db + 2 * k, idesc, sfa, sfb, kb > kb0 || k >= C::kChains);
         umma_commit(&empty[stage]);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if ((kb & 3) == 3) {
-          umma_commit(&sf_empty[slot]);
-          if (++slot == C::kSlots) {
-            slot = 0;
-            sf_phase ^= 1u;
-          }
-        }
+        if ((kb & 3) == 3) umma_commit(&sf_empty[slot]);
       }
-      umma_commit(done);   // (whatever was issued)
+      __syncwarp();
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if ((kb & 3) == 3 && ++slot == C::kSlots) {
+        slot = 0;
+        sf_phase ^= 1u;
+      }
     }
+    if (one) umma_commit(done);   // (whatever was issued)
   } else if (warp == 2) {
     int slot = 0;
     uint32_t phase = 0;

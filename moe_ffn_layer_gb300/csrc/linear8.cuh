@@ -73,6 +73,18 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// The MMA warps run whole, so that descriptors and addresses stay in uniform registers, as the
+// MMA takes them; one elected lane issues.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
+  if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, status, limit_ns)) != 0;
+}
+
 // Scale words of rows row0 + lane + 32 c (c < 4) for the blocks 4 g .. 4 g + 3;
 // rows from `rows` on have 1.0 (their codes read as 0).
 __device__ __forceinline__ uint4 scale_words(const uint8_t* scales, long long lds, int row0, int rows, int g) {

@@ -35,7 +35,7 @@ struct Cfg {
   static_assert(kStageBytes % 1024 == 0 && kBN % 32 == 0, "swizzled tiles, scale words by 32 rows");
 };
 
-// mbar_wait for a barrier that threads of the other CTA arrive on.
+// A wait for a barrier that threads of the other CTA arrive on.
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -47,10 +47,10 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
                                                   uint64_t limit_ns) {
   // (the second test, of a phase that is complete, has the other CTA's writes acquired)
-  return mbar_wait(bar, parity, abort, status, limit_ns) && try_wait_cluster(bar, parity);
+  return warp_wait(bar, parity, abort, status, limit_ns) && __all_sync(0xFFFFFFFFu, try_wait_cluster(bar, parity));
 }
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {   // on the first CTA's barrier
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(smem_u32(bar), 0)) : "memory");
@@ -165,54 +165,50 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      int stage = 0, slot = 0, buf = 0;
-      uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
-        if (!(ok = mbar_wait_cluster(&acc_empty[buf], acc_phase ^ 1u, abort_flag, status, wait_ns))) break;
+  } else if (warp == 1 && rank == 0) {
+    const bool one = elect_one();
+    int stage = 0, slot = 0, buf = 0;
+    uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+      if (!(ok = warp_wait_cluster(&acc_empty[buf], acc_phase ^ 1u, abort_flag, status, wait_ns))) break;
+      const uint32_t d = tmem + buf * kBN;
+      for (int kb = 0; kb < blocks; ++kb) {
+        const uint32_t sfa = tmem + C::kSfBase + slot * C::kSlotCols, sfb = sfa + kSfCols;
+        if ((kb & 3) == 0 && !(ok = warp_wait_cluster(&sf_full[slot], sf_phase, abort_flag, status, wait_ns))) break;
+        if (!(ok = warp_wait(&full[stage], phase, abort_flag, status, wait_ns))) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * kBN;
-        for (int kb = 0; kb < blocks; ++kb) {
-          const uint32_t sfa = tmem + C::kSfBase + slot * C::kSlotCols, sfb = sfa + kSfCols;
+        const uint32_t sf_at = smem_u32(smem + C::kSf + slot * C::kSlotBytes), at = smem_u32(smem + stage * C::kStageBytes);
+        const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + C::kABytes);
+        const uint32_t idesc = idesc_mx8(kM, kBN) | mx8_byte(kb & 3);
+        if (one) {
           if ((kb & 3) == 0) {
-            if (!(ok = mbar_wait_cluster(&sf_full[slot], sf_phase, abort_flag, status, wait_ns))) break;
-            tc_fence_after();
-            const uint32_t at = smem_u32(smem + C::kSf + slot * C::kSlotBytes);
 #pragma unroll
-            for (int i = 0; i < 1 + C::kBCopies; ++i) scales_to_tmem<2>(sfa + i * kSfCols, at + i * kSfBytes);
+            for (int i = 0; i < 1 + C::kBCopies; ++i) scales_to_tmem<2>(sfa + i * kSfCols, sf_at + i * kSfBytes);
           }
-          if (!(ok = mbar_wait(&full[stage], phase, abort_flag, status, wait_ns))) break;
-          tc_fence_after();
-          const uint32_t at = smem_u32(smem + stage * C::kStageBytes);
-          const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + C::kABytes);
-          const uint32_t idesc = idesc_mx8(kM, kBN) | mx8_byte(kb & 3);
 #pragma unroll
           for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
             umma_mx8<2>(d, da + 2 * k, db + 2 * k, idesc, sfa, sfb, kb > 0 || k > 0);
           commit_pair(&empty[stage]);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if ((kb & 3) == 3 || kb == blocks - 1) {
-            commit_pair(&sf_empty[slot]);
-            if (++slot == C::kSlots) {
-              slot = 0;
-              sf_phase ^= 1u;
-            }
-          }
+          if ((kb & 3) == 3 || kb == blocks - 1) commit_pair(&sf_empty[slot]);
+          if (kb == blocks - 1) commit_pair(&acc_full[buf]);
         }
-        if (!ok) break;
-        commit_pair(&acc_full[buf]);
-        if (++buf == C::kBufs) {
-          buf = 0;
-          acc_phase ^= 1u;
+        __syncwarp();
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (((kb & 3) == 3 || kb == blocks - 1) && ++slot == C::kSlots) {
+          slot = 0;
+          sf_phase ^= 1u;
         }
       }
-      commit_pair(drained);   // (whatever was issued)
+      if (++buf == C::kBufs) {
+        buf = 0;
+        acc_phase ^= 1u;
+      }
     }
+    if (one) commit_pair(drained);   // (whatever was issued)
   } else if (warp == 2) {
     int slot = 0;
     uint32_t phase = 0;
