@@ -292,7 +292,7 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t rows, uint64_t cols, uint64_t ld_bytes,
-            uint32_t box_cols, uint32_t box_rows) {
+            uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   static EncodeFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -306,17 +306,17 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld_bytes};
   const cuuint32_t box[2] = {box_cols, box_rows}, one[2] = {1, 1};
   return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rows, cols, ld, kBlockK, box_rows);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rows, cols, ld, kBlockK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows) {
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.T, a.N, 2 * a.ldo, 64, box_rows);
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.T, a.N, 2 * a.ldo, 32, box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches) {

@@ -22,7 +22,7 @@ struct Cfg {
   static constexpr int kSlots = 2;   // of scale words, four blocks of K each
   static constexpr int kBCopies = (kBN + 127) / 128;
   static constexpr uint32_t kSlotBytes = (1 + kBCopies) * kSfBytes;
-  static constexpr uint32_t kOutBytes = 4 * 32 * 128;   // an epilogue warp's 32 rows of 64 bf16
+  static constexpr uint32_t kOutBytes = 4 * 2 * 32 * 64;   // an epilogue warp's 32 rows of 32 bf16, twice
   static constexpr int kStages = (232448 - 1024 - 512 - kOutBytes - kSlots * kSlotBytes) / kStageBytes;
   static constexpr uint32_t kOut = kStages * kStageBytes;
   static constexpr uint32_t kSf = kOut + kOutBytes;
@@ -241,7 +241,37 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     }
   } else if (warp >= 4) {
     const int quad = warp & 3;
-    const uint32_t stage_out = smem_u32(smem + C::kOut) + quad * 32 * 128;
+    const uint32_t stage_out = smem_u32(smem + C::kOut) + quad * 2 * 32 * 64;
+    uint32_t half = 0;   // of the staging rows: one is written while the other leaves
+    // 32 columns of this lane's row, as 16 pairs
+    auto store = [&](const uint32_t* v, int col, int row0) {
+      if (col >= a.N || row0 >= a.T) return;
+      const uint32_t at = stage_out + half;
+      half ^= 32 * 64;
+      if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j)   // rows of 64 bytes in the 64-byte swizzle
+        sts_u4(at + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+      if (tma_out) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                           reinterpret_cast<uint64_t>(&mo)), "r"(at), "r"(col), "r"(row0)
+                       : "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      } else {
+        __syncwarp();
+        __nv_bfloat16* to = a.out + row0 * a.ldo + col + lane;
+        for (int r = 0; r < 32 && row0 + r < a.T; ++r) {
+          uint16_t x;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4) + (lane & 7) * 2));
+          if (col + lane < a.N) *reinterpret_cast<uint16_t*>(to + r * a.ldo) = x;
+        }
+      }
+    };
     int buf = 0;
     uint32_t phase = 0;
     for (int tile = blockIdx.x >> 1; tile < tiles; tile += step) {
@@ -251,56 +281,29 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], phase, abort_flag, status, wait_ns))) break;
       tc_fence_after();
       const uint32_t acc = tmem + buf * kBN + (static_cast<uint32_t>(quad * 32) << 16);
-      uint32_t v[kBN / 2];
+      // 32 columns at a time, packed to bf16; a single accumulator is given back before anything is stored
+      uint32_t v[C::kBufs == 1 ? kBN / 2 : 16];
 #pragma unroll
       for (int c = 0; c < kBN; c += 32) {
         uint32_t r[32];
         tmem_ld_32cols(acc + c, r);
         tmem_ld_wait();
+        uint32_t* to = v + (C::kBufs == 1 ? c / 2 : 0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[c / 2 + i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        for (int i = 0; i < 16; ++i) to[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        if (c + 32 == kBN) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first(&acc_empty[buf]);
+        }
+        if (C::kBufs > 1) store(v, col0 + c, row0);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_first(&acc_empty[buf]);
+      if (C::kBufs == 1)
+#pragma unroll
+        for (int c = 0; c < kBN; c += 32) store(v + c / 2, col0 + c, row0);
       if (++buf == C::kBufs) {
         buf = 0;
         phase ^= 1u;
-      }
-#pragma unroll
-      for (int c = 0; c < kBN; c += 64) {
-        if (col0 + c >= a.N || row0 >= a.T) break;
-        // the last chunk has left the staging rows
-        if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c + 8 * j < kBN)
-            sts_u4(stage_out + lane * 128 + ((j ^ (lane & 7)) << 4),
-                   make_uint4(v[c / 2 + 4 * j], v[c / 2 + 4 * j + 1], v[c / 2 + 4 * j + 2], v[c / 2 + 4 * j + 3]));
-        if (tma_out) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                             reinterpret_cast<uint64_t>(&mo)), "r"(stage_out), "r"(col0 + c), "r"(row0)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
-        } else {
-          __syncwarp();
-          const int cols = min(min(64, kBN - c), a.N - col0 - c);
-          for (int r = 0; r < 32 && row0 + r < a.T; ++r) {
-            __nv_bfloat16* to = a.out + (row0 + r) * a.ldo + col0 + c;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = lane + 32 * h;
-              uint16_t x;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(stage_out + r * 128 + (((i >> 3) ^ (r & 7)) << 4) + (i & 7) * 2));
-              if (i < cols) *reinterpret_cast<uint16_t*>(to + i) = x;
-            }
-          }
-        }
       }
     }
     if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -366,6 +369,6 @@ int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
 
 }  // namespace
 
-int linear8_wide_launch(const Linear8& a, int* status, cudaStream_t stream) { return launch_wide<256>(a, status, stream); }
+int linear8_wide_launch(const Linear8& a, int* status, cudaStream_t stream) { return launch_wide<224>(a, status, stream); }
 
 }  // namespace moe
