@@ -11,28 +11,31 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;   // 4 warps: copies, MMAs, scales, tensor memory; 4 warps: the epilogue
-constexpr int kM = 256;         // tokens of a pair's tile
+constexpr int kThreads = 384;   // 4 warps: copies, MMAs, scales, tensor memory; 4 warps for each accumulator's epilogue
+constexpr int kRows = 256;      // tokens of an accumulator, 128 in each CTA
 
-template <int kBN>
+// Two accumulators of 256 x kBN: kAcc == 1, a tile's, in turn; kAcc == 2, the halves of a tile of 512 tokens.
+template <int kBN, int kAcc>
 struct Cfg {
-  static constexpr int kBufs = 2 * kBN <= 480 ? 2 : 1;   // accumulators
-  static constexpr uint32_t kABytes = kM / 2 * kBlockK, kBBytes = kBN / 2 * kBlockK;
-  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+  static constexpr int kM = kAcc * kRows;
+  static constexpr uint32_t kABytes = kRows / 2 * kBlockK, kBBytes = kBN / 2 * kBlockK;
+  static constexpr uint32_t kStageBytes = kAcc * kABytes + kBBytes;
   static constexpr int kSlots = 2;   // of scale words, four blocks of K each
-  static constexpr int kBCopies = (kBN + 127) / 128;
-  static constexpr uint32_t kSlotBytes = (1 + kBCopies) * kSfBytes;
-  static constexpr uint32_t kOutBytes = 4 * 2 * 32 * 64;   // an epilogue warp's 32 rows of 32 bf16, twice
+  static constexpr int kCopies = kAcc + (kBN + 127) / 128;   // of 128 rows: the tokens', the weights'
+  static constexpr uint32_t kSlotBytes = kCopies * kSfBytes;
+  static constexpr uint32_t kOutBytes = 8 * 2 * 32 * 64;   // an epilogue warp's 32 rows of 32 bf16, twice
   static constexpr int kStages = (232448 - 1024 - 512 - kOutBytes - kSlots * kSlotBytes) / kStageBytes;
   static constexpr uint32_t kOut = kStages * kStageBytes;
   static constexpr uint32_t kSf = kOut + kOutBytes;
   static constexpr uint32_t kCtl = kSf + kSlots * kSlotBytes;
   static constexpr uint32_t kSmem = kCtl + 512 + 1024;   // (1024: the ring's alignment)
-  static constexpr uint32_t kSfBase = kBufs * kBN;
-  static constexpr uint32_t kSlotCols = (1 + kBCopies) * kSfCols;
+  static constexpr uint32_t kSfBase = 2 * kBN;
+  static constexpr uint32_t kSlotCols = kCopies * kSfCols;
+  static constexpr int kChunk = kAcc;   // blocks of K that an accumulator takes before the other's turn
   static_assert(kSfBase + kSlots * kSlotCols <= 512, "tensor memory");
-  static_assert((2 * kStages + 2 * kSlots + 2 * kBufs + 1) * 8 + 16 <= 512, "control region");
+  static_assert((2 * kStages + 2 * kSlots + 4 + 1) * 8 + 16 <= 512, "control region");
   static_assert(kStageBytes % 1024 == 0 && kBN % 32 == 0, "swizzled tiles, scale words by 32 rows");
+  static_assert(kStages >= 2 * kChunk, "a chunk is loaded while one is multiplied");
 };
 
 // A wait for a barrier that threads of the other CTA arrive on.
@@ -82,12 +85,12 @@ struct Tiles {
   }
 };
 
-template <int kBN>
+template <int kBN, int kAcc>
 __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_constant__ CUtensorMap ma,
                                                                    const __grid_constant__ CUtensorMap mw,
                                                                    const __grid_constant__ CUtensorMap mo, Linear8 a, int tma_out,
                                                                    int* status, uint64_t wait_ns) {
-  using C = Cfg<kBN>;
+  using C = Cfg<kBN, kAcc>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kCtl);   // (the first CTA's)
@@ -95,14 +98,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
   uint64_t* sf_full = empty + C::kStages;                         // (the first CTA's)
   uint64_t* sf_empty = sf_full + C::kSlots;
   uint64_t* acc_full = sf_empty + C::kSlots;
-  uint64_t* acc_empty = acc_full + C::kBufs;                      // (the first CTA's)
-  uint64_t* drained = acc_empty + C::kBufs;
+  uint64_t* acc_empty = acc_full + 2;                             // (the first CTA's)
+  uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int blocks = (a.K + kBlockK - 1) / kBlockK;
-  const Tiles order{(a.T + kM - 1) / kM, (a.N + kBN - 1) / kBN};
+  const Tiles order{(a.T + C::kM - 1) / C::kM, (a.N + kBN - 1) / kBN};
   const int tiles = order.mt * order.nt, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       mbar_init(&sf_full[i], 2);
       mbar_init(&sf_empty[i], 1);
     }
-    for (int i = 0; i < C::kBufs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 8);
     }
@@ -150,13 +153,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
         int m, n;
         order.at(tile, &m, &n);
-        const int row_a = m * kM + rank * (kM / 2), row_b = n * kBN + rank * (kBN / 2);
+        const int row_a = m * C::kM + rank * (kRows / 2), row_b = n * kBN + rank * (kBN / 2);
         for (int kb = 0; kb < blocks; ++kb) {
           if (!(ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, status, wait_ns))) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
           const uint32_t at = smem_u32(smem + stage * C::kStageBytes), bar = cluster_addr(smem_u32(&full[stage]), 0);
-          tma_load_pair(at, &ma, bar, kb * kBlockK, row_a, pol);
-          tma_load_pair(at + C::kABytes, &mw, bar, kb * kBlockK, row_b, pol);
+#pragma unroll
+          for (int h = 0; h < kAcc; ++h) tma_load_pair(at + h * C::kABytes, &ma, bar, kb * kBlockK, row_a + h * kRows, pol);
+          tma_load_pair(at + kAcc * C::kABytes, &mw, bar, kb * kBlockK, row_b, pol);
           ++issued;
           if (++stage == C::kStages) {
             stage = 0;
@@ -167,45 +171,57 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     }
   } else if (warp == 1 && rank == 0) {
     const bool one = elect_one();
-    int stage = 0, slot = 0, buf = 0;
-    uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
+    int stage = 0, slot = 0, tile_no = 0;
+    uint32_t phase = 0, sf_phase = 0;
     bool ok = true;
-    for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
-      if (!(ok = warp_wait_cluster(&acc_empty[buf], acc_phase ^ 1u, abort_flag, status, wait_ns))) break;
-      const uint32_t d = tmem + buf * kBN;
-      for (int kb = 0; kb < blocks; ++kb) {
-        const uint32_t sfa = tmem + C::kSfBase + slot * C::kSlotCols, sfb = sfa + kSfCols;
-        if ((kb & 3) == 0 && !(ok = warp_wait_cluster(&sf_full[slot], sf_phase, abort_flag, status, wait_ns))) break;
-        if (!(ok = warp_wait(&full[stage], phase, abort_flag, status, wait_ns))) break;
-        tc_fence_after();
-        const uint32_t sf_at = smem_u32(smem + C::kSf + slot * C::kSlotBytes), at = smem_u32(smem + stage * C::kStageBytes);
-        const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + C::kABytes);
-        const uint32_t idesc = idesc_mx8(kM, kBN) | mx8_byte(kb & 3);
-        if (one) {
-          if ((kb & 3) == 0) {
+    for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step, ++tile_no) {
+      for (int k0 = 0; k0 < blocks && ok; k0 += C::kChunk) {
+        const uint32_t sfa = tmem + C::kSfBase + slot * C::kSlotCols, sfb = sfa + kAcc * kSfCols;
+        const bool first = (k0 & 3) == 0;   // of the slot's blocks
+        if (first && !(ok = warp_wait_cluster(&sf_full[slot], sf_phase, abort_flag, status, wait_ns))) break;
+        const int in = min(C::kChunk, blocks - k0);
+        const bool last = k0 + in == blocks;
 #pragma unroll
-            for (int i = 0; i < 1 + C::kBCopies; ++i) scales_to_tmem<2>(sfa + i * kSfCols, sf_at + i * kSfBytes);
+        for (int h = 0; h < kAcc; ++h) {
+          // the accumulator: given back by the epilogue before a tile's first block
+          const int acc = kAcc == 1 ? tile_no & 1 : h;
+          const uint32_t uses = kAcc == 1 ? tile_no >> 1 : tile_no;
+          if (k0 == 0 && !(ok = warp_wait_cluster(&acc_empty[acc], (uses & 1) ^ 1u, abort_flag, status, wait_ns))) break;
+          for (int i = 0; i < in; ++i) {
+            const bool wraps = stage + i >= C::kStages;
+            const int st = wraps ? stage + i - C::kStages : stage + i;
+            if (h == 0 && !(ok = warp_wait(&full[st], wraps ? phase ^ 1u : phase, abort_flag, status, wait_ns))) break;
+            tc_fence_after();
+            const uint32_t sf_at = smem_u32(smem + C::kSf + slot * C::kSlotBytes), at = smem_u32(smem + st * C::kStageBytes);
+            const uint64_t da = smem_desc_k128(at + h * C::kABytes), db = smem_desc_k128(at + kAcc * C::kABytes);
+            const uint32_t idesc = idesc_mx8(kRows, kBN) | mx8_byte((k0 + i) & 3);
+            if (one) {
+              if (h == 0 && first && i == 0) {
+#pragma unroll
+                for (int c = 0; c < C::kCopies; ++c) scales_to_tmem<2>(sfa + c * kSfCols, sf_at + c * kSfBytes);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
+                umma_mx8<2>(tmem + acc * kBN, da + 2 * k, db + 2 * k, idesc, sfa + h * kSfCols, sfb, k0 + i > 0 || k > 0);
+              if (h == kAcc - 1) commit_pair(&empty[st]);
+            }
+            __syncwarp();
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
-            umma_mx8<2>(d, da + 2 * k, db + 2 * k, idesc, sfa, sfb, kb > 0 || k > 0);
-          commit_pair(&empty[stage]);
-          if ((kb & 3) == 3 || kb == blocks - 1) commit_pair(&sf_empty[slot]);
-          if (kb == blocks - 1) commit_pair(&acc_full[buf]);
+          if (!ok) break;
+          if (one && last) commit_pair(&acc_full[acc]);
         }
+        if (!ok) break;
+        const bool slot_done = ((k0 + in) & 3) == 0 || last;
+        if (one && slot_done) commit_pair(&sf_empty[slot]);
         __syncwarp();
-        if (++stage == C::kStages) {
-          stage = 0;
+        if ((stage += in) >= C::kStages) {
+          stage -= C::kStages;
           phase ^= 1u;
         }
-        if (((kb & 3) == 3 || kb == blocks - 1) && ++slot == C::kSlots) {
+        if (slot_done && ++slot == C::kSlots) {
           slot = 0;
           sf_phase ^= 1u;
         }
-      }
-      if (++buf == C::kBufs) {
-        buf = 0;
-        acc_phase ^= 1u;
       }
     }
     if (one) commit_pair(drained);   // (whatever was issued)
@@ -218,18 +234,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       int m, n;
       order.at(tile, &m, &n);
       for (int g = 0; g < groups; ++g) {
-        const uint4 tok = scale_words(a.a_scales, a.las, m * kM + rank * (kM / 2), a.T, g);
-        uint32_t w[4 * C::kBCopies];
+        uint4 w[C::kCopies];
 #pragma unroll
-        for (int c = 0; c < 4 * C::kBCopies; ++c) {
-          const int row = n * kBN + 32 * c;
-          w[c] = c < kBN / 32 && row < a.N ? *reinterpret_cast<const uint32_t*>(a.w_scales + (row >> 7) * a.lws + 4 * g) : 0x7F7F7F7Fu;
+        for (int h = 0; h < kAcc; ++h) w[h] = scale_words(a.a_scales, a.las, m * C::kM + h * kRows + rank * (kRows / 2), a.T, g);
+#pragma unroll
+        for (int i = 0; i < C::kCopies - kAcc; ++i) {
+          uint32_t v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {   // one scale for 128 weight rows: the same for 32 rows of a tile
+            const int of = 128 * i + 32 * c, row = n * kBN + of;
+            v[c] = of < kBN && row < a.N ? *reinterpret_cast<const uint32_t*>(a.w_scales + (row >> 7) * a.lws + 4 * g) : 0x7F7F7F7Fu;
+          }
+          w[kAcc + i] = make_uint4(v[0], v[1], v[2], v[3]);
         }
         if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], phase ^ 1u, abort_flag, status, wait_ns)))) break;
         const uint32_t at = smem_u32(smem + C::kSf + slot * C::kSlotBytes) + lane * 16;
-        sts_u4(at, tok);
 #pragma unroll
-        for (int i = 0; i < C::kBCopies; ++i) sts_u4(at + (1 + i) * kSfBytes, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+        for (int i = 0; i < C::kCopies; ++i) sts_u4(at + i * kSfBytes, w[i]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_first(&sf_full[slot]);
@@ -240,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       }
     }
   } else if (warp >= 4) {
-    const int quad = warp & 3;
-    const uint32_t stage_out = smem_u32(smem + C::kOut) + quad * 2 * 32 * 64;
+    const int quad = warp & 3, acc_no = (warp >> 2) - 1;
+    const uint32_t stage_out = smem_u32(smem + C::kOut) + (warp - 4) * 2 * 32 * 64;
     uint32_t half = 0;   // of the staging rows: one is written while the other leaves
     // 32 columns of this lane's row, as 16 pairs
     auto store = [&](const uint32_t* v, int col, int row0) {
@@ -272,39 +293,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
         }
       }
     };
-    int buf = 0;
     uint32_t phase = 0;
-    for (int tile = blockIdx.x >> 1; tile < tiles; tile += step) {
+    const uint32_t acc = tmem + acc_no * kBN + (static_cast<uint32_t>(quad * 32) << 16);
+    for (int tile = (blockIdx.x >> 1) + (kAcc == 1 ? acc_no * step : 0); tile < tiles; tile += (kAcc == 1 ? 2 : 1) * step) {
       int m, n;
       order.at(tile, &m, &n);
-      const int row0 = m * kM + rank * (kM / 2) + quad * 32, col0 = n * kBN;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], phase, abort_flag, status, wait_ns))) break;
+      const int row0 = m * C::kM + (kAcc == 1 ? 0 : acc_no * kRows) + rank * (kRows / 2) + quad * 32, col0 = n * kBN;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[acc_no], phase, abort_flag, status, wait_ns))) break;
+      phase ^= 1u;
       tc_fence_after();
-      const uint32_t acc = tmem + buf * kBN + (static_cast<uint32_t>(quad * 32) << 16);
-      // 32 columns at a time, packed to bf16; a single accumulator is given back before anything is stored
-      uint32_t v[C::kBufs == 1 ? kBN / 2 : 16];
+      // packed to bf16 at once, so that the accumulator is given back before anything is stored
+      uint32_t v[kBN / 2];
 #pragma unroll
       for (int c = 0; c < kBN; c += 32) {
         uint32_t r[32];
         tmem_ld_32cols(acc + c, r);
         tmem_ld_wait();
-        uint32_t* to = v + (C::kBufs == 1 ? c / 2 : 0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) to[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        if (c + 32 == kBN) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_first(&acc_empty[buf]);
-        }
-        if (C::kBufs > 1) store(v, col0 + c, row0);
+        for (int i = 0; i < 16; ++i) v[c / 2 + i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
       }
-      if (C::kBufs == 1)
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_first(&acc_empty[acc_no]);
 #pragma unroll
-        for (int c = 0; c < kBN; c += 32) store(v + c / 2, col0 + c, row0);
-      if (++buf == C::kBufs) {
-        buf = 0;
-        phase ^= 1u;
-      }
+      for (int c = 0; c < kBN; c += 32) store(v + c / 2, col0 + c, row0);
     }
     if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -329,9 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
   }
 }
 
-template <int kBN>
+template <int kBN, int kAcc>
 int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
-  using C = Cfg<kBN>;
+  using C = Cfg<kBN, kAcc>;
   static std::mutex mu;
   static int pairs_of[64] = {};   // the pairs that fit a device at once
   int dev = 0, pairs = 0;
@@ -339,7 +351,7 @@ int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!pairs_of[dev]) {
-      if (cudaFuncSetAttribute(linear8_wide_kernel<kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+      if (cudaFuncSetAttribute(linear8_wide_kernel<kBN, kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
         return MOE_ERR_CUDA;
       cudaLaunchConfig_t q = {};
       q.gridDim = dim3(2);
@@ -351,24 +363,24 @@ int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
       at.val.clusterDim.y = at.val.clusterDim.z = 1;
       q.attrs = &at;
       q.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&pairs, linear8_wide_kernel<kBN>, &q) != cudaSuccess || pairs < 1) return MOE_ERR_CUDA;
+      if (cudaOccupancyMaxActiveClusters(&pairs, linear8_wide_kernel<kBN, kAcc>, &q) != cudaSuccess || pairs < 1) return MOE_ERR_CUDA;
       pairs_of[dev] = pairs;
     }
     pairs = pairs_of[dev];
   }
-  const long long tiles = static_cast<long long>((a.T + kM - 1) / kM) * ((a.N + kBN - 1) / kBN);
+  const long long tiles = static_cast<long long>((a.T + C::kM - 1) / C::kM) * ((a.N + kBN - 1) / kBN);
   if (tiles > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   CUtensorMap ma, mw, mo = {};
-  if (!linear8_map(&ma, a.a, a.T, a.K, a.lda, kM / 2) || !linear8_map(&mw, a.w, a.N, a.K, a.ldw, kBN / 2)) return MOE_ERR_CUDA;
+  if (!linear8_map(&ma, a.a, a.T, a.K, a.lda, kRows / 2) || !linear8_map(&mw, a.w, a.N, a.K, a.ldw, kBN / 2)) return MOE_ERR_CUDA;
   // whole boxes by TMA where the rows lie as it takes them
   const bool tma_out = a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && linear8_out_map(&mo, a, 32);
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-  return launch_chained_cluster(linear8_wide_kernel<kBN>, dim3(grid), dim3(kThreads), C::kSmem, stream, 2, ma, mw, mo, a,
+  return launch_chained_cluster(linear8_wide_kernel<kBN, kAcc>, dim3(grid), dim3(kThreads), C::kSmem, stream, 2, ma, mw, mo, a,
                                 tma_out ? 1 : 0, status, wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
 
-int linear8_wide_launch(const Linear8& a, int* status, cudaStream_t stream) { return launch_wide<224>(a, status, stream); }
+int linear8_wide_launch(const Linear8& a, int* status, cudaStream_t stream) { return launch_wide<224, 2>(a, status, stream); }
 
 }  // namespace moe
