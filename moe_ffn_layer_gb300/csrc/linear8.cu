@@ -303,7 +303,8 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t
       fn = reinterpret_cast<EncodeFn>(p);
   });
   if (!fn) return false;
-  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld_bytes};
+  // (a single row has no stride, but the map wants one)
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {rows == 1 ? 16 : ld_bytes};
   const cuuint32_t box[2] = {box_cols, box_rows}, one[2] = {1, 1};
   return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

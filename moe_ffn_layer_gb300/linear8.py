@@ -22,49 +22,72 @@ from . import binding as B
 from .kv_cache import _call, _current, _device
 
 
-class Block8(NamedTuple):
-    """A matrix in 8 bits."""
+# The calls are a few microseconds of kernels at decode sizes, and the host has to
+# keep ahead of them: the checks are a few comparisons a tensor, and results that
+# a call made itself are known by what they were made for when they come back as `into`.
+
+
+class _Block8(NamedTuple):
     codes: torch.Tensor
     scales: torch.Tensor
 
 
-class Norm8(NamedTuple):
-    """What ``rms_norm8`` gives; None for what was not asked for."""
+class Block8(_Block8):
+    """A matrix in 8 bits: codes, scales."""
+    _for = None     # what they were made for
+    _args = ()      # and where they lie
+
+
+class _Norm8(NamedTuple):
     codes: torch.Tensor | None
     scales: torch.Tensor | None
     h: torch.Tensor | None
     y: torch.Tensor | None
 
 
-def _empty8(rows, K, high, device) -> Block8:
+class Norm8(_Norm8):
+    """What ``rms_norm8`` gives: codes, scales, h, y; None for what was not asked for."""
+    _for = None
+    _args = ()
+
+
+_BF16, _U8 = torch.bfloat16, torch.uint8
+
+
+def _empty8(rows, K, high, device):
     # (rows of scales lie a multiple of 4 bytes apart: the product reads four at a time)
     blocks = -(-K // 128)
-    scales = torch.empty(-(-rows // high), -(-blocks // 4) * 4, dtype=torch.uint8, device=device)
-    return Block8(torch.empty(rows, K, dtype=torch.uint8, device=device), scales[:, :blocks])
+    scales = torch.empty(-(-rows // high), -(-blocks // 4) * 4, dtype=_U8, device=device)
+    return torch.empty(rows, K, dtype=_U8, device=device), scales[:, :blocks]
 
 
 def rows8(codes: torch.Tensor, scales: torch.Tensor) -> Block8:
     """Codes and scales from elsewhere (uint8 [R, K]; uint8 [.., ceil(K / 128)]),
     each copied where its rows do not lie as the calls here take them."""
     if codes.stride(1) != 1 or codes.stride(0) % 16 or codes.data_ptr() % 16:
-        codes = codes.contiguous() if codes.shape[1] % 16 == 0 and not codes.is_contiguous() else codes.clone()
+        codes = torch.empty(codes.shape, dtype=codes.dtype, device=codes.device).copy_(codes)
     if scales.stride(1) != 1 or scales.stride(0) % 4 or scales.data_ptr() % 4:
         padded = torch.empty(scales.shape[0], -(-scales.shape[1] // 4) * 4, dtype=scales.dtype, device=scales.device)
         scales = padded[:, :scales.shape[1]].copy_(scales)
     return Block8(codes, scales)
 
 
+def _is_rows(t, dtype, dev, shape):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and (t.stride(1) == 1 or shape[1] == 1)
+
+
 def _want_rows(name, t, dtype, dev, shape):
     """Raises ValueError unless t has that type, device and shape, its rows contiguous."""
-    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev or t.shape != shape or (t.stride(1) != 1 and t.shape[1] > 1):
+    if t.dim() != 2 or not _is_rows(t, dtype, dev, shape):
         raise ValueError(f"{name}: want {dtype} {tuple(shape)} with contiguous rows on device {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} of strides {tuple(t.stride())} on {t.device}")
 
 
-def _stride(t) -> int:
-    # (a single row's stride says nothing: the C call wants one that holds the row)
-    n = t.shape[1]
-    return t.stride(0) if t.shape[0] > 1 else -(-n // 16) * 16
+def _want_input(name, x):
+    """Raises ValueError unless x is a bf16 matrix with contiguous rows on a CUDA device."""
+    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError(f"{name}: want 2-d {_BF16} with contiguous rows on a CUDA device, got {x.dim()}-d {x.dtype} of "
+                         f"strides {tuple(x.stride())} on {x.device}")
 
 
 def _made(stream, device, make):
@@ -75,9 +98,19 @@ def _made(stream, device, make):
         return make()
 
 
-def _is_bf16_rows(name, x):
-    if x.dtype is not torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
-        raise ValueError(f"{name}: want 2-d torch.bfloat16 on a CUDA device, got {x.dim()}-d {x.dtype} on {x.device}")
+def _norm_into(into, want, x):
+    """Checks results that are to be written, and finds where they lie."""
+    shape, dev, outputs, plain = want
+    codes, scales, h, y = into
+    if (codes is None) != (outputs == "y") or (y is None) != (outputs == "codes") or (h is None) != plain:
+        raise ValueError(f"into: not the results of a call with outputs={outputs!r} and {'no' if plain else 'a'} residual")
+    args = [None, 0, None, 0, None, 0, None, 0]
+    for name, t, dtype, at, of in (("h", h, _BF16, 0, shape), ("y", y, _BF16, 2, shape), ("codes", codes, _U8, 4, shape),
+                                   ("scales", scales, _U8, 6, (shape[0], -(-shape[1] // 128)))):
+        if t is not None:
+            _want_rows("into." + name, t, dtype, dev, of)
+            args[at:at + 2] = t.data_ptr(), t.stride(0)
+    return tuple(args)
 
 
 def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -85,86 +118,83 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
     """h = x + residual (bf16), y = RMS norm of h's rows times weight.  x and
     residual bf16 [T, H], rows any multiple of 8 elements apart; weight bf16 [H]
     (None: ones).  outputs: "codes" (y in 8 bits), "y" (in bf16) or "both".
-    `into` takes the results of an earlier call of the same sizes; its h may be
-    x or residual themselves.  Without a residual, h is None (it would be x)."""
-    _is_bf16_rows("x", x)
-    if outputs not in ("codes", "y", "both"):
-        raise ValueError(f"outputs: want 'codes', 'y' or 'both', got {outputs!r}")
-    dev, shape = x.get_device(), x.shape
-    T, H = shape
-    bf16 = torch.bfloat16
+    `into` takes the results of an earlier call of the same sizes, or a Norm8 of
+    other tensors; its h may be x or residual themselves.  Without a residual, h is
+    None (it would be x)."""
+    _want_input("x", x)
+    shape, dev = x.shape, x.get_device()
     if _device() != dev:   # (the library works on the current device)
         with torch.cuda.device(dev):
             return rms_norm8(x, weight, eps, residual, outputs, into, stream)
+    T, H = shape
+    if residual is None:
+        r, r_stride = None, 0
+    else:
+        if not _is_rows(residual, _BF16, dev, shape):
+            _want_rows("residual", residual, _BF16, dev, shape)
+        r, r_stride = residual.data_ptr(), residual.stride(0)
+    if weight is not None and (weight.dtype is not _BF16 or weight.shape != shape[1:] or weight.get_device() != dev or
+                               not weight.is_contiguous()):
+        raise ValueError(f"weight: want contiguous {_BF16} ({H},) on {x.device}, got {weight.dtype} {tuple(weight.shape)} on {weight.device}")
+    want = (shape, dev, outputs, r is None)
     if into is None:
+        if outputs not in ("codes", "y", "both"):
+            raise ValueError(f"outputs: want 'codes', 'y' or 'both', got {outputs!r}")
+
         def make():
+            row = lambda: torch.empty(shape, dtype=_BF16, device=x.device)  # noqa: E731
             q = _empty8(T, H, 1, x.device) if outputs != "y" else (None, None)
-            return Norm8(*q, None if residual is None else torch.empty(shape, dtype=bf16, device=x.device),
-                         None if outputs == "codes" else torch.empty(shape, dtype=bf16, device=x.device))
+            return Norm8(*q, None if residual is None else row(), None if outputs == "codes" else row())
         into = _made(stream, x.device, make)
-    codes, scales, h, y = into
-    _want_rows("x", x, bf16, dev, shape)
-    if (codes is None) != (outputs == "y") or (y is None) != (outputs == "codes") or (h is None) != (residual is None):
-        raise ValueError(f"into: not the results of a call with outputs={outputs!r} and {'no' if residual is None else 'a'} residual")
-    args = [None, 0, None, 0, None, 0, None, 0]
-    if residual is not None:
-        _want_rows("residual", residual, bf16, dev, shape)
-        _want_rows("into.h", h, bf16, dev, shape)
-        args[0], args[1] = h.data_ptr(), _stride(h)
-    if weight is not None and (weight.dtype is not bf16 or weight.shape != (H,) or weight.get_device() != dev or not weight.is_contiguous()):
-        raise ValueError(f"weight: want contiguous {bf16} ({H},) on {x.device}, got {weight.dtype} {tuple(weight.shape)} on {weight.device}")
-    if y is not None:
-        _want_rows("into.y", y, bf16, dev, shape)
-        args[2], args[3] = y.data_ptr(), _stride(y)
-    if codes is not None:
-        _want_rows("into.codes", codes, torch.uint8, dev, shape)
-        _want_rows("into.scales", scales, torch.uint8, dev, (T, -(-H // 128)))
-        args[4:] = codes.data_ptr(), _stride(codes), scales.data_ptr(), _stride(scales)
+        into._args = _norm_into(into, want, x)
+        into._for = want
+    args = into._args if into._for == want else _norm_into(into, want, x)
     _call("moe_rms_norm8", B.lib().moe_rms_norm8(
-        x.data_ptr(), _stride(x), None if residual is None else residual.data_ptr(), 0 if residual is None else _stride(residual),
-        None if weight is None else weight.data_ptr(), eps, T, H, *args, _current(dev) if stream is None else B.handle(stream)))
+        x.data_ptr(), x.stride(0), r, r_stride, None if weight is None else weight.data_ptr(), eps, T, H, *args,
+        _current(dev) if stream is None else B.handle(stream)))
     return into
 
 
 def quantize8(x: torch.Tensor, silu_mul: bool = False, into: Block8 | None = None, stream=None) -> Block8:
     """The rows of x (bf16 [T, K], any multiple of 8 elements apart) in 8 bits;
     silu_mul: of SiLU(x[:, :K]) * x[:, K:], x bf16 [T, 2K].  `into` takes the
-    results of an earlier call of the same sizes."""
-    _is_bf16_rows("x", x)
-    T, K = x.shape
+    results of an earlier call of the same sizes, or a Block8 of other tensors."""
+    _want_input("x", x)
     dev = x.get_device()
     if _device() != dev:
         with torch.cuda.device(dev):
             return quantize8(x, silu_mul, into, stream)
+    T, K = x.shape
     if silu_mul:
         if K % 2:
             raise ValueError(f"x: want an even number of columns (gate, up), got {K}")
         K //= 2
+    want = (T, K, dev)
     if into is None:
-        into = _made(stream, x.device, lambda: _empty8(T, K, 1, x.device))
-    codes, scales = into
-    _want_rows("x", x, torch.bfloat16, dev, x.shape)
-    _want_rows("into.codes", codes, torch.uint8, dev, (T, K))
-    _want_rows("into.scales", scales, torch.uint8, dev, (T, -(-K // 128)))
-    _call("moe_quantize8", B.lib().moe_quantize8(
-        x.data_ptr(), _stride(x), T, K, 1 if silu_mul else 0, codes.data_ptr(), _stride(codes), scales.data_ptr(),
-        _stride(scales), _current(dev) if stream is None else B.handle(stream)))
+        into = Block8(*_made(stream, x.device, lambda: _empty8(T, K, 1, x.device)))
+    if into._for != want:
+        codes, scales = into
+        _want_rows("into.codes", codes, _U8, dev, (T, K))
+        _want_rows("into.scales", scales, _U8, dev, (T, -(-K // 128)))
+        into._args = (codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0))
+        into._for = want
+    _call("moe_quantize8", B.lib().moe_quantize8(x.data_ptr(), x.stride(0), T, K, 1 if silu_mul else 0, *into._args,
+                                                 _current(dev) if stream is None else B.handle(stream)))
     return into
 
 
 def quantize8_weight(w: torch.Tensor, stream=None) -> Block8:
     """A weight bf16 [N, K] (rows any multiple of 8 elements apart) in 8 bits, with
     a scale per block of 128 x 128."""
-    _is_bf16_rows("w", w)
+    _want_input("w", w)
     N, K = w.shape
     dev = w.get_device()
     if _device() != dev:
         with torch.cuda.device(dev):
             return quantize8_weight(w, stream)
-    codes, scales = made = _made(stream, w.device, lambda: _empty8(N, K, 128, w.device))
-    _want_rows("w", w, torch.bfloat16, dev, w.shape)
+    codes, scales = made = Block8(*_made(stream, w.device, lambda: _empty8(N, K, 128, w.device)))
     _call("moe_quantize8_weight", B.lib().moe_quantize8_weight(
-        w.data_ptr(), _stride(w), N, K, codes.data_ptr(), _stride(codes), scales.data_ptr(), _stride(scales),
+        w.data_ptr(), w.stride(0), N, K, codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0),
         _current(dev) if stream is None else B.handle(stream)))
     return made
 
@@ -179,13 +209,13 @@ class Linear8:
         self.N, self.K = codes.shape
         self.device, self._dev = codes.device, codes.get_device()
         self._blocks = -(-self.K // 128)
-        if codes.dtype is not torch.uint8:
-            raise ValueError(f"codes: want torch.uint8, got {codes.dtype}")
-        if scales.dtype is not torch.uint8 or scales.shape != (-(-self.N // 128), self._blocks) or scales.device != codes.device:
-            raise ValueError(f"scales: want torch.uint8 {(-(-self.N // 128), self._blocks)} on {codes.device}, got "
-                             f"{scales.dtype} {tuple(scales.shape)} on {scales.device}")
+        of = (-(-self.N // 128), self._blocks)
+        if codes.dtype is not _U8:
+            raise ValueError(f"codes: want {_U8}, got {codes.dtype}")
+        if scales.dtype is not _U8 or scales.shape != of or scales.device != codes.device:
+            raise ValueError(f"scales: want {_U8} {of} on {codes.device}, got {scales.dtype} {tuple(scales.shape)} on {scales.device}")
         self.codes, self.scales = rows8(codes, scales)
-        self._w = (self.codes.data_ptr(), _stride(self.codes), self.scales.data_ptr(), _stride(self.scales))
+        self._w = (self.codes.data_ptr(), self.codes.stride(0), self.scales.data_ptr(), self.scales.stride(0))
 
     @classmethod
     def from_weight(cls, w: torch.Tensor) -> "Linear8":
@@ -196,17 +226,19 @@ class Linear8:
         """out bf16 [T, N] = A W^T of A in 8 bits (codes uint8 [T, K], scales uint8
         [T, ceil(K / 128)], as ``rms_norm8`` and ``quantize8`` give them)."""
         T, dev = codes.shape[0], self._dev
-        _want_rows("codes", codes, torch.uint8, dev, (T, self.K))
-        _want_rows("scales", scales, torch.uint8, dev, (T, self._blocks))
+        if not (_is_rows(codes, _U8, dev, (T, self.K)) and _is_rows(scales, _U8, dev, (T, self._blocks))):
+            _want_rows("codes", codes, _U8, dev, (T, self.K))
+            _want_rows("scales", scales, _U8, dev, (T, self._blocks))
         if _device() != dev:
             with torch.cuda.device(dev):
                 return self.forward(codes, scales, out, stream)
         if out is None:
-            out = _made(stream, self.device, lambda: torch.empty(T, self.N, dtype=torch.bfloat16, device=self.device))
-        _want_rows("out", out, torch.bfloat16, dev, (T, self.N))
+            out = _made(stream, self.device, lambda: torch.empty(T, self.N, dtype=_BF16, device=self.device))
+        elif not _is_rows(out, _BF16, dev, (T, self.N)):
+            _want_rows("out", out, _BF16, dev, (T, self.N))
         _call("moe_linear8", B.lib().moe_linear8(
-            codes.data_ptr(), _stride(codes), scales.data_ptr(), _stride(scales), *self._w, T, self.N, self.K,
-            out.data_ptr(), out.stride(0) if T > 1 else self.N, _current(dev) if stream is None else B.handle(stream)))
+            codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), *self._w, T, self.N, self.K,
+            out.data_ptr(), out.stride(0), _current(dev) if stream is None else B.handle(stream)))
         return out
 
     __call__ = forward

@@ -358,7 +358,9 @@ def test_wrappers_refuse():
                 lambda: L8.rms_norm8(x, outputs="h"), lambda: L8.rms_norm8(x, torch.ones(256, device="cuda")),
                 lambda: L8.rms_norm8(x, residual=x[:3]), lambda: L8.rms_norm8(x, residual=x.cpu()),
                 lambda: L8.rms_norm8(x, into=L8.rms_norm8(x, outputs="y")),
-                lambda: L8.rms_norm8(x, residual=x, into=L8.rms_norm8(x)),
+                lambda: L8.rms_norm8(x, residual=x, into=L8.rms_norm8(x)), lambda: L8.rms_norm8(x[:2], into=L8.rms_norm8(x)),
+                lambda: L8.rms_norm8(x, into=L8.Norm8(q.codes, q.scales[:2], None, None)),
+                lambda: L8.quantize8(x[:3], into=q), lambda: L8.quantize8(x, into=L8.Block8(q.codes, q.scales.float())),
                 lambda: lin(x, q.scales), lambda: lin(q.codes[:, :128], q.scales), lambda: lin(q.codes, q.scales[:2]),
                 lambda: lin(*q, out=torch.empty(4, 39, device="cuda").bfloat16()), lambda: lin(*q, out=torch.empty(4, 40, device="cuda")),
                 lambda: L8.Linear8(q.codes, q.scales), lambda: L8.Linear8(x, q.scales)):

@@ -74,7 +74,7 @@ LINEAR = dict(a=P, lda=256, a_scales=P, las=4, w=P, ldw=256, w_scales=P, lws=4, 
     ("moe_quantize8", ROWS, dict(K=-16), INVALID),
     ("moe_quantize8_weight", WEIGHT, dict(w=None), INVALID),
     ("moe_quantize8_weight", WEIGHT, dict(N=-1), INVALID),
-    ("moe_quantize8_weight", WEIGHT, dict(lds=1), INVALID),
+    ("moe_quantize8_weight", WEIGHT, dict(N=400, lds=1), INVALID),
     ("moe_linear8", LINEAR, dict(a=None), INVALID),
     ("moe_linear8", LINEAR, dict(w_scales=None), INVALID),
     ("moe_linear8", LINEAR, dict(out=None), INVALID),
