@@ -6,7 +6,7 @@
 // its B operand, 16 to 128 columns, so that few tokens waste little of the MMA.
 // K is cut between the CTAs of a cluster, enough of them to draw the weights'
 // stream over every SM; each then sums its share of the tokens' partial sums, which
-// the others store into its shared memory, in the order of the ranks.
+// the others copy into its shared memory, in the order of the ranks.
 #include <mutex>
 
 #include "linear8.cuh"
@@ -21,16 +21,19 @@ template <int kNT>
 struct Cfg {
   static constexpr int kChains = kNT <= 32 ? 4 : 2;   // accumulators that the MMAs of a block take in turn
   static constexpr int kStages = kNT == 16 ? 5 : kNT == 32 ? 4 : kNT == 64 ? 3 : 4;
-  static constexpr int kLog = kNT == 16 ? 4 : kNT == 32 ? 5 : kNT == 64 ? 6 : 7;
   static constexpr int kSlots = 2;   // of scale words, four blocks of K each
   static constexpr uint32_t kStageBytes = kWideM * kBlockK + kNT * kBlockK;
-  static constexpr uint32_t kRecv = kStages * kStageBytes;                   // partial sums [rank][token][128] fp32
-  static constexpr uint32_t kSf = kRecv + kNT * kWideM * 4;                  // scale words: weights, tokens
+  static constexpr uint32_t kPart = kStages * kStageBytes;         // the others' partial sums [rank][token of the share][128] fp32
+  static constexpr uint32_t kSf = kPart + (kNT + 8) * kWideM * 4;  // scale words: weights, tokens
   static constexpr uint32_t kCtl = kSf + kSlots * 2 * kSfBytes;
-  static constexpr uint32_t kSmem = kCtl + (2 * kStages + 2 * kSlots + 1) * 8 + 48 + 1024;   // (1024: the ring's alignment)
-  static constexpr int kCols = (kChains * kNT < 32 ? 32 : kChains * kNT) + kSlots * 2 * kSfCols;
+  static constexpr uint32_t kSmem = kCtl + (2 * kStages + 2 * kSlots + 2) * 8 + 8 + 1024;   // (1024: the ring's alignment)
+  static constexpr int kCols = kChains * kNT + kSlots * 2 * kSfCols;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr uint32_t kSfBase = kChains * kNT;
+  static_assert(kNT * kWideM * 4 <= kStages * kStageBytes, "this CTA's partial sums take the ring's place");
+  // No two clusters' CTAs may each wait for tensor memory that a CTA of the other holds: as many CTAs
+  // as an SM's shared memory takes (of this kernel, or the others here) find room for their columns.
+  static_assert(kTmemCols * (kSmem <= 75 * 1024 ? 3 : kSmem <= 113 * 1024 ? 2 : 1) <= 512, "tensor memory of an SM's CTAs");
 };
 
 template <int kNT>
@@ -45,17 +48,40 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
   uint64_t* sf_full = empty + C::kStages;
   uint64_t* sf_empty = sf_full + C::kSlots;
   uint64_t* done = sf_empty + C::kSlots;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* parts = done + 1;   // the others' partial sums have come
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(parts + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* ok_of = reinterpret_cast<int*>(tmem_slot + 2);   // [8] whether each CTA of the cluster has its sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = blockIdx.x % split;   // == rank in the cluster
+  const int rank = blockIdx.x % split;   // == rank in the cluster
   const int n0 = blockIdx.x / split * kWideM, t0 = blockIdx.y * kNT;
   const int blocks = (a.K + kBlockK - 1) / kBlockK;
   const int kb0 = static_cast<int>(static_cast<long long>(blocks) * rank / split);
   const int kb1 = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / split);
+  // the tile's tokens, and those of them that each CTA sums, and this one
+  const int tokens = min(kNT, a.T - t0), share = (tokens + split - 1) / split;
+  const int first = rank * share, mine = min(share, tokens - first);
 
+  // the copies: started before the tensor memory is there, by the thread that made their barriers
+  int issued = 0;   // blocks of K whose copies were started
+  // (the weights are read once where one tile holds all tokens)
+  const uint64_t pol_w = gridDim.y == 1 ? l2_policy_evict_first() : l2_policy_evict_normal(), pol_a = l2_policy_evict_last();
+  auto load = [&](int kb, int stage) {
+    mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
+    uint8_t* at = smem + stage * C::kStageBytes;
+    tma_load_2d(at, &mw, &full[stage], kb * kBlockK, n0, pol_w);
+    tma_load_2d(at + kWideM * kBlockK, &ma, &full[stage], kb * kBlockK, t0, pol_a);
+    ++issued;
+  };
+  // a group's scale words: the tokens', and the tile's weight rows', which share one
+  uint4 sf_a;
+  uint32_t sf_w;
+  auto scales = [&](int g) {
+    sf_a = scale_words(a.a_scales, a.las, t0, a.T, g);
+    sf_w = *reinterpret_cast<const uint32_t*>(a.w_scales + static_cast<long long>(n0 >> 7) * a.lws + 4 * g);
+  };
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&mw);
+    tma_prefetch_desc(&ma);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -65,39 +91,34 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
       mbar_init(&sf_empty[i], 1);
     }
     mbar_init(done, 1);
+    mbar_init(parts, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    if (mine > 0 && split > 1) mbar_arrive_expect_tx(parts, (split - 1) * mine * kWideM * 4);
+    chain_wait();
+    for (int i = 0; i < C::kStages && kb0 + i < kb1; ++i) load(kb0 + i, i);
+  }
+  if (warp == 2) {
+    chain_wait();
+    scales(kb0 >> 2);
   }
   if (warp == 3) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
-  }
-  if (warp == 2 && lane == 0) {
-    tma_prefetch_desc(&mw);
-    tma_prefetch_desc(&ma);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (split > 1) cluster_arrive();   // (waited for before the first access to another CTA)
-  chain_wait();
-  ChainReleaseAtExit release;
 
-  int issued = 0;   // blocks of K whose copies were started
   if (warp == 0) {
     if (lane == 0) {
-      // the weights are read once where one tile holds all tokens
-      const uint64_t pol_w = gridDim.y == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-      const uint64_t pol_a = l2_policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++issued) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, status, wait_ns)) break;
-        mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
-        uint8_t* at = smem + stage * C::kStageBytes;
-        tma_load_2d(at, &mw, &full[stage], kb * kBlockK, n0, pol_w);
-        tma_load_2d(at + kWideM * kBlockK, &ma, &full[stage], kb * kBlockK, t0, pol_a);
+      for (int kb = kb0 + C::kStages; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty[stage], phase, abort_flag, status, wait_ns)) break;
+        load(kb, stage);
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -144,20 +165,23 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
     uint32_t phase = 0;
     const int g1 = (kb1 + 3) >> 2;
     for (int g = kb0 >> 2; g < g1; ++g) {
-      const uint4 tok = scale_words(a.a_scales, a.las, t0, a.T, g);
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(a.w_scales + static_cast<long long>(n0 >> 7) * a.lws + 4 * g);
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], phase ^ 1u, abort_flag, status, wait_ns))) break;
       const uint32_t at = smem_u32(smem + C::kSf + slot * 2 * kSfBytes) + lane * 16;
-      sts_u4(at, make_uint4(w, w, w, w));
-      sts_u4(at + kSfBytes, tok);
+      sts_u4(at, make_uint4(sf_w, sf_w, sf_w, sf_w));
+      sts_u4(at + kSfBytes, sf_a);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sf_full[slot]);
+      if (g + 1 < g1) scales(g + 1);
       if (++slot == C::kSlots) {
         slot = 0;
         phase ^= 1u;
       }
     }
+  } else {
+    // The next launch may set itself up meanwhile: this CTA holds its tensor memory (one that still
+    // had to get it could wait for a CTA that waits for this launch).
+    chain_release();
   }
   __syncwarp();
 
@@ -171,92 +195,94 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
       mbar_wait_timed(&full[i], ((issued - 1 - i) / C::kStages) & 1, status);
   }
   tc_fence_after();
-  float acc[kNT];
+  float* own = reinterpret_cast<float*>(smem);   // [token][128], where the ring was
   if (ok) {
     const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll
     for (int c = 0; c < kNT; c += 16) {
+      if (c >= tokens) break;
       uint32_t r[C::kChains][16];
 #pragma unroll
       for (int i = 0; i < C::kChains; ++i) tmem_ld_16cols(at + i * kNT + c, r[i]);
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        float s = __uint_as_float(r[0][j]);
+        float v = __uint_as_float(r[0][j]);
 #pragma unroll
-        for (int i = 1; i < C::kChains; ++i) s += __uint_as_float(r[i][j]);
-        acc[c + j] = s;
+        for (int i = 1; i < C::kChains; ++i) v += __uint_as_float(r[i][j]);
+        own[(c + j) * kWideM + threadIdx.x] = v;
       }
     }
   }
   tc_fence_before();
-  const bool pairs = (a.ldo & 1) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 3) == 0;
-  if (split == 1) {
-    if (ok) {
-      const int n = n0 + warp * 32 + lane;
-      if (pairs) {
-        // neighbouring lanes trade, so that the even one has both rows' sums of one token and the odd one of the next
-        const int np = n & ~1;
-#pragma unroll
-        for (int j = 0; j < kNT; j += 2) {
-          const float other = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? acc[j] : acc[j + 1], 1);
-          const int t = t0 + j + (lane & 1);
-          const uint32_t v = (lane & 1) ? pack_bf16x2(other, acc[j + 1]) : pack_bf16x2(acc[j], other);
-          if (t < a.T && np < a.N) {
-            __nv_bfloat16* to = a.out + t * a.ldo + np;
-            if (np + 1 < a.N) *reinterpret_cast<uint32_t*>(to) = v;
-            else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(v);
-          }
-        }
-      } else if (n < a.N) {
-#pragma unroll
-        for (int j = 0; j < kNT; ++j)
-          if (t0 + j < a.T) a.out[(t0 + j) * a.ldo + n] = __float2bfloat16_rn(acc[j]);
+  bool whole = ok;
+  if (split > 1) {
+    fence_proxy_async_smem();
+    cluster_wait();   // (every CTA has made its barrier; and this one's sums are in shared memory)
+    __syncthreads();
+    if (ok && threadIdx.x < split && threadIdx.x != rank) {
+      // to CTA r the sums of its tokens, counted on its barrier
+      const int r = threadIdx.x, n = min(share, tokens - r * share);
+      if (n > 0) {
+        const uint32_t to = cluster_addr(smem_u32(smem + C::kPart) + rank * share * kWideM * 4, r);
+        asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                     "r"(smem_u32(own + r * share * kWideM)), "r"(n * kWideM * 4), "r"(cluster_addr(smem_u32(parts), r))
+                     : "memory");
       }
     }
+    if (mine > 0) whole = mbar_wait(parts, 0, abort_flag, status, wait_ns) && ok;
+    __syncwarp();
+    cluster_arrive();   // what was sent here has come
   } else {
-    cluster_wait();
-    const int lg = __ffs(split) - 1, share = kNT >> lg;   // tokens of each CTA
-    if (threadIdx.x < split) {
-      const uint32_t to = cluster_addr(smem_u32(&ok_of[rank]), threadIdx.x);
-      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(ok ? 1 : 0) : "memory");
-    }
-    if (ok) {
-      const uint32_t mine = smem_u32(smem + C::kRecv) + (rank * share * kWideM + threadIdx.x) * 4;
+    __syncthreads();
+  }
+  if (whole) {
+    const int n = n0 + lane * 4;
+    const float4* part = reinterpret_cast<const float4*>(smem + C::kPart) + lane;
+    const float4* here = reinterpret_cast<const float4*>(own) + first * (kWideM / 4) + lane;
+    const int width = (reinterpret_cast<uintptr_t>(a.out) & 7) == 0 && (a.ldo & 3) == 0 && n + 4 <= a.N ? 4 : 1;
+    for (int j0 = warp; j0 < mine; j0 += 16) {   // four tokens at a time, in the order of the ranks
+      float4 s[4] = {};
+      for (int r = 0; r < split; ++r) {
+        const float4* from = r == rank ? here : part + r * share * (kWideM / 4);
+        float4 p[4] = {};
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) {
-        const uint32_t to = cluster_addr(mine, j >> (C::kLog - lg)) + (j & (share - 1)) * kWideM * 4;
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(acc[j]) : "memory");
+        for (int i = 0; i < 4; ++i)
+          if (j0 + 4 * i < mine) p[i] = from[(j0 + 4 * i) * (kWideM / 4)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[i].x += p[i].x;
+          s[i].y += p[i].y;
+          s[i].z += p[i].z;
+          s[i].w += p[i].w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (j0 + 4 * i >= mine) break;
+        __nv_bfloat16* to = a.out + (t0 + first + j0 + 4 * i) * a.ldo + n;
+        if (width == 4) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(s[i].x, s[i].y), pack_bf16x2(s[i].z, s[i].w));
+        } else {
+          const float v[4] = {s[i].x, s[i].y, s[i].z, s[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (n + k < a.N) to[k] = __float2bfloat16_rn(v[k]);
+        }
       }
     }
-    cluster_arrive();
-    cluster_wait();
-    bool all = true;
-    for (int r = 0; r < split; ++r) all = all && ok_of[r];
-    const int n = n0 + (threadIdx.x & 63) * 2;
-    if (all && n < a.N)
-      for (int j = threadIdx.x >> 6; j < share; j += 2) {
-        const int t = t0 + static_cast<int>(rank) * share + j;
-        if (t >= a.T) break;
-        float2 s = make_float2(0.f, 0.f);
-        for (int r = 0; r < split; ++r) {
-          const float2 p = *reinterpret_cast<const float2*>(smem + C::kRecv + ((r * share + j) * kWideM + (threadIdx.x & 63) * 2) * 4);
-          s.x += p.x;
-          s.y += p.y;
-        }
-        __nv_bfloat16* to = a.out + t * a.ldo + n;
-        if (pairs && n + 1 < a.N) {
-          *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(s.x, s.y);
-        } else {
-          to[0] = __float2bfloat16_rn(s.x);
-          if (n + 1 < a.N) to[1] = __float2bfloat16_rn(s.y);
-        }
-      }
   }
   __syncthreads();
   if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (split > 1) {
+    cluster_wait();   // no CTA leaves before its sums have been taken
+    if (!whole || wait_ns == 0) {   // given up: what the others sent may still be on its way
+      const uint64_t from = globaltimer();
+      while (globaltimer() - from < 1000000) __nanosleep(1000);
+    }
   }
 }
 
@@ -329,8 +355,10 @@ int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, 
   const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
   const int blocks = (a.K + kBlockK - 1) / kBlockK;
   const long long tiles = static_cast<long long>((a.N + kWideM - 1) / kWideM) * ((a.T + nt - 1) / nt);
-  int split = 1;
-  while (split < 8 && tiles * split < sms && blocks >= 2 * split) split *= 2;
+  // as many CTAs for each tile as fill the SMs once: a second CTA of an SM starts late
+  int split = tiles < sms ? static_cast<int>(sms / tiles) : 1;
+  split = split > 8 ? 8 : split;
+  split = split > blocks ? blocks : split;
   const int rc = nt == 16   ? launch_narrow<16>(a, split, status, stream)
                  : nt == 32 ? launch_narrow<32>(a, split, status, stream)
                  : nt == 64 ? launch_narrow<64>(a, split, status, stream)

@@ -140,8 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // The next launch may set itself up meanwhile: this CTA holds its tensor memory (one that still had
+  // to get it could wait for a CTA that waits for this launch).
+  chain_release();
   chain_wait();
-  ChainReleaseAtExit release;
 
   int issued = 0;   // blocks of K whose copies were started
   if (warp == 0) {

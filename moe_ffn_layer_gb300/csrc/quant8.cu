@@ -76,7 +76,7 @@ constexpr int kMaxNormWarps = 32;
 template <int kVecs>
 __global__ void __launch_bounds__(1024) rms_norm8_kernel(Norm8 a) {
   chain_wait();
-  ChainReleaseAtExit release;
+  chain_release();
   __shared__ float part[kMaxNormWarps];
   const long long row = blockIdx.x;
   const int n = a.H >> 3;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(1024) rms_norm8_kernel(Norm8 a) {
 template <int kAct>
 __global__ void __launch_bounds__(256) quantize8_kernel(Quantize8 a, uint32_t blocks_per_row, uint32_t blocks) {
   chain_wait();
-  ChainReleaseAtExit release;
+  chain_release();
   const uint32_t b = blockIdx.x * 16u + (threadIdx.x >> 4);
   const uint32_t row = b / blocks_per_row, col = (b - row * blocks_per_row) * 128u + (threadIdx.x & 15u) * 8u;
   const bool in = b < blocks && col < static_cast<uint32_t>(a.K);
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256) quantize8_kernel(Quantize8 a, uint32_t bl
 // A CTA per block of 128 x 128: 16 lanes a row, eight rows a thread.
 __global__ void __launch_bounds__(256) quantize8_weight_kernel(Quantize8 a, int N) {
   chain_wait();
-  ChainReleaseAtExit release;
+  chain_release();
   __shared__ float part[8];
   const int col = blockIdx.x * 128 + (threadIdx.x & 15) * 8, row0 = blockIdx.y * 128 + (threadIdx.x >> 4);
   float v[8][8], m = 0.f;
