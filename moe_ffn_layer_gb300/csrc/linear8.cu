@@ -20,32 +20,36 @@ constexpr int kWideM = 128;   // weight rows of a tile
 template <int kNT>
 struct Cfg {
   static constexpr int kChains = kNT <= 32 ? 4 : 2;   // accumulators that the MMAs of a block take in turn
-  static constexpr int kStages = kNT == 16 ? 5 : kNT == 32 ? 4 : kNT == 64 ? 3 : 4;
+  // stages of the ring: so many that one CTA fills an SM, or two do
+  static constexpr int kDeep = kNT == 16 ? 9 : kNT == 32 ? 8 : kNT == 64 ? 6 : 4;
+  static constexpr int kShallow = kNT == 16 ? 5 : kNT == 32 ? 4 : kNT == 64 ? 3 : 4;
   static constexpr int kSlots = 2;   // of scale words, four blocks of K each
   static constexpr uint32_t kStageBytes = kWideM * kBlockK + kNT * kBlockK;
-  static constexpr uint32_t kPart = kStages * kStageBytes;         // the others' partial sums [rank][token of the share][128] fp32
-  static constexpr uint32_t kSf = kPart + (kNT + 8) * kWideM * 4;  // scale words: weights, tokens
+  // behind the ring: the others' partial sums [rank][token of the share][128] fp32, scale words (weights, tokens), barriers
+  static constexpr uint32_t kSf = (kNT + 8) * kWideM * 4;
   static constexpr uint32_t kCtl = kSf + kSlots * 2 * kSfBytes;
-  static constexpr uint32_t kSmem = kCtl + (2 * kStages + 2 * kSlots + 2) * 8 + 8 + 1024;   // (1024: the ring's alignment)
+  static constexpr uint32_t kBehind = kCtl + (2 * kDeep + 2 * kSlots + 2) * 8 + 8;
+  static constexpr uint32_t smem(int stages) { return stages * kStageBytes + kBehind + 1024; }   // (1024: the ring's alignment)
   static constexpr int kCols = kChains * kNT + kSlots * 2 * kSfCols;
   static constexpr int kTmemCols = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr uint32_t kSfBase = kChains * kNT;
-  static_assert(kNT * kWideM * 4 <= kStages * kStageBytes, "this CTA's partial sums take the ring's place");
+  static_assert(kNT * kWideM * 4 <= kShallow * kStageBytes, "this CTA's partial sums take the ring's place");
   // No two clusters' CTAs may each wait for tensor memory that a CTA of the other holds: as many CTAs
   // as an SM's shared memory takes (of this kernel, or the others here) find room for their columns.
-  static_assert(kTmemCols * (kSmem <= 75 * 1024 ? 3 : kSmem <= 113 * 1024 ? 2 : 1) <= 512, "tensor memory of an SM's CTAs");
+  static_assert(smem(kShallow) > 75 * 1024 && kTmemCols * (smem(kShallow) <= 113 * 1024 ? 2 : 1) <= 512, "tensor memory of an SM's CTAs");
 };
 
 template <int kNT>
 __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_constant__ CUtensorMap mw,
-                                                                  const __grid_constant__ CUtensorMap ma, Linear8 a, int split,
+                                                                  const __grid_constant__ CUtensorMap ma, Linear8 a, int split, int stages,
                                                                   int* status, uint64_t wait_ns) {
   using C = Cfg<kNT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kCtl);
-  uint64_t* empty = full + C::kStages;
-  uint64_t* sf_full = empty + C::kStages;
+  uint8_t* behind = smem + stages * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(behind + C::kCtl);
+  uint64_t* empty = full + C::kDeep;
+  uint64_t* sf_full = empty + C::kDeep;
   uint64_t* sf_empty = sf_full + C::kSlots;
   uint64_t* done = sf_empty + C::kSlots;
   uint64_t* parts = done + 1;   // the others' partial sums have come
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&mw);
     tma_prefetch_desc(&ma);
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
     fence_barrier_init();
     if (mine > 0 && split > 1) mbar_arrive_expect_tx(parts, (split - 1) * mine * kWideM * 4);
     chain_wait();
-    for (int i = 0; i < C::kStages && kb0 + i < kb1; ++i) load(kb0 + i, i);
+    for (int i = 0; i < stages && kb0 + i < kb1; ++i) load(kb0 + i, i);
   }
   if (warp == 2) {
     chain_wait();
@@ -116,10 +120,10 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int kb = kb0 + C::kStages; kb < kb1; ++kb) {
+      for (int kb = kb0 + stages; kb < kb1; ++kb) {
         if (!mbar_wait(&empty[stage], phase, abort_flag, status, wait_ns)) break;
         load(kb, stage);
-        if (++stage == C::kStages) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
       if (group && !warp_wait(&sf_full[slot], sf_phase, abort_flag, status, wait_ns)) break;
       if (!warp_wait(&full[stage], phase, abort_flag, status, wait_ns)) break;
       tc_fence_after();
-      const uint32_t sf_at = smem_u32(smem + C::kSf + slot * 2 * kSfBytes), at = smem_u32(smem + stage * C::kStageBytes);
+      const uint32_t sf_at = smem_u32(behind + C::kSf + slot * 2 * kSfBytes), at = smem_u32(smem + stage * C::kStageBytes);
       const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + kWideM * kBlockK);
       const uint32_t idesc = idesc_mx8(kWideM, kNT) | mx8_byte(kb & 3);
       if (one) {
@@ -150,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
         if ((kb & 3) == 3) umma_commit(&sf_empty[slot]);
       }
       __syncwarp();
-      if (++stage == C::kStages) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
     const int g1 = (kb1 + 3) >> 2;
     for (int g = kb0 >> 2; g < g1; ++g) {
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], phase ^ 1u, abort_flag, status, wait_ns))) break;
-      const uint32_t at = smem_u32(smem + C::kSf + slot * 2 * kSfBytes) + lane * 16;
+      const uint32_t at = smem_u32(behind + C::kSf + slot * 2 * kSfBytes) + lane * 16;
       sts_u4(at, make_uint4(sf_w, sf_w, sf_w, sf_w));
       sts_u4(at + kSfBytes, sf_a);
       fence_proxy_async_smem();
@@ -191,8 +195,8 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
   if (!ok && threadIdx.x == 0) {
     // given up: the MMAs and copies in flight end before the CTA does (bounded waits)
     mbar_wait_timed(done, 0, status);
-    for (int i = 0; i < C::kStages && i < issued; ++i)
-      mbar_wait_timed(&full[i], ((issued - 1 - i) / C::kStages) & 1, status);
+    for (int i = 0; i < stages && i < issued; ++i)
+      mbar_wait_timed(&full[i], ((issued - 1 - i) / stages) & 1, status);
   }
   tc_fence_after();
   float* own = reinterpret_cast<float*>(smem);   // [token][128], where the ring was
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
       // to CTA r the sums of its tokens, counted on its barrier
       const int r = threadIdx.x, n = min(share, tokens - r * share);
       if (n > 0) {
-        const uint32_t to = cluster_addr(smem_u32(smem + C::kPart) + rank * share * kWideM * 4, r);
+        const uint32_t to = cluster_addr(smem_u32(behind) + rank * share * kWideM * 4, r);
         asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
                      "r"(smem_u32(own + r * share * kWideM)), "r"(n * kWideM * 4), "r"(cluster_addr(smem_u32(parts), r))
                      : "memory");
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
   }
   if (whole) {
     const int n = n0 + lane * 4;
-    const float4* part = reinterpret_cast<const float4*>(smem + C::kPart) + lane;
+    const float4* part = reinterpret_cast<const float4*>(behind) + lane;
     const float4* here = reinterpret_cast<const float4*>(own) + first * (kWideM / 4) + lane;
     const int width = (reinterpret_cast<uintptr_t>(a.out) & 7) == 0 && (a.ldo & 3) == 0 && n + 4 <= a.N ? 4 : 1;
     for (int j0 = warp; j0 < mine; j0 += 16) {   // four tokens at a time, in the order of the ranks
@@ -286,27 +290,61 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
   }
 }
 
+// How many clusters of `split` CTAs a device takes at once, with deep rings.
 template <int kNT>
-int launch_narrow(const Linear8& a, int split, int* status, cudaStream_t stream) {
+int clusters_at_once(int split) {
   using C = Cfg<kNT>;
   static std::mutex mu;
-  static bool ready[64] = {};
+  static int known[64][9] = {};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return MOE_ERR_CUDA;
-  {
-    std::lock_guard<std::mutex> lk(mu);
-    if (!ready[dev]) {
-      if (cudaFuncSetAttribute(linear8_narrow_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-        return MOE_ERR_CUDA;
-      ready[dev] = true;
-    }
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  int& n = known[dev][split];
+  if (!n) {
+    if (cudaFuncSetAttribute(linear8_narrow_kernel<kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(C::kDeep)) != cudaSuccess)
+      return 0;
+    cudaLaunchConfig_t q = {};
+    q.gridDim = dim3(split);
+    q.blockDim = dim3(kThreads);
+    q.dynamicSmemBytes = C::smem(C::kDeep);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    q.attrs = &at;
+    q.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, linear8_narrow_kernel<kNT>, &q) != cudaSuccess) n = 0;
   }
+  return n;
+}
+
+template <int kNT>
+int launch_narrow(const Linear8& a, int* status, cudaStream_t stream) {
+  using C = Cfg<kNT>;
+  const int blocks = (a.K + kBlockK - 1) / kBlockK;
+  const long long tiles = static_cast<long long>((a.N + kWideM - 1) / kWideM) * ((a.T + kNT - 1) / kNT);
+  if ((a.T + kNT - 1) / kNT > 65535 || !clusters_at_once<kNT>(1)) return MOE_ERR_CUDA;
+  // The most CTAs a tile that fit at once; 16 and 32 tokens: four, two CTAs an SM, where that many fit.
+  int split = 1, stages = C::kDeep;
+  if (kNT <= 32 && tiles <= 2 * clusters_at_once<kNT>(4) && tiles > clusters_at_once<kNT>(8)) {
+    split = 4;
+    if (tiles > clusters_at_once<kNT>(4)) stages = C::kShallow;
+  } else {
+    for (int s : {8, 4, 2})
+      if (tiles <= clusters_at_once<kNT>(s)) {
+        split = s;
+        break;
+      }
+    if (tiles > clusters_at_once<kNT>(1)) stages = C::kShallow;
+  }
+  if (split > blocks) split = blocks;
+  const int most = (blocks + split - 1) / split;   // no deeper than a CTA's blocks (so that the next launch finds room)
+  if (stages > most) stages = most < C::kShallow ? C::kShallow : most;
   CUtensorMap mw, ma;
   if (!linear8_map(&mw, a.w, a.N, a.K, a.ldw, kWideM) || !linear8_map(&ma, a.a, a.T, a.K, a.lda, kNT)) return MOE_ERR_CUDA;
   const dim3 grid((a.N + kWideM - 1) / kWideM * split, (a.T + kNT - 1) / kNT);
-  if (grid.y > 65535) return MOE_ERR_UNSUPPORTED;
-  return launch_chained_cluster(linear8_narrow_kernel<kNT>, grid, dim3(kThreads), C::kSmem, stream, split, mw, ma, a, split, status,
-                                wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_chained_cluster(linear8_narrow_kernel<kNT>, grid, dim3(kThreads), C::smem(stages), stream, split, mw, ma, a, split,
+                                stages, status, wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -347,22 +385,14 @@ bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows) {
 }
 
 int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches) {
-  if (a.T > 512) {
-    const int rc = linear8_wide_launch(a, status, stream);
-    if (rc == MOE_OK) ++*launches;
-    return rc;
-  }
-  const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
-  const int blocks = (a.K + kBlockK - 1) / kBlockK;
-  const long long tiles = static_cast<long long>((a.N + kWideM - 1) / kWideM) * ((a.T + nt - 1) / nt);
-  // as many CTAs for each tile as fill the SMs once: a second CTA of an SM starts late
-  int split = tiles < sms ? static_cast<int>(sms / tiles) : 1;
-  split = split > 8 ? 8 : split;
-  split = split > blocks ? blocks : split;
-  const int rc = nt == 16   ? launch_narrow<16>(a, split, status, stream)
-                 : nt == 32 ? launch_narrow<32>(a, split, status, stream)
-                 : nt == 64 ? launch_narrow<64>(a, split, status, stream)
-                            : launch_narrow<128>(a, split, status, stream);
+  // Tiles of 64 tokens while an SM each is enough for them, then of 128, then the pairs' tiles.
+  const long long wide = (a.N + kWideM - 1) / kWideM;
+  int rc;
+  if (a.T <= 16) rc = launch_narrow<16>(a, status, stream);
+  else if (a.T <= 32) rc = launch_narrow<32>(a, status, stream);
+  else if (a.T <= 64 || wide * ((a.T + 63) / 64) <= sms) rc = launch_narrow<64>(a, status, stream);
+  else if (wide * ((a.T + 127) / 128) <= sms) rc = launch_narrow<128>(a, status, stream);
+  else rc = linear8_wide_launch(a, status, sms, stream);
   if (rc == MOE_OK) ++*launches;
   return rc;
 }

@@ -104,6 +104,6 @@ bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
 bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows);
 
 // Many rows: tiles of 256 tokens by pairs of CTAs.
-int linear8_wide_launch(const Linear8& a, int* status, cudaStream_t stream);
+int linear8_wide_launch(const Linear8& a, int* status, int sms, cudaStream_t stream);
 
 }  // namespace moe

@@ -88,7 +88,7 @@ struct Tiles {
 template <int kBN, int kAcc>
 __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_constant__ CUtensorMap ma,
                                                                    const __grid_constant__ CUtensorMap mw,
-                                                                   const __grid_constant__ CUtensorMap mo, Linear8 a, int tma_out,
+                                                                   const __grid_constant__ CUtensorMap mo, Linear8 a, int out_vec,
                                                                    int* status, uint64_t wait_ns) {
   using C = Cfg<kBN, kAcc>;
   extern __shared__ uint8_t smem_raw[];
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
   if (warp == 2 && lane == 0) {
     tma_prefetch_desc(&ma);
     tma_prefetch_desc(&mw);
-    if (tma_out) tma_prefetch_desc(&mo);
+    if (out_vec == 16) tma_prefetch_desc(&mo);
   }
   tc_fence_before();
   __syncthreads();
@@ -271,12 +271,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       if (col >= a.N || row0 >= a.T) return;
       const uint32_t at = stage_out + half;
       half ^= 32 * 64;
-      if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      if (out_vec == 16 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; ++j)   // rows of 64 bytes in the 64-byte swizzle
         sts_u4(at + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-      if (tma_out) {
+      if (out_vec == 16) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -287,11 +287,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
         }
       } else {
         __syncwarp();
-        __nv_bfloat16* to = a.out + row0 * a.ldo + col + lane;
-        for (int r = 0; r < 32 && row0 + r < a.T; ++r) {
-          uint16_t x;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4) + (lane & 7) * 2));
-          if (col + lane < a.N) *reinterpret_cast<uint16_t*>(to + r * a.ldo) = x;
+        // rows as far as they go, in vectors of 8, 4 or 2 bytes: 8, 16 or 32 lanes a row
+        const int per = out_vec >> 1, lanes = 32 / per, c = lane % lanes * per;
+        __nv_bfloat16* to = a.out + row0 * a.ldo + col + c;
+#pragma unroll 4
+        for (int r = lane / lanes; r < 32; r += per) {
+          const uint32_t from = at + r * 64 + (((c >> 3) ^ (r >> 1 & 3)) << 4) + (c & 7) * 2;
+          if (row0 + r >= a.T) break;
+          if (out_vec == 8 && col + c + 4 <= a.N) {
+            *reinterpret_cast<uint2*>(to + r * a.ldo) = lds_u2(from);
+          } else if (out_vec == 4 && col + c + 2 <= a.N) {
+            uint32_t x;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(from));
+            *reinterpret_cast<uint32_t*>(to + r * a.ldo) = x;
+          } else {
+            for (int k = 0; k < per && col + c + k < a.N; ++k) {
+              uint16_t x;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(from + 2 * k));
+              *reinterpret_cast<uint16_t*>(to + r * a.ldo + k) = x;
+            }
+          }
         }
       }
     };
@@ -320,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
 #pragma unroll
       for (int c = 0; c < kBN; c += 32) store(v + c / 2, col0 + c, row0);
     }
-    if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (out_vec == 16 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   __syncthreads();
@@ -374,15 +389,22 @@ int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
   if (tiles > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   CUtensorMap ma, mw, mo = {};
   if (!linear8_map(&ma, a.a, a.T, a.K, a.lda, kRows / 2) || !linear8_map(&mw, a.w, a.N, a.K, a.ldw, kBN / 2)) return MOE_ERR_CUDA;
-  // whole boxes by TMA where the rows lie as it takes them
-  const bool tma_out = a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && linear8_out_map(&mo, a, 32);
+  // whole boxes by TMA where the rows lie as it takes them, else vectors of so many bytes
+  const uintptr_t lie = reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.T > 1 ? 2 * a.ldo : 0);
+  const int out_vec = lie % 16 == 0 ? 16 : lie % 8 == 0 ? 8 : lie % 4 == 0 ? 4 : 2;
+  if (out_vec == 16 && !linear8_out_map(&mo, a, 32)) return MOE_ERR_CUDA;
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
   return launch_chained_cluster(linear8_wide_kernel<kBN, kAcc>, dim3(grid), dim3(kThreads), C::kSmem, stream, 2, ma, mw, mo, a,
-                                tma_out ? 1 : 0, status, wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+                                out_vec, status, wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
 
-int linear8_wide_launch(const Linear8& a, int* status, cudaStream_t stream) { return launch_wide<224, 2>(a, status, stream); }
+int linear8_wide_launch(const Linear8& a, int* status, int sms, cudaStream_t stream) {
+  // A tile of 512 tokens takes 7/4 of the time of one of 256.
+  const long long n = (a.N + 223) / 224, pairs = sms / 2;
+  const long long one = (n * ((a.T + 255) / 256) + pairs - 1) / pairs, two = (n * ((a.T + 511) / 512) + pairs - 1) / pairs;
+  return 4 * one < 7 * two ? launch_wide<224, 1>(a, status, stream) : launch_wide<224, 2>(a, status, stream);
+}
 
 }  // namespace moe
