@@ -241,18 +241,23 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
     __syncthreads();
   }
   if (whole) {
-    const int n = n0 + lane * 4;
-    const float4* part = reinterpret_cast<const float4*>(behind) + lane;
-    const float4* here = reinterpret_cast<const float4*>(own) + first * (kWideM / 4) + lane;
-    const int width = (reinterpret_cast<uintptr_t>(a.out) & 7) == 0 && (a.ldo & 3) == 0 && n + 4 <= a.N ? 4 : 1;
+    // a lane's four weight rows: neighbours, stored as a vector, or 32 apart where the rows of `out` do not lie so
+    const bool vec = (reinterpret_cast<uintptr_t>(a.out) & 7) == 0 && ((a.ldo & 3) == 0 || a.T == 1) && n0 + kWideM <= a.N;
+    const int at = vec ? lane * 4 : lane, n = n0 + at;
+    const float* part = reinterpret_cast<const float*>(behind) + at;
+    const float* here = own + first * kWideM + at;
     for (int j0 = warp; j0 < mine; j0 += 16) {   // four tokens at a time, in the order of the ranks
       float4 s[4] = {};
       for (int r = 0; r < split; ++r) {
-        const float4* from = r == rank ? here : part + r * share * (kWideM / 4);
+        const float* from = r == rank ? here : part + r * share * kWideM;
         float4 p[4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (j0 + 4 * i < mine) p[i] = from[(j0 + 4 * i) * (kWideM / 4)];
+        for (int i = 0; i < 4; ++i) {
+          const float* q = from + (j0 + 4 * i) * kWideM;
+          if (j0 + 4 * i >= mine) continue;
+          if (vec) p[i] = *reinterpret_cast<const float4*>(q);
+          else p[i] = make_float4(q[0], q[32], q[64], q[96]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           s[i].x += p[i].x;
@@ -265,13 +270,13 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
       for (int i = 0; i < 4; ++i) {
         if (j0 + 4 * i >= mine) break;
         __nv_bfloat16* to = a.out + (t0 + first + j0 + 4 * i) * a.ldo + n;
-        if (width == 4) {
+        if (vec) {
           *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(s[i].x, s[i].y), pack_bf16x2(s[i].z, s[i].w));
         } else {
           const float v[4] = {s[i].x, s[i].y, s[i].z, s[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (n + k < a.N) to[k] = __float2bfloat16_rn(v[k]);
+            if (n + 32 * k < a.N) to[32 * k] = __float2bfloat16_rn(v[k]);
         }
       }
     }

@@ -85,10 +85,61 @@ struct Tiles {
   }
 };
 
+// 32 rows of bf16 pairs, a lane's each, to rows of any alignment, ldo apart: each lane the elements up to its
+// row's first 16-byte boundary; the rest, moved down so that vectors begin there, through shared memory (32 rows of
+// 128 bytes at `staging`), from where eight lanes store a row's vectors side by side.  (16384 x 2047 x 64: 149 us by
+// single elements.)
+template <int kPairs>
+__device__ __forceinline__ void store_rows(__nv_bfloat16* first, long long ldo, int rows, int cols, uint32_t staging,
+                                           uint32_t (&v)[kPairs]) {
+  const int lane = threadIdx.x & 31;
+  auto head_of = [&](const __nv_bfloat16* to) { return static_cast<int>(-(reinterpret_cast<uintptr_t>(to) >> 1) & 7); };
+  __nv_bfloat16* own = first + lane * ldo;
+  const int head = head_of(own);
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < min(head, cols) && lane < rows) *reinterpret_cast<uint16_t*>(own + i) = static_cast<uint16_t>(v[i >> 1] >> (16 * (i & 1)));
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const uint32_t next = i + 1 < kPairs ? v[i + 1] : 0u;
+    v[i] = head & 1 ? __byte_perm(v[i], next, 0x5432) : v[i];
+  }
+#pragma unroll
+  for (int i = 0; i + 1 < kPairs; ++i) v[i] = head & 2 ? v[i + 1] : v[i];
+#pragma unroll
+  for (int i = 0; i + 2 < kPairs; ++i) v[i] = head & 4 ? v[i + 2] : v[i];
+#pragma unroll
+  for (int c = 0; c < kPairs; c += 32) {   // 32 pairs: 8 vectors of a row
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + 4 * j < kPairs)
+        sts_u4(staging + lane * 128 + ((j ^ (lane & 7)) << 4), make_uint4(v[c + 4 * j], v[c + 4 * j + 1], v[c + 4 * j + 2], v[c + 4 * j + 3]));
+    __syncwarp();
+    const int j = lane & 7;
+    if (c + 4 * j < kPairs)
+#pragma unroll 2
+      for (int r = lane >> 3; r < rows; r += 4) {
+        __nv_bfloat16* to = first + r * ldo;
+        const int at = head_of(to) + 2 * c + 8 * j;
+        if (at >= cols) continue;
+        const uint4 x = lds_u4(staging + r * 128 + ((j ^ (r & 7)) << 4));
+        if (at + 8 <= cols) {
+          *reinterpret_cast<uint4*>(to + at) = x;
+        } else {
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 7; ++i)
+            if (at + i < cols) *reinterpret_cast<uint16_t*>(to + at + i) = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        }
+      }
+  }
+}
+
 template <int kBN, int kAcc>
 __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_constant__ CUtensorMap ma,
                                                                    const __grid_constant__ CUtensorMap mw,
-                                                                   const __grid_constant__ CUtensorMap mo, Linear8 a, int out_vec,
+                                                                   const __grid_constant__ CUtensorMap mo, Linear8 a, int tma_out,
                                                                    int* status, uint64_t wait_ns) {
   using C = Cfg<kBN, kAcc>;
   extern __shared__ uint8_t smem_raw[];
@@ -133,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
   if (warp == 2 && lane == 0) {
     tma_prefetch_desc(&ma);
     tma_prefetch_desc(&mw);
-    if (out_vec == 16) tma_prefetch_desc(&mo);
+    if (tma_out) tma_prefetch_desc(&mo);
   }
   tc_fence_before();
   __syncthreads();
@@ -266,48 +317,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     const int quad = warp & 3, acc_no = (warp >> 2) - 1;
     const uint32_t stage_out = smem_u32(smem + C::kOut) + (warp - 4) * 2 * 32 * 64;
     uint32_t half = 0;   // of the staging rows: one is written while the other leaves
-    // 32 columns of this lane's row, as 16 pairs
+    // 32 columns of this lane's row, as 16 pairs, through staging rows that leave by TMA
     auto store = [&](const uint32_t* v, int col, int row0) {
       if (col >= a.N || row0 >= a.T) return;
       const uint32_t at = stage_out + half;
       half ^= 32 * 64;
-      if (out_vec == 16 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; ++j)   // rows of 64 bytes in the 64-byte swizzle
         sts_u4(at + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-      if (out_vec == 16) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                           reinterpret_cast<uint64_t>(&mo)), "r"(at), "r"(col), "r"(row0)
-                       : "memory");
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-      } else {
-        __syncwarp();
-        // rows as far as they go, in vectors of 8, 4 or 2 bytes: 8, 16 or 32 lanes a row
-        const int per = out_vec >> 1, lanes = 32 / per, c = lane % lanes * per;
-        __nv_bfloat16* to = a.out + row0 * a.ldo + col + c;
-#pragma unroll 4
-        for (int r = lane / lanes; r < 32; r += per) {
-          const uint32_t from = at + r * 64 + (((c >> 3) ^ (r >> 1 & 3)) << 4) + (c & 7) * 2;
-          if (row0 + r >= a.T) break;
-          if (out_vec == 8 && col + c + 4 <= a.N) {
-            *reinterpret_cast<uint2*>(to + r * a.ldo) = lds_u2(from);
-          } else if (out_vec == 4 && col + c + 2 <= a.N) {
-            uint32_t x;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(from));
-            *reinterpret_cast<uint32_t*>(to + r * a.ldo) = x;
-          } else {
-            for (int k = 0; k < per && col + c + k < a.N; ++k) {
-              uint16_t x;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(from + 2 * k));
-              *reinterpret_cast<uint16_t*>(to + r * a.ldo + k) = x;
-            }
-          }
-        }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(&mo)), "r"(at), "r"(col), "r"(row0)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     };
     uint32_t phase = 0;
@@ -332,10 +358,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_first(&acc_empty[acc_no]);
+      if (tma_out) {
 #pragma unroll
-      for (int c = 0; c < kBN; c += 32) store(v + c / 2, col0 + c, row0);
+        for (int c = 0; c < kBN; c += 32) store(v + c / 2, col0 + c, row0);
+      } else {
+        store_rows(a.out + row0 * a.ldo + col0, a.ldo, min(32, a.T - row0), min(kBN, a.N - col0), stage_out, v);
+      }
     }
-    if (out_vec == 16 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
   __syncthreads();
@@ -389,13 +419,12 @@ int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
   if (tiles > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   CUtensorMap ma, mw, mo = {};
   if (!linear8_map(&ma, a.a, a.T, a.K, a.lda, kRows / 2) || !linear8_map(&mw, a.w, a.N, a.K, a.ldw, kBN / 2)) return MOE_ERR_CUDA;
-  // whole boxes by TMA where the rows lie as it takes them, else vectors of so many bytes
-  const uintptr_t lie = reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.T > 1 ? 2 * a.ldo : 0);
-  const int out_vec = lie % 16 == 0 ? 16 : lie % 8 == 0 ? 8 : lie % 4 == 0 ? 4 : 2;
-  if (out_vec == 16 && !linear8_out_map(&mo, a, 32)) return MOE_ERR_CUDA;
+  // by TMA where the rows lie as it takes them
+  const bool tma_out = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && (a.T == 1 || a.ldo % 8 == 0);
+  if (tma_out && !linear8_out_map(&mo, a, 32)) return MOE_ERR_CUDA;
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
   return launch_chained_cluster(linear8_wide_kernel<kBN, kAcc>, dim3(grid), dim3(kThreads), C::kSmem, stream, 2, ma, mw, mo, a,
-                                out_vec, status, wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+                                tma_out ? 1 : 0, status, wait_limit_ns()) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
