@@ -11,7 +11,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 384;   // 4 warps: copies, MMAs, scales, tensor memory; 4 warps for each accumulator's epilogue
+constexpr int kThreads = 384;   // 4 warps: copies, MMAs, scales, tensor memory; 8 warps: the epilogue
 constexpr int kRows = 256;      // tokens of an accumulator, 128 in each CTA
 
 // Two accumulators of 256 x kBN: kAcc == 1, a tile's, in turn; kAcc == 2, the halves of a tile of 512 tokens.
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], kAcc == 1 ? 16 : 8);
     }
     mbar_init(drained, 1);
     *abort_flag = 0;
@@ -191,21 +191,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The next launch may set itself up meanwhile: this CTA holds its tensor memory (one that still had
-  // to get it could wait for a CTA that waits for this launch).
-  chain_release();
-  chain_wait();
 
   int issued = 0;   // blocks of K whose copies were started
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_normal();
-      int stage = 0;
+      int stage = 0, m, n;
       uint32_t phase = 0;
       bool ok = true;
+      order.at(blockIdx.x >> 1, &m, &n);
+      chain_wait();
       for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
-        int m, n;
-        order.at(tile, &m, &n);
         const int row_a = m * C::kM + rank * (kRows / 2), row_b = n * kBN + rank * (kBN / 2);
         for (int kb = 0; kb < blocks; ++kb) {
           if (!(ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, status, wait_ns))) break;
@@ -220,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
             phase ^= 1u;
           }
         }
+        if (tile + step < tiles) order.at(tile + step, &m, &n);
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -283,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     uint32_t phase = 0;
     const int groups = (blocks + 3) >> 2;
     bool ok = true;
+    chain_wait();
     for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
       int m, n;
       order.at(tile, &m, &n);
@@ -313,8 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
         }
       }
     }
+  } else if (warp == 3) {
+    // The next launch may set itself up meanwhile: this CTA holds its tensor memory (one that still
+    // had to get it could wait for a CTA that waits for this launch).
+    chain_release();
   } else if (warp >= 4) {
-    const int quad = warp & 3, acc_no = (warp >> 2) - 1;
+    chain_wait();
+    const int quad = warp & 3, group = (warp >> 2) - 1;
     const uint32_t stage_out = smem_u32(smem + C::kOut) + (warp - 4) * 2 * 32 * 64;
     uint32_t half = 0;   // of the staging rows: one is written while the other leaves
     // 32 columns of this lane's row, as 16 pairs, through staging rows that leave by TMA
@@ -336,19 +339,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     };
+    // A group of four warps has an accumulator of its own (kAcc == 2), or half the columns of each in turn.
+    constexpr int kCols = kAcc == 2 ? kBN : (kBN + 63) / 64 * 32;
+    const int from = kAcc == 2 ? 0 : group * kCols, cols = min(kCols, kBN - from);
+    int acc_no = kAcc == 2 ? group : 0;
     uint32_t phase = 0;
-    const uint32_t acc = tmem + acc_no * kBN + (static_cast<uint32_t>(quad * 32) << 16);
-    for (int tile = (blockIdx.x >> 1) + (kAcc == 1 ? acc_no * step : 0); tile < tiles; tile += (kAcc == 1 ? 2 : 1) * step) {
+    for (int tile = blockIdx.x >> 1; tile < tiles; tile += step) {
       int m, n;
       order.at(tile, &m, &n);
-      const int row0 = m * C::kM + (kAcc == 1 ? 0 : acc_no * kRows) + rank * (kRows / 2) + quad * 32, col0 = n * kBN;
+      const int row0 = m * C::kM + (kAcc == 1 ? 0 : group * kRows) + rank * (kRows / 2) + quad * 32, col0 = n * kBN + from;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[acc_no], phase, abort_flag, status, wait_ns))) break;
-      phase ^= 1u;
       tc_fence_after();
+      const uint32_t acc = tmem + acc_no * kBN + from + (static_cast<uint32_t>(quad * 32) << 16);
       // packed to bf16 at once, so that the accumulator is given back before anything is stored
-      uint32_t v[kBN / 2];
+      uint32_t v[kCols / 2];
 #pragma unroll
-      for (int c = 0; c < kBN; c += 32) {
+      for (int c = 0; c < kCols; c += 32) {
+        if (c >= cols) break;
         uint32_t r[32];
         tmem_ld_32cols(acc + c, r);
         tmem_ld_wait();
@@ -358,11 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_first(&acc_empty[acc_no]);
+      if (kAcc == 2 || (acc_no ^= 1) == 0) phase ^= 1u;
       if (tma_out) {
 #pragma unroll
-        for (int c = 0; c < kBN; c += 32) store(v + c / 2, col0 + c, row0);
+        for (int c = 0; c < kCols; c += 32)
+          if (c < cols) store(v + c / 2, col0 + c, row0);
       } else {
-        store_rows(a.out + row0 * a.ldo + col0, a.ldo, min(32, a.T - row0), min(kBN, a.N - col0), stage_out, v);
+        store_rows(a.out + row0 * a.ldo + col0, a.ldo, min(32, a.T - row0), min(cols, a.N - col0), stage_out, v);
       }
     }
     if (tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

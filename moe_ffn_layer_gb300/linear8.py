@@ -57,8 +57,11 @@ _BF16, _U8 = torch.bfloat16, torch.uint8
 def _empty8(rows, K, high, device):
     # (rows of scales lie a multiple of 4 bytes apart: the product reads four at a time)
     blocks = -(-K // 128)
-    scales = torch.empty(-(-rows // high), -(-blocks // 4) * 4, dtype=_U8, device=device)
-    return torch.empty(rows, K, dtype=_U8, device=device), scales[:, :blocks]
+    of, apart = (-(-rows // high), blocks), -(-blocks // 4) * 4
+    # room for whole rows, the last one's too
+    scales = (torch.empty(of, dtype=_U8, device=device) if apart == blocks else
+              torch.empty((of[0], apart), dtype=_U8, device=device).as_strided(of, (apart, 1)))
+    return torch.empty((rows, K), dtype=_U8, device=device), scales
 
 
 def rows8(codes: torch.Tensor, scales: torch.Tensor) -> Block8:
@@ -192,11 +195,12 @@ def quantize8_weight(w: torch.Tensor, stream=None) -> Block8:
     if _device() != dev:
         with torch.cuda.device(dev):
             return quantize8_weight(w, stream)
-    codes, scales = made = Block8(*_made(stream, w.device, lambda: _empty8(N, K, 128, w.device)))
+    device = w.device
+    codes, scales = _empty8(N, K, 128, device) if stream is None else _made(stream, device, lambda: _empty8(N, K, 128, device))
     _call("moe_quantize8_weight", B.lib().moe_quantize8_weight(
         w.data_ptr(), w.stride(0), N, K, codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0),
         _current(dev) if stream is None else B.handle(stream)))
-    return made
+    return Block8(codes, scales)
 
 
 class Linear8:
@@ -225,19 +229,19 @@ class Linear8:
     def forward(self, codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """out bf16 [T, N] = A W^T of A in 8 bits (codes uint8 [T, K], scales uint8
         [T, ceil(K / 128)], as ``rms_norm8`` and ``quantize8`` give them)."""
-        T, dev = codes.shape[0], self._dev
-        if not (_is_rows(codes, _U8, dev, (T, self.K)) and _is_rows(scales, _U8, dev, (T, self._blocks))):
-            _want_rows("codes", codes, _U8, dev, (T, self.K))
+        T, K, N, dev = codes.shape[0], self.K, self.N, self._dev
+        if not (_is_rows(codes, _U8, dev, (T, K)) and _is_rows(scales, _U8, dev, (T, self._blocks))):
+            _want_rows("codes", codes, _U8, dev, (T, K))
             _want_rows("scales", scales, _U8, dev, (T, self._blocks))
         if _device() != dev:
             with torch.cuda.device(dev):
                 return self.forward(codes, scales, out, stream)
         if out is None:
-            out = _made(stream, self.device, lambda: torch.empty(T, self.N, dtype=_BF16, device=self.device))
-        elif not _is_rows(out, _BF16, dev, (T, self.N)):
-            _want_rows("out", out, _BF16, dev, (T, self.N))
+            out = _made(stream, self.device, lambda: torch.empty((T, N), dtype=_BF16, device=self.device))
+        elif not _is_rows(out, _BF16, dev, (T, N)):
+            _want_rows("out", out, _BF16, dev, (T, N))
         _call("moe_linear8", B.lib().moe_linear8(
-            codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), *self._w, T, self.N, self.K,
+            codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), *self._w, T, N, K,
             out.data_ptr(), out.stride(0), _current(dev) if stream is None else B.handle(stream)))
         return out
 
