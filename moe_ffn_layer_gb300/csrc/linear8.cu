@@ -393,7 +393,8 @@ int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, 
   // Tiles of 64 tokens while an SM each is enough for them, then of 128, then the pairs' tiles.
   const long long wide = (a.N + kWideM - 1) / kWideM;
   int rc;
-  if (a.T <= 16) rc = launch_narrow<16>(a, status, stream);
+  if (linear8_few_takes(a, sms)) rc = linear8_few_launch(a, stream);
+  else if (a.T <= 16) rc = launch_narrow<16>(a, status, stream);
   else if (a.T <= 32) rc = launch_narrow<32>(a, status, stream);
   else if (a.T <= 64 || wide * ((a.T + 63) / 64) <= sms) rc = launch_narrow<64>(a, status, stream);
   else if (wide * ((a.T + 127) / 128) <= sms) rc = launch_narrow<128>(a, status, stream);

@@ -1,0 +1,129 @@
+// Product of two 8-bit matrices with block scales for up to 8 rows of A: a stream of
+// the weights through registers.
+//
+// A CTA has 16 weight rows, its eight warps an eighth of K each, and adds their sums
+// in shared memory in the order of the warps: no barrier, copy engine or tensor
+// memory stands before the loads, and all of them are in flight at once (up to
+// 2048 values of K; beyond, a block at a time, with more CTAs an SM).  The codes
+// become f16, exactly, in registers, and are multiplied by 16 x 8 x 16 MMAs with
+// fp32 sums: any order of K serves the sum, so a thread's 16 neighbouring codes of a
+// row are its part of four MMAs.  A block's sum takes its scales when the block is
+// done.
+#include "linear8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 16;   // weight rows of a CTA
+constexpr int kTokens = 8;
+
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t codes) {   // two codes, the first in the low byte
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(codes)));
+  return d;
+}
+
+// d += a b over 16 values of K: a 16 rows, b 8 columns.
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// x += d times the scales of two exponent bytes, whose product may pass what one fp32 factor holds: then by two.
+__device__ __forceinline__ void add_scaled(float& x0, float d0, float& x1, float d1, int a, int w) {
+  const int e = a + w - 127;   // biased
+  if (a != 255 && w != 255 && e > 0 && e < 255) {
+    const float f = __int_as_float(e << 23);
+    x0 = fmaf(d0, f, x0);
+    x1 = fmaf(d1, f, x1);
+    return;
+  }
+  const int e1 = max(1, min(254, e)), e2 = max(1, e - e1 + 127);
+  const float f1 = __int_as_float(e1 << 23), f2 = a == 255 || w == 255 ? __int_as_float(0x7FFFFFFF) : __int_as_float(e2 << 23);
+  x0 = fmaf(d0 * f1, f2, x0);
+  x1 = fmaf(d1 * f1, f2, x1);
+}
+
+template <int kBatch>   // blocks of K whose loads a warp issues together
+__global__ void __launch_bounds__(kThreads, kBatch == 1 ? 3 : 2) linear8_few_kernel(Linear8 a) {
+  __shared__ float part[kWarps][kTokens][kRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * kRows;
+  const int blocks = (a.K + kBlockK - 1) / kBlockK;
+  const int b0 = blocks * warp / kWarps, b1 = blocks * (warp + 1) / kWarps;
+  // rows beyond the last weight read it again; their sums are not stored
+  const uint8_t* w0 = a.w + min(n0 + g, a.N - 1) * a.ldw + 16 * t;
+  const uint8_t* w1 = a.w + min(n0 + g + 8, a.N - 1) * a.ldw + 16 * t;
+  const uint8_t* sw = a.w_scales + static_cast<long long>(n0 >> 7) * a.lws;
+  const uint8_t* x = a.a + min(g, a.T - 1) * a.lda + 16 * t;   // (columns beyond the last token have its sums, which are not stored)
+  const uint8_t* sa[2] = {a.a_scales + min(2 * t, a.T - 1) * a.las, a.a_scales + min(2 * t + 1, a.T - 1) * a.las};
+  float total[4] = {};
+  chain_wait();
+  chain_release();
+  for (int b = b0; b < b1; b += kBatch) {
+    uint4 w[kBatch][2][2], v[kBatch][2];
+    int ew[kBatch], ea[kBatch][2];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = (b + i) * kBlockK, left = b + i < b1 ? a.K - k - 16 * t : 0;   // values from this lane's on
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool in = left > 64 * j;
+        w[i][j][0] = in ? __ldcs(reinterpret_cast<const uint4*>(w0 + k + 64 * j)) : zero;
+        w[i][j][1] = in ? __ldcs(reinterpret_cast<const uint4*>(w1 + k + 64 * j)) : zero;
+        v[i][j] = in ? *reinterpret_cast<const uint4*>(x + k + 64 * j) : zero;
+      }
+      const int at = min(b + i, b1 - 1);
+      ew[i] = sw[at];
+      ea[i][0] = sa[0][at];
+      ea[i][1] = sa[1][at];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (b + i >= b1) break;
+      float d[4] = {};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t p[4] = {w[i][j][0].x, w[i][j][0].y, w[i][j][0].z, w[i][j][0].w};
+        const uint32_t q[4] = {w[i][j][1].x, w[i][j][1].y, w[i][j][1].z, w[i][j][1].w};
+        const uint32_t y[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          mma16(d, f16x2_of(p[m]), f16x2_of(q[m]), f16x2_of(p[m] >> 16), f16x2_of(q[m] >> 16), f16x2_of(y[m]), f16x2_of(y[m] >> 16));
+      }
+      add_scaled(total[0], d[0], total[2], d[2], ea[i][0], ew[i]);
+      add_scaled(total[1], d[1], total[3], d[3], ea[i][1], ew[i]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) part[warp][2 * t + (k & 1)][g + 8 * (k >> 1)] = total[k];
+  __syncthreads();
+  const int n = threadIdx.x & 15, tok = threadIdx.x >> 4;
+  if (tok < a.T && n0 + n < a.N) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += part[i][tok][n];
+    a.out[tok * a.ldo + n0 + n] = __float2bfloat16_rn(s);
+  }
+}
+
+}  // namespace
+
+// Where it is the faster one (the tensor-memory kernel's time in parentheses): 1 x 2048 x 2048 2.5 (4.7) us,
+// 1 x 4096 x 2048 3.4 (5.5), 8 x 6144 x 4096 7.3 (8.9); not where a warp has more than four blocks of K one after
+// the other (1 x 8192 x 8192 20.7 (15.0)) or the CTAs do not fit at once (1 x 16384 x 4096 16.9 (14.0)).
+bool linear8_few_takes(const Linear8& a, int sms) {
+  return a.T <= kTokens && a.K <= 4 * kWarps * kBlockK && (a.N + kRows - 1) / kRows <= 3 * sms;
+}
+
+int linear8_few_launch(const Linear8& a, cudaStream_t stream) {
+  const dim3 grid((a.N + kRows - 1) / kRows);
+  return launch_chained(a.K <= 2 * kWarps * kBlockK ? linear8_few_kernel<2> : linear8_few_kernel<1>, grid, dim3(kThreads), 0, stream, a) ==
+             cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace moe
