@@ -17,7 +17,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 16;   // weight rows of a CTA
-constexpr int kTokens = 8;
 
 __device__ __forceinline__ uint32_t f16x2_of(uint32_t codes) {   // two codes, the first in the low byte
   uint32_t d;
@@ -47,9 +46,10 @@ __device__ __forceinline__ void add_scaled(float& x0, float d0, float& x1, float
   x1 = fmaf(d1 * f1, f2, x1);
 }
 
-template <int kBatch>   // blocks of K whose loads a warp issues together
+// kBatch blocks of K whose loads a warp issues together, kTiles of eight tokens.
+template <int kBatch, int kTiles>
 __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 3 : 2) linear8_few_kernel(Linear8 a) {
-  __shared__ float part[kWarps][kTokens][kRows];
+  __shared__ float part[kWarps][8 * kTiles][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kRows;
   const int blocks = (a.K + kBlockK - 1) / kBlockK;
@@ -58,14 +58,20 @@ __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 3 : 2) linear8_few_ker
   const uint8_t* w0 = a.w + min(n0 + g, a.N - 1) * a.ldw + 16 * t;
   const uint8_t* w1 = a.w + min(n0 + g + 8, a.N - 1) * a.ldw + 16 * t;
   const uint8_t* sw = a.w_scales + static_cast<long long>(n0 >> 7) * a.lws;
-  const uint8_t* x = a.a + min(g, a.T - 1) * a.lda + 16 * t;   // (columns beyond the last token have its sums, which are not stored)
-  const uint8_t* sa[2] = {a.a_scales + min(2 * t, a.T - 1) * a.las, a.a_scales + min(2 * t + 1, a.T - 1) * a.las};
-  float total[4] = {};
+  // (columns beyond the last token have its sums, which are not stored)
+  const uint8_t *x[kTiles], *sa[kTiles][2];
+#pragma unroll
+  for (int c = 0; c < kTiles; ++c) {
+    x[c] = a.a + min(8 * c + g, a.T - 1) * a.lda + 16 * t;
+    sa[c][0] = a.a_scales + min(8 * c + 2 * t, a.T - 1) * a.las;
+    sa[c][1] = a.a_scales + min(8 * c + 2 * t + 1, a.T - 1) * a.las;
+  }
+  float total[kTiles][4] = {};
   chain_wait();
   chain_release();
   for (int b = b0; b < b1; b += kBatch) {
-    uint4 w[kBatch][2][2], v[kBatch][2];
-    int ew[kBatch], ea[kBatch][2];
+    uint4 w[kBatch][2][2], v[kBatch][kTiles][2];
+    int ew[kBatch], ea[kBatch][kTiles][2];
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -75,32 +81,46 @@ __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 3 : 2) linear8_few_ker
         const bool in = left > 64 * j;
         w[i][j][0] = in ? __ldcs(reinterpret_cast<const uint4*>(w0 + k + 64 * j)) : zero;
         w[i][j][1] = in ? __ldcs(reinterpret_cast<const uint4*>(w1 + k + 64 * j)) : zero;
-        v[i][j] = in ? *reinterpret_cast<const uint4*>(x + k + 64 * j) : zero;
+#pragma unroll
+        for (int c = 0; c < kTiles; ++c) v[i][c][j] = in ? *reinterpret_cast<const uint4*>(x[c] + k + 64 * j) : zero;
       }
       const int at = min(b + i, b1 - 1);
       ew[i] = sw[at];
-      ea[i][0] = sa[0][at];
-      ea[i][1] = sa[1][at];
+#pragma unroll
+      for (int c = 0; c < kTiles; ++c) {
+        ea[i][c][0] = sa[c][0][at];
+        ea[i][c][1] = sa[c][1][at];
+      }
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (b + i >= b1) break;
-      float d[4] = {};
+      float d[kTiles][4] = {};
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t p[4] = {w[i][j][0].x, w[i][j][0].y, w[i][j][0].z, w[i][j][0].w};
         const uint32_t q[4] = {w[i][j][1].x, w[i][j][1].y, w[i][j][1].z, w[i][j][1].w};
-        const uint32_t y[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          mma16(d, f16x2_of(p[m]), f16x2_of(q[m]), f16x2_of(p[m] >> 16), f16x2_of(q[m] >> 16), f16x2_of(y[m]), f16x2_of(y[m] >> 16));
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t a0 = f16x2_of(p[m]), a1 = f16x2_of(q[m]), a2 = f16x2_of(p[m] >> 16), a3 = f16x2_of(q[m] >> 16);
+#pragma unroll
+          for (int c = 0; c < kTiles; ++c) {
+            const uint32_t y[4] = {v[i][c][j].x, v[i][c][j].y, v[i][c][j].z, v[i][c][j].w};
+            mma16(d[c], a0, a1, a2, a3, f16x2_of(y[m]), f16x2_of(y[m] >> 16));
+          }
+        }
       }
-      add_scaled(total[0], d[0], total[2], d[2], ea[i][0], ew[i]);
-      add_scaled(total[1], d[1], total[3], d[3], ea[i][1], ew[i]);
+#pragma unroll
+      for (int c = 0; c < kTiles; ++c) {
+        add_scaled(total[c][0], d[c][0], total[c][2], d[c][2], ea[i][c][0], ew[i]);
+        add_scaled(total[c][1], d[c][1], total[c][3], d[c][3], ea[i][c][1], ew[i]);
+      }
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) part[warp][2 * t + (k & 1)][g + 8 * (k >> 1)] = total[k];
+  for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) part[warp][8 * c + 2 * t + (k & 1)][g + 8 * (k >> 1)] = total[c][k];
   __syncthreads();
   const int n = threadIdx.x & 15, tok = threadIdx.x >> 4;
   if (tok < a.T && n0 + n < a.N) {
@@ -117,13 +137,13 @@ __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 3 : 2) linear8_few_ker
 // 1 x 4096 x 2048 3.4 (5.5), 8 x 6144 x 4096 7.3 (8.9); not where a warp has more than four blocks of K one after
 // the other (1 x 8192 x 8192 20.7 (15.0)) or the CTAs do not fit at once (1 x 16384 x 4096 16.9 (14.0)).
 bool linear8_few_takes(const Linear8& a, int sms) {
-  return a.T <= kTokens && a.K <= 4 * kWarps * kBlockK && (a.N + kRows - 1) / kRows <= 3 * sms;
+  return a.T <= 16 && a.K <= 4 * kWarps * kBlockK && (a.N + kRows - 1) / kRows <= 3 * sms;
 }
 
 int linear8_few_launch(const Linear8& a, cudaStream_t stream) {
-  const dim3 grid((a.N + kRows - 1) / kRows);
-  return launch_chained(a.K <= 2 * kWarps * kBlockK ? linear8_few_kernel<2> : linear8_few_kernel<1>, grid, dim3(kThreads), 0, stream, a) ==
-             cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const bool once = a.K <= 2 * kWarps * kBlockK;
+  auto kernel = a.T <= 8 ? (once ? linear8_few_kernel<2, 1> : linear8_few_kernel<1, 1>) : (once ? linear8_few_kernel<2, 2> : linear8_few_kernel<1, 2>);
+  return launch_chained(kernel, dim3((a.N + kRows - 1) / kRows), dim3(kThreads), 0, stream, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe

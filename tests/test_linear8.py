@@ -222,7 +222,8 @@ SIZES = [(1, 1, 16), (1, 128, 128), (1, 4096, 2048), (2, 40, 144), (7, 129, 272)
          (16, 384, 640), (17, 128, 1024), (31, 513, 80), (33, 130, 528), (63, 2048, 768), (64, 1000, 128), (65, 64, 2064),
          (127, 300, 256), (128, 256, 512), (129, 257, 1040), (200, 2500, 2000), (255, 77, 64), (256, 512, 2048),
          (257, 1030, 384), (400, 255, 1536), (511, 8, 128), (513, 2049, 192), (1000, 640, 896), (1500, 3000, 1168),
-         (2049, 1025, 336), (4100, 264, 160)]
+         (2049, 1025, 336), (4100, 264, 160),
+         (1, 300, 4112), (5, 129, 8208), (16, 130, 4128), (9, 7400, 272), (3, 20000, 80), (16, 257, 2064), (12, 16, 4096)]
 
 
 @pytest.mark.parametrize("T,N,K", SIZES)
@@ -232,30 +233,32 @@ def test_linear(T, N, K):
     assert_linear(out, a, w)
 
 
-@pytest.mark.parametrize("T", [1, 5, 16, 40, 64, 100, 128, 300, 1024])
-def test_linear_exact(T):
+@pytest.mark.parametrize("T,N,K", [(1, 520, 1040), (5, 520, 1040), (5, 520, 4112), (16, 520, 1040), (16, 7400, 1040), (30, 520, 1040),
+                                   (40, 520, 1040), (64, 520, 4112), (100, 2000, 1040), (128, 520, 1040), (300, 8200, 1040),
+                                   (1024, 520, 1040), (1024, 5200, 528), (2100, 4520, 272)])
+def test_linear_exact(T, N, K):
     """Small whole numbers, whose sums fp32 holds: every bit, on every path."""
-    N, K = 520, 1040
     g = torch.Generator("cuda").manual_seed(T)
     x = torch.randint(-4, 5, (T, K), generator=g, device="cuda").float()
     m = torch.randint(-4, 5, (N, K), generator=g, device="cuda").float()
     e = lambda v: v.to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
-    sa = torch.randint(126, 129, (T, 9), generator=g, device="cuda", dtype=torch.uint8)
-    sw = torch.randint(126, 129, (5, 9), generator=g, device="cuda", dtype=torch.uint8)
+    sa = torch.randint(126, 129, (T, -(-K // 128)), generator=g, device="cuda", dtype=torch.uint8)
+    sw = torch.randint(126, 129, (-(-N // 128), -(-K // 128)), generator=g, device="cuda", dtype=torch.uint8)
     a, w = L8.rows8(e(x), sa), L8.rows8(e(m), sw)
     out = L8.Linear8(*w)(*a)
     ref = lo.linear(lo.values(np8(a.codes), np8(a.scales)), lo.values(np8(w.codes), np8(w.scales), 128))[0]
     assert torch.equal(out.cpu().view(torch.int16), torch.from_numpy(ref).float().bfloat16().view(torch.int16))
 
 
-@pytest.mark.parametrize("T,N,K", [(3, 200, 272), (70, 136, 400), (600, 300, 272)])
+@pytest.mark.parametrize("T,N,K", [(3, 200, 272), (2, 200, 4112), (20, 200, 272), (70, 136, 400), (600, 300, 272), (1100, 4300, 272)])
 def test_linear_strides_and_rows_behind(T, N, K):
     """Operands and outputs that lie in larger tensors; what is beyond them stays as it was."""
     big = torch.randint(0, 120, (T + 3, K + 48), dtype=torch.uint8, device="cuda")
-    bs = torch.randint(120, 130, (T + 3, 12), dtype=torch.uint8, device="cuda")
-    wide = torch.randint(0, 120, (N, K + 16), dtype=torch.uint8, device="cuda")
-    ws = torch.randint(120, 130, (-(-N // 128), 8), dtype=torch.uint8, device="cuda")
     nb = -(-K // 128)
+    apart = -(-nb // 4) * 4 + 4
+    bs = torch.randint(120, 130, (T + 3, apart + 4), dtype=torch.uint8, device="cuda")
+    wide = torch.randint(0, 120, (N, K + 16), dtype=torch.uint8, device="cuda")
+    ws = torch.randint(120, 130, (-(-N // 128), apart), dtype=torch.uint8, device="cuda")
     a, w = L8.Block8(big[:T, 16:16 + K], bs[:T, 4:4 + nb]), L8.Block8(wide[:, :K], ws[:, :nb])
     lin = L8.Linear8(*w)
     assert lin.codes.data_ptr() == wide.data_ptr()   # not copied
@@ -267,12 +270,12 @@ def test_linear_strides_and_rows_behind(T, N, K):
         assert (out[T:] == 7).all() and (out[:, :at] == 7).all() and (out[:, at + N:] == 7).all()
 
 
-@pytest.mark.parametrize("T", [2, 40, 200, 700])
-def test_linear_nan(T):
+@pytest.mark.parametrize("T,K", [(2, 528), (2, 4112), (14, 528), (40, 528), (200, 528), (700, 528), (6000, 528)])
+def test_linear_nan(T, K):
     """A NaN code or scale reaches its row or column, and nothing else."""
-    N, K = 300, 528
+    N = 300
     a, w = random8(T, K, 1, 1, 4), random8(N, K, 128, 2, 4)
-    a.codes[1, 527], a.scales[T - 1, 2] = 127, 255
+    a.codes[1, K - 1], a.scales[T - 1, 2] = 127, 255
     w.codes[5, 0], w.scales[2, 3] = 255, 255
     out = np64(L8.Linear8(*w)(*a))
     want = np.zeros((T, N), bool)
@@ -281,10 +284,10 @@ def test_linear_nan(T):
     assert (np.isnan(out) == want).all()
 
 
-@pytest.mark.parametrize("T", [3, 50, 300])
-def test_linear_far_scales(T):
+@pytest.mark.parametrize("T,K", [(3, 256), (3, 4112), (50, 256), (300, 256), (6000, 256)])
+def test_linear_far_scales(T, K):
     """Scales at both ends of their range, whose product is of ordinary size."""
-    N, K = 140, 256
+    N = 140
     a, w = random8(T, K, 1, 3, 1), random8(N, K, 128, 4, 1)
     for la, lw in ((1, 240), (247, 10)):
         a.scales.fill_(la)
@@ -292,7 +295,7 @@ def test_linear_far_scales(T):
         assert_linear(L8.Linear8(*w)(*a), a, w)
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 4096, 2048), (60, 640, 4096), (500, 1000, 1024)])
+@pytest.mark.parametrize("T,N,K", [(1, 4096, 2048), (4, 600, 8192), (60, 640, 4096), (500, 1000, 1024), (1500, 4000, 512)])
 def test_same_bits_again(T, N, K):
     a, w = random8(T, K, 1, 5), random8(N, K, 128, 6)
     lin = L8.Linear8(*w)
@@ -376,7 +379,8 @@ def test_wrappers_refuse():
     assert L8.rms_norm8(x[:0], residual=x[:0], outputs="both").y.shape == (0, 256)
 
 
-@pytest.mark.parametrize("T,N,K", [(3, 128, 256), (3, 300, 2048), (40, 520, 1024), (300, 2048, 512), (1100, 512, 640)])
+@pytest.mark.parametrize("T,N,K", [(3, 128, 4112), (3, 300, 8192), (3, 7400, 272), (20, 300, 2048), (40, 520, 1024), (300, 2048, 512),
+                                   (1100, 512, 640), (1200, 4100, 640)])
 def test_expired_waits_write_nothing(T, N, K):
     """With the wait limit at 0 a wait that is not complete at its first test expires: the product records it,
     lets its copies and MMAs in flight end, and writes nothing; the next call is clean."""
