@@ -151,6 +151,8 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
         into = _made(stream, x.device, make)
         into._args = _norm_into(into, want, x)
         into._for = want
+    elif not isinstance(into, Norm8):
+        into = Norm8(*into)
     args = into._args if into._for == want else _norm_into(into, want, x)
     _call("moe_rms_norm8", B.lib().moe_rms_norm8(
         x.data_ptr(), x.stride(0), r, r_stride, None if weight is None else weight.data_ptr(), eps, T, H, *args,
@@ -175,6 +177,8 @@ def quantize8(x: torch.Tensor, silu_mul: bool = False, into: Block8 | None = Non
     want = (T, K, dev)
     if into is None:
         into = Block8(*_made(stream, x.device, lambda: _empty8(T, K, 1, x.device)))
+    elif not isinstance(into, Block8):
+        into = Block8(*into)
     if into._for != want:
         codes, scales = into
         _want_rows("into.codes", codes, _U8, dev, (T, K))

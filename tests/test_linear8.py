@@ -257,8 +257,10 @@ def test_linear_strides_and_rows_behind(T, N, K):
     nb = -(-K // 128)
     apart = -(-nb // 4) * 4 + 4
     bs = torch.randint(120, 130, (T + 3, apart + 4), dtype=torch.uint8, device="cuda")
+    bs[:, :4] = bs[:, 4 + nb:] = 255   # NaN beside what is used
     wide = torch.randint(0, 120, (N, K + 16), dtype=torch.uint8, device="cuda")
     ws = torch.randint(120, 130, (-(-N // 128), apart), dtype=torch.uint8, device="cuda")
+    ws[:, nb:] = 255
     a, w = L8.Block8(big[:T, 16:16 + K], bs[:T, 4:4 + nb]), L8.Block8(wide[:, :K], ws[:, :nb])
     lin = L8.Linear8(*w)
     assert lin.codes.data_ptr() == wide.data_ptr()   # not copied
@@ -399,3 +401,77 @@ def test_expired_waits_write_nothing(T, N, K):
     assert (out == 5.0).all()
     assert torch.equal(lin(*a).view(torch.int16), fresh.view(torch.int16))
     assert B.moe_last_device_error(s) == 0
+
+
+def test_first_call_inside_a_capture():
+    """In a process that has made no call before."""
+    code = """
+import torch
+from moe_ffn_layer_gb300 import linear8 as L8
+x = torch.ones(600, 256, device="cuda").bfloat16()
+w = L8.Block8(torch.full((4000, 256), 56, dtype=torch.uint8, device="cuda"), torch.full((32, 4), 127, dtype=torch.uint8, device="cuda")[:, :2])
+lin, outs = L8.Linear8(*w), []
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for T in (1, 12, 20, 60, 128, 600):
+        n = L8.rms_norm8(x[:T], None, 0.0, x[:T])
+        outs.append(lin(n.codes, n.scales))
+graph.replay()
+torch.cuda.synchronize()
+assert all((o == 256).all() for o in outs), [o.float().mean() for o in outs]
+print("fine")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_calls_on_two_streams_at_once():
+    """Nothing is shared between calls: two streams' results are those of one after the other."""
+    work = []
+    for i, (T, N, K) in enumerate([(3, 4096, 2048), (50, 3000, 2048), (400, 1000, 1024), (1500, 4000, 512)]):
+        a, w = random8(T, K, 1, i), random8(N, K, 128, 9 + i)
+        work.append((L8.Linear8(*w), a))
+    want = [lin(*a) for lin, a in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for s, out, order in zip(streams, got, (work, work[::-1])):
+            with torch.cuda.stream(s):
+                out.append([lin(*a) for lin, a in order])
+    torch.cuda.synchronize()
+    for outs in got[0]:
+        assert all(torch.equal(o.view(torch.int16), x.view(torch.int16)) for o, x in zip(outs, want))
+    for outs in got[1]:
+        assert all(torch.equal(o.view(torch.int16), x.view(torch.int16)) for o, x in zip(outs[::-1], want))
+
+
+def test_offsets_past_32_bits():
+    """Rows whose bytes and elements lie past 2^32: quantised, normed and multiplied as the same rows by themselves."""
+    T, K = 1100000, 4096
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda").zero_()
+    at = torch.tensor([0, 1, 524288, 1048575, 1048576, T - 2, T - 1], device="cuda")
+    few = rows(len(at), K, 0, 11)
+    x[at] = few
+    q, want = L8.quantize8(x), L8.quantize8(few)
+    assert torch.equal(q.codes[at], want.codes) and torch.equal(q.scales[at], want.scales)
+    assert int(q.codes.count_nonzero()) == int(want.codes.count_nonzero())
+    n, some = L8.rms_norm8(x, None, 1e-6, x, "both"), L8.rms_norm8(few, None, 1e-6, few, "both")
+    for t, u in zip(n, some):
+        assert torch.equal(t[at].view(torch.uint8), u.view(torch.uint8))
+    del n, x
+    w = random8(40, K, 128, 3, 4)
+    lin = L8.Linear8(*w)
+    out, rest = lin(*q)[at], lin(*want)   # (by other kernels: the same up to the order of their sums)
+    assert (out.float() - rest.float()).abs().max() <= 2.0 ** -7 * rest.float().abs().max()
+    big = L8.Block8(q.codes[:1048600], q.scales[:1048600])   # as weights: 4 GB of rows
+    ones = torch.full((8208, 32), 127, dtype=torch.uint8, device="cuda")[:-(-1048600 // 128)]
+    a = random8(3, K, 1, 4, 4)
+    y = L8.Linear8(big.codes, ones)(*a)
+    ref, size = lo.linear(lo.values(np8(a.codes), np8(a.scales)), lo.VALUES[np8(big.codes[at[:5]])])
+    assert (np.abs(np64(y[:, at[:5]]) - ref) <= 2.0 ** -8 * np.abs(ref) + 160 * 2.0 ** -22 * size).all()
