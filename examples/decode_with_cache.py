@@ -6,7 +6,9 @@ brought back to a budget where it grows past a limit.
 
 Per call of ``DecoderLayer``: q, k, v = norm(x) Wqkv^T; append k, v; x += attend(q)
 Wo^T; x += MoEFFN(norm(x)).  (No positions and random weights: the layer shows
-how the calls fit together.)  All matmuls are this library's.
+how the calls fit together.)  All matmuls are this library's.  ``DecoderLayer8``
+has the same weights in 8 bits, multiplied by rows that the norm and the
+quantisation give in 8 bits; the second norm adds the attention's output as well.
 """
 from __future__ import annotations
 
@@ -21,6 +23,7 @@ from moe_ffn_layer_gb300 import binding as B  # noqa: E402
 from moe_ffn_layer_gb300 import synth  # noqa: E402
 from moe_ffn_layer_gb300.kv_cache import KVCache8  # noqa: E402
 from moe_ffn_layer_gb300.layer import MoEFFN  # noqa: E402
+from moe_ffn_layer_gb300.linear8 import Linear8, quantize8, rms_norm8  # noqa: E402
 
 
 class Pages:
@@ -80,13 +83,30 @@ class DecoderLayer:
         return x + self.ffn(norm(x))
 
 
-def make_layer(H=512, heads=8, kv_heads=2, D=64, page=32, pages=64, seed=0, device="cuda"):
+class DecoderLayer8(DecoderLayer):
+    """The layer with its projections in 8 bits."""
+
+    def __init__(self, w_qkv, w_o, ffn: MoEFFN, cache: KVCache8, heads: int):
+        super().__init__(w_qkv, w_o, ffn, cache, heads)
+        self.qkv, self.o = Linear8.from_weight(w_qkv), Linear8.from_weight(w_o)
+
+    def __call__(self, x, table, lens, cu, max_new, max_len, weights=None):
+        Hq, Hkv, D = self.heads, self.cache.kv_heads, self.cache.head_dim
+        n = rms_norm8(x)
+        qkv = self.qkv(n.codes, n.scales).view(-1, Hq + 2 * Hkv, D)
+        self.cache.append(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], table, lens, cu)
+        att = self.cache.attend(qkv[:, :Hq], table, lens, cu, max_new, max_len, weights=weights)
+        n = rms_norm8(self.o(*quantize8(att.view(-1, Hq * D))), residual=x, outputs="y")   # (the router takes bf16)
+        return n.h + self.ffn(n.y)
+
+
+def make_layer(H=512, heads=8, kv_heads=2, D=64, page=32, pages=64, seed=0, device="cuda", kind=DecoderLayer):
     g = torch.Generator(device).manual_seed(seed)
     mat = lambda n, k: (torch.randn(n, k, generator=g, device=device) * k ** -0.5).bfloat16()  # noqa: E731
     w = synth.Workload("example", 8, H, 8, 2, 256, 256, sigma_router=0.1)
     ffn = MoEFFN.from_inputs(synth.make_inputs(w, seed), w.k, device)
     cache = KVCache8(pages, kv_heads, D, page, device)
-    return DecoderLayer(mat((heads + 2 * kv_heads) * D, H), mat(H, heads * D), ffn, cache, heads)
+    return kind(mat((heads + 2 * kv_heads) * D, H), mat(H, heads * D), ffn, cache, heads)
 
 
 def serve(layer, prompts, steps, limit, budget, sink=4, recent=16, seed=1):
@@ -121,8 +141,9 @@ def serve(layer, prompts, steps, limit, budget, sink=4, recent=16, seed=1):
 
 
 if __name__ == "__main__":
-    layer = make_layer()
-    y, lens, evictions = serve(layer, [200, 75, 131], 120, limit=256, budget=128)
-    torch.cuda.synchronize()
-    print(f"lengths {lens}, {evictions} eviction(s), |y| = {float(y.float().norm()):.3f}, "
-          f"device status {B.moe_last_device_error(torch.cuda.current_stream())}")
+    for kind in (DecoderLayer, DecoderLayer8):
+        layer = make_layer(kind=kind)
+        y, lens, evictions = serve(layer, [200, 75, 131], 120, limit=256, budget=128)
+        torch.cuda.synchronize()
+        print(f"{kind.__name__}: lengths {lens}, {evictions} eviction(s), |y| = {float(y.float().norm()):.3f}, "
+              f"device status {B.moe_last_device_error(torch.cuda.current_stream())}")
