@@ -80,9 +80,22 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
 }
+// Such a warp's wait: tested again and again, since a suspended wait is woken late, within mbar_wait's limits.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
   if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) return true;
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, status, limit_ns)) != 0;
+  uint64_t from = 0;
+  for (uint32_t it = 1; limit_ns; ++it) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) return true;
+    if ((it & 255u) == 0) {
+      if (__any_sync(0xFFFFFFFFu, *abort)) return false;
+      const uint64_t now = globaltimer();
+      if (from == 0) from = now;
+      if (__any_sync(0xFFFFFFFFu, now - from > limit_ns)) break;
+    }
+  }
+  set_status(status, MOE_ERR_TIMEOUT);
+  *abort = 1;
+  return false;
 }
 
 // Scale words of rows row0 + lane + 32 c (c < 4) for the blocks 4 g .. 4 g + 3;

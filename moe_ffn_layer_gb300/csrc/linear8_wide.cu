@@ -194,30 +194,33 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
 
   int issued = 0;   // blocks of K whose copies were started
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
-      int stage = 0, m, n;
-      uint32_t phase = 0;
-      bool ok = true;
-      order.at(blockIdx.x >> 1, &m, &n);
-      chain_wait();
-      for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
-        const int row_a = m * C::kM + rank * (kRows / 2), row_b = n * kBN + rank * (kBN / 2);
-        for (int kb = 0; kb < blocks; ++kb) {
-          if (!(ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, status, wait_ns))) break;
+    const bool one = elect_one();
+    const uint64_t pol = l2_policy_evict_normal();
+    const uint32_t ring = smem_u32(smem), bars = cluster_addr(smem_u32(full), 0);
+    int stage = 0, m, n;
+    uint32_t phase = 0;
+    bool ok = true;
+    order.at(blockIdx.x >> 1, &m, &n);
+    chain_wait();
+    for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
+      const int row_a = m * C::kM + rank * (kRows / 2), row_b = n * kBN + rank * (kBN / 2);
+      for (int kb = 0; kb < blocks; ++kb) {
+        if (!(ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, status, wait_ns))) break;
+        const uint32_t at = ring + stage * C::kStageBytes, bar = bars + stage * 8;
+        if (one) {
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
-          const uint32_t at = smem_u32(smem + stage * C::kStageBytes), bar = cluster_addr(smem_u32(&full[stage]), 0);
 #pragma unroll
           for (int h = 0; h < kAcc; ++h) tma_load_pair(at + h * C::kABytes, &ma, bar, kb * kBlockK, row_a + h * kRows, pol);
           tma_load_pair(at + kAcc * C::kABytes, &mw, bar, kb * kBlockK, row_b, pol);
-          ++issued;
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (tile + step < tiles) order.at(tile + step, &m, &n);
+        __syncwarp();
+        ++issued;
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
+      if (tile + step < tiles) order.at(tile + step, &m, &n);
     }
   } else if (warp == 1 && rank == 0) {
     const bool one = elect_one();
