@@ -389,7 +389,8 @@ MOE_API int moe_kv_evict(const moe_kv_dims* d, const moe_kv_pool* src, const moe
  * aligned, lds % 4 == 0 (bytes of a row beyond ceil(K / 128) may be read, never
  * used or written: a last row of scales has room up to a multiple of 4).  bf16
  * rows are 16-byte aligned, strides multiples of 8.  The stride of a matrix of
- * one row is not looked at. */
+ * one row is not looked at.  The product reads codes fastest where their rows
+ * begin at multiples of 128 bytes. */
 
 /* RMS norm of rows, with the residual's addition:
  *   h[t] = bf16(x[t] + residual[t])  (residual NULL: h = x, and no h is stored)

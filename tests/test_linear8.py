@@ -258,7 +258,7 @@ def test_linear_strides_and_rows_behind(T, N, K):
     apart = -(-nb // 4) * 4 + 4
     bs = torch.randint(120, 130, (T + 3, apart + 4), dtype=torch.uint8, device="cuda")
     bs[:, :4] = bs[:, 4 + nb:] = 255   # NaN beside what is used
-    wide = torch.randint(0, 120, (N, K + 16), dtype=torch.uint8, device="cuda")
+    wide = torch.randint(0, 120, (N, -(-K // 128) * 128 + 128), dtype=torch.uint8, device="cuda")
     ws = torch.randint(120, 130, (-(-N // 128), apart), dtype=torch.uint8, device="cuda")
     ws[:, nb:] = 255
     a, w = L8.Block8(big[:T, 16:16 + K], bs[:T, 4:4 + nb]), L8.Block8(wide[:, :K], ws[:, :nb])
@@ -270,6 +270,11 @@ def test_linear_strides_and_rows_behind(T, N, K):
         assert lin(*a, out=view) is view
         assert_linear(view, a, w)
         assert (out[T:] == 7).all() and (out[:, :at] == 7).all() and (out[:, at + N:] == 7).all()
+    near = torch.empty(N, K + 16, dtype=torch.uint8, device="cuda")[:, :K].copy_(w.codes)   # weights' rows that begin anywhere
+    got = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    B.moe_linear8(a.codes, a.codes.stride(0), a.scales, a.scales.stride(0), near, K + 16, w.scales, apart, T, N, K, got, N,
+                  torch.cuda.current_stream())
+    assert torch.equal(got.view(torch.int16), view.view(torch.int16))
 
 
 @pytest.mark.parametrize("T,K", [(2, 528), (2, 4112), (14, 528), (40, 528), (200, 528), (700, 528), (6000, 528)])

@@ -134,13 +134,19 @@ def test_wrappers_refuse_what_is_on_no_gpu():
 
 
 def test_rows8_lays_out_what_lies_otherwise():
-    codes, scales = torch.arange(3 * 144).to(torch.uint8).view(3, 144), torch.arange(6, dtype=torch.uint8).view(3, 2)
+    def apart(n, K, step):   # codes whose rows begin at multiples of `step`, from 128 bytes on
+        base = torch.zeros(n * step + 256, dtype=torch.uint8)
+        return base[-base.data_ptr() % 128:].as_strided((n, K), (step, 1))
+
+    values = torch.arange(3 * 144).to(torch.uint8).view(3, 144)
+    scales = torch.arange(6, dtype=torch.uint8).view(3, 2)
+    codes = apart(3, 144, 256).copy_(values)
     c, s = L8.rows8(codes, scales)
     assert c.data_ptr() == codes.data_ptr() and s.stride() == (4, 1) and torch.equal(s, scales)
     assert L8.rows8(c, s)[1].data_ptr() == s.data_ptr()   # as it is
-    wide = torch.zeros(144, 3, dtype=torch.uint8).t().copy_(codes)
-    c, _ = L8.rows8(wide, scales)
-    assert c.is_contiguous() and torch.equal(c, codes)
-    shifted = torch.zeros(3 * 144 + 8, dtype=torch.uint8)[8:].view(3, 144).copy_(codes)
-    c, _ = L8.rows8(shifted, scales)
-    assert c.data_ptr() % 16 == 0 and torch.equal(c, codes)
+    wide = torch.zeros(144, 3, dtype=torch.uint8).t().copy_(values)
+    for other in (values, wide, apart(3, 144, 160).copy_(values)):   # rows 144 bytes, columns, 160 bytes apart
+        c, _ = L8.rows8(other, scales)
+        assert c.stride() == (256, 1) and c.data_ptr() != other.data_ptr() and torch.equal(c, values)
+    one = apart(1, 144, 16)   # a single row has no stride
+    assert L8.rows8(one, scales[:1])[0].data_ptr() == one.data_ptr()
