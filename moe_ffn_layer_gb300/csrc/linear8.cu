@@ -390,13 +390,15 @@ bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows) {
 }
 
 int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches) {
-  // Tiles of 64 tokens while an SM each is enough for them, then of 128, then the pairs' tiles.
-  const long long wide = (a.N + kWideM - 1) / kWideM;
+  // Tiles of 64 tokens while an SM each is enough for them, or, up to 24 blocks of K, half an SM (777 x 2500 x 2048
+  // 10.0 us, of 128 tokens 10.9; 256 x 6144 x 4096 15.9 and 15.1); then of 128, then the pairs' tiles (512 x 6144 x
+  // 4096 26.5, 27.8 and 17.7; 1024 x 4096 x 2048 18.9, 19.7 and 11.8; 512 x 4096 x 2048 9.7, 10.3 and 11.1).
+  const long long wide = (a.N + kWideM - 1) / kWideM, most = a.K <= 24 * kBlockK ? 2 * sms : sms;
   int rc;
   if (linear8_few_takes(a, sms)) rc = linear8_few_launch(a, stream);
   else if (a.T <= 16) rc = launch_narrow<16>(a, status, stream);
   else if (a.T <= 32) rc = launch_narrow<32>(a, status, stream);
-  else if (a.T <= 64 || wide * ((a.T + 63) / 64) <= sms) rc = launch_narrow<64>(a, status, stream);
+  else if (a.T <= 64 || wide * ((a.T + 63) / 64) <= most) rc = launch_narrow<64>(a, status, stream);
   else if (wide * ((a.T + 127) / 128) <= sms) rc = launch_narrow<128>(a, status, stream);
   else rc = linear8_wide_launch(a, status, sms, stream);
   if (rc == MOE_OK) ++*launches;

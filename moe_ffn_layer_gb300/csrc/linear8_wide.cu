@@ -31,11 +31,9 @@ struct Cfg {
   static constexpr uint32_t kSmem = kCtl + 512 + 1024;   // (1024: the ring's alignment)
   static constexpr uint32_t kSfBase = 2 * kBN;
   static constexpr uint32_t kSlotCols = kCopies * kSfCols;
-  static constexpr int kChunk = kAcc;   // blocks of K that an accumulator takes before the other's turn
   static_assert(kSfBase + kSlots * kSlotCols <= 512, "tensor memory");
   static_assert((2 * kStages + 2 * kSlots + 4 + 1) * 8 + 16 <= 512, "control region");
   static_assert(kStageBytes % 1024 == 0 && kBN % 32 == 0, "swizzled tiles, scale words by 32 rows");
-  static_assert(kStages >= 2 * kChunk, "a chunk is loaded while one is multiplied");
 };
 
 // A wait for a barrier that threads of the other CTA arrive on.
@@ -228,47 +226,41 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     uint32_t phase = 0, sf_phase = 0;
     bool ok = true;
     for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step, ++tile_no) {
-      for (int k0 = 0; k0 < blocks && ok; k0 += C::kChunk) {
+      for (int kb = 0; kb < blocks; ++kb) {
         const uint32_t sfa = tmem + C::kSfBase + slot * C::kSlotCols, sfb = sfa + kAcc * kSfCols;
-        const bool first = (k0 & 3) == 0;   // of the slot's blocks
-        if (first && !(ok = warp_wait_cluster(&sf_full[slot], sf_phase, abort_flag, status, wait_ns))) break;
-        const int in = min(C::kChunk, blocks - k0);
-        const bool last = k0 + in == blocks;
+        const bool last = kb == blocks - 1, slot_done = (kb & 3) == 3 || last;
+        if ((kb & 3) == 0 && !(ok = warp_wait_cluster(&sf_full[slot], sf_phase, abort_flag, status, wait_ns))) break;
+        if (!(ok = warp_wait(&full[stage], phase, abort_flag, status, wait_ns))) break;
+        const uint32_t sf_at = smem_u32(smem + C::kSf + slot * C::kSlotBytes), at = smem_u32(smem + stage * C::kStageBytes);
+        const uint64_t da = smem_desc_k128(at), db = smem_desc_k128(at + kAcc * C::kABytes);
+        const uint32_t idesc = idesc_mx8(kRows, kBN) | mx8_byte(kb & 3);
 #pragma unroll
         for (int h = 0; h < kAcc; ++h) {
           // the accumulator: given back by the epilogue before a tile's first block
           const int acc = kAcc == 1 ? tile_no & 1 : h;
           const uint32_t uses = kAcc == 1 ? tile_no >> 1 : tile_no;
-          if (k0 == 0 && !(ok = warp_wait_cluster(&acc_empty[acc], (uses & 1) ^ 1u, abort_flag, status, wait_ns))) break;
-          for (int i = 0; i < in; ++i) {
-            const bool wraps = stage + i >= C::kStages;
-            const int st = wraps ? stage + i - C::kStages : stage + i;
-            if (h == 0 && !(ok = warp_wait(&full[st], wraps ? phase ^ 1u : phase, abort_flag, status, wait_ns))) break;
-            tc_fence_after();
-            const uint32_t sf_at = smem_u32(smem + C::kSf + slot * C::kSlotBytes), at = smem_u32(smem + st * C::kStageBytes);
-            const uint64_t da = smem_desc_k128(at + h * C::kABytes), db = smem_desc_k128(at + kAcc * C::kABytes);
-            const uint32_t idesc = idesc_mx8(kRows, kBN) | mx8_byte((k0 + i) & 3);
-            if (one) {
-              if (h == 0 && first && i == 0) {
+          if (kb == 0 && !(ok = warp_wait_cluster(&acc_empty[acc], (uses & 1) ^ 1u, abort_flag, status, wait_ns))) break;
+          tc_fence_after();
+          if (one) {
+            if (h == 0 && (kb & 3) == 0) {
 #pragma unroll
-                for (int c = 0; c < C::kCopies; ++c) scales_to_tmem<2>(sfa + c * kSfCols, sf_at + c * kSfBytes);
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
-                umma_mx8<2>(tmem + acc * kBN, da + 2 * k, db + 2 * k, idesc, sfa + h * kSfCols, sfb, k0 + i > 0 || k > 0);
-              if (h == kAcc - 1) commit_pair(&empty[st]);
+              for (int c = 0; c < C::kCopies; ++c) scales_to_tmem<2>(sfa + c * kSfCols, sf_at + c * kSfBytes);
             }
-            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)   // 32 values of K: 32 bytes, 2 in the descriptor's units
+              umma_mx8<2>(tmem + acc * kBN, da + h * (C::kABytes >> 4) + 2 * k, db + 2 * k, idesc, sfa + h * kSfCols, sfb, kb > 0 || k > 0);
+            if (last) commit_pair(&acc_full[acc]);
           }
-          if (!ok) break;
-          if (one && last) commit_pair(&acc_full[acc]);
+          __syncwarp();
         }
         if (!ok) break;
-        const bool slot_done = ((k0 + in) & 3) == 0 || last;
-        if (one && slot_done) commit_pair(&sf_empty[slot]);
+        if (one) {
+          commit_pair(&empty[stage]);
+          if (slot_done) commit_pair(&sf_empty[slot]);
+        }
         __syncwarp();
-        if ((stage += in) >= C::kStages) {
-          stage -= C::kStages;
+        if (++stage == C::kStages) {
+          stage = 0;
           phase ^= 1u;
         }
         if (slot_done && ++slot == C::kSlots) {
