@@ -59,12 +59,12 @@ def _empty8(rows, K, high, device):
     # lines (8192 x 4096 x 2000 50 us, with rows of 2000 bytes 68), rows of scales a multiple of 4, which it reads at once.
     blocks = -(-K // 128)
     of, apart = (-(-rows // high), blocks), -(-blocks // 4) * 4
-    # room for whole rows, the last one's too
-    scales = (torch.empty(of, dtype=_U8, device=device) if apart == blocks else
-              torch.empty((of[0], apart), dtype=_U8, device=device).as_strided(of, (apart, 1)))
-    codes = (torch.empty((rows, K), dtype=_U8, device=device) if K % 128 == 0 else
-             torch.empty((rows, 128 * blocks), dtype=_U8, device=device).as_strided((rows, K), (128 * blocks, 1)))
-    return codes, scales
+    if K % 128 == 0 and apart == blocks:
+        return torch.empty((rows, K), dtype=_U8, device=device), torch.empty(of, dtype=_U8, device=device)
+    # (one allocation for both, each with room for whole rows, the last one's too)
+    codes = rows * blocks * 128
+    both = torch.empty(codes + of[0] * apart, dtype=_U8, device=device)
+    return both.as_strided((rows, K), (128 * blocks, 1)), both.as_strided(of, (apart, 1), codes)
 
 
 def rows8(codes: torch.Tensor, scales: torch.Tensor) -> Block8:
