@@ -7,6 +7,15 @@
 // K is cut between the CTAs of a cluster, enough of them to draw the weights'
 // stream over every SM; each then sums its share of the tokens' partial sums, which
 // the others copy into its shared memory, in the order of the ranks.
+//
+// Bound: of 17 to 64 rows the latency of one pass (launch, a round trip to memory, the
+// exchange between CTAs: 4.5 us before any streaming) and then the weights' stream
+// (64 x 6144 x 4096 in 9.9 us, 2.6 TB/s); of more rows the operands' way from L2 and
+// the MMAs, which take 122 clocks each however narrow (777 x 2500 x 2000 in 10.9 us).
+// What it took: copies started before the tensor memory is allocated and the next
+// launch set up meanwhile (1 x 4096 x 2048, which was computed here then, 6.7 -> 5.4 us); bulk
+// copies between the CTAs instead of single stores (64 x 6144 x 4096 12.2 -> 10.8);
+// MMAs issued by a whole warp that spins on its barriers (10.7 -> 9.9).
 #include <mutex>
 
 #include "linear8.cuh"
@@ -19,7 +28,8 @@ constexpr int kWideM = 128;   // weight rows of a tile
 
 template <int kNT>
 struct Cfg {
-  static constexpr int kChains = kNT <= 32 ? 4 : 2;   // accumulators that the MMAs of a block take in turn
+  // accumulators that the MMAs of a block take in turn (16 x 512 x 8192 6.2 us, one 6.5; 64 x 6144 x 4096 10.0 and 9.9)
+  static constexpr int kChains = kNT <= 32 ? 4 : 1;
   // stages of the ring: so many that one CTA fills an SM, or two do
   static constexpr int kDeep = kNT == 16 ? 9 : kNT == 32 ? 8 : kNT == 64 ? 6 : 4;
   static constexpr int kShallow = kNT == 16 ? 5 : kNT == 32 ? 4 : kNT == 64 ? 3 : 4;

@@ -1,9 +1,21 @@
 // Product of two 8-bit matrices with block scales, many rows of A: tiles of 256
 // tokens x kBN weight rows, computed by pairs of CTAs (two-CTA MMAs, M = 256).
 //
-// Each CTA of a pair stages its 128 tokens and half of the tile's weight rows, and
-// holds its tokens' sums in tensor memory; the first one's MMA thread issues for
-// both.  So a CTA reads (128 + kBN / 2) rows a block of K for a 128 x kBN tile.
+// Each CTA of a pair stages its tokens and half of the tile's weight rows, and holds
+// its tokens' sums in tensor memory; the first one's MMA warp issues for both.  Tensor
+// memory holds two accumulators of 256 x 224 and the scales beside them (two of 256
+// columns would leave the scales no room).
+//
+// Bound: 16384 x 8192 x 4096 in 317 us, 3.46 PFLOP/s, at 2070 MHz: copies and MMAs
+// beside each other, which meet in shared memory (the copies without MMAs take 237 us of
+// it, the MMAs without copies 264), and then the power cap: run back to back the
+// clock settles at 1.45 GHz and a call at 368 us.  A tile has 512 tokens where that
+// many fill the pairs, since it then moves (512 + 224) rows a block of K instead of
+// 2 (256 + 224) for the same products.
+// What it took (16384 x 8192 x 4096): pairs instead of single CTAs 997 -> 408 us; the
+// MMA warp run whole, descriptors in uniform registers -> 356; two accumulators of a
+// 512-token tile -> 327; copies issued by a whole warp, the accumulators in turn
+// block by block instead of by twos -> 317.
 #include <mutex>
 
 #include "linear8.cuh"
