@@ -144,11 +144,10 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
     if weight is not None and (weight.dtype is not _BF16 or weight.shape != shape[1:] or weight.get_device() != dev or
                                not weight.is_contiguous()):
         raise ValueError(f"weight: want contiguous {_BF16} ({H},) on {x.device}, got {weight.dtype} {tuple(weight.shape)} on {weight.device}")
+    if outputs not in ("codes", "y", "both"):
+        raise ValueError(f"outputs: want 'codes', 'y' or 'both', got {outputs!r}")
     want = (shape, dev, outputs, r is None)
     if into is None:
-        if outputs not in ("codes", "y", "both"):
-            raise ValueError(f"outputs: want 'codes', 'y' or 'both', got {outputs!r}")
-
         def make():
             row = lambda: torch.empty(shape, dtype=_BF16, device=x.device)  # noqa: E731
             q = _empty8(T, H, 1, x.device) if outputs != "y" else (None, None)
