@@ -212,19 +212,24 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
   float* own = reinterpret_cast<float*>(smem);   // [token][128], where the ring was
   if (ok) {
     const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    // 64 registers at once: 16 columns of four accumulators, 64 of one
+    constexpr int kStep = C::kChains == 4 ? 16 : 64;
 #pragma unroll
-    for (int c = 0; c < kNT; c += 16) {
+    for (int c = 0; c < kNT; c += kStep) {
       if (c >= tokens) break;
-      uint32_t r[C::kChains][16];
+      uint32_t r[4][16];
 #pragma unroll
-      for (int i = 0; i < C::kChains; ++i) tmem_ld_16cols(at + i * kNT + c, r[i]);
+      for (int i = 0; i < 4; ++i) tmem_ld_16cols(at + (C::kChains == 4 ? i * kNT + c : c + 16 * i), r[i]);
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        float v = __uint_as_float(r[0][j]);
+        const float v[4] = {__uint_as_float(r[0][j]), __uint_as_float(r[1][j]), __uint_as_float(r[2][j]), __uint_as_float(r[3][j])};
+        if (C::kChains == 4) {
+          own[(c + j) * kWideM + threadIdx.x] = v[0] + v[1] + v[2] + v[3];
+        } else {
 #pragma unroll
-        for (int i = 1; i < C::kChains; ++i) v += __uint_as_float(r[i][j]);
-        own[(c + j) * kWideM + threadIdx.x] = v;
+          for (int i = 0; i < 4; ++i) own[(c + 16 * i + j) * kWideM + threadIdx.x] = v[i];
+        }
       }
     }
   }

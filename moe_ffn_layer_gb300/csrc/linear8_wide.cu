@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  cluster_arrive();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
