@@ -410,7 +410,7 @@ int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, 
   // 4096 26.5, 27.8 and 17.7; 1024 x 4096 x 2048 18.9, 19.7 and 11.8; 512 x 4096 x 2048 9.7, 10.3 and 11.1).
   const long long wide = (a.N + kWideM - 1) / kWideM, most = a.K <= 24 * kBlockK ? 2 * sms : sms;
   int rc;
-  if (linear8_few_takes(a, sms)) rc = linear8_few_launch(a, stream);
+  if (linear8_few_takes(a, sms)) rc = linear8_few_launch(a, sms, stream);
   else if (a.T <= 16) rc = launch_narrow<16>(a, status, stream);
   else if (a.T <= 32) rc = launch_narrow<32>(a, status, stream);
   else if (a.T <= 64 || wide * ((a.T + 63) / 64) <= most) rc = launch_narrow<64>(a, status, stream);

@@ -117,9 +117,9 @@ bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
 // The output in boxes of 32 columns x box_rows (64-byte swizzle); what lies outside is not written.
 bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows);
 
-// Up to 8 rows, of the sizes that it takes: a stream of the weights.
+// Up to 16 rows, of the sizes that it takes: a stream of the weights.
 bool linear8_few_takes(const Linear8& a, int sms);
-int linear8_few_launch(const Linear8& a, cudaStream_t stream);
+int linear8_few_launch(const Linear8& a, int sms, cudaStream_t stream);
 // Many rows: tiles of 256 tokens by pairs of CTAs.
 int linear8_wide_launch(const Linear8& a, int* status, int sms, cudaStream_t stream);
 

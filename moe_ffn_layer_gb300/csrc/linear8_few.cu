@@ -1,4 +1,4 @@
-// Product of two 8-bit matrices with block scales for up to 8 rows of A: a stream of
+// Product of two 8-bit matrices with block scales for up to 16 rows of A: a stream of
 // the weights through registers.
 //
 // A CTA has 16 weight rows, its eight warps an eighth of K each, and adds their sums
@@ -133,17 +133,22 @@ __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 3 : 2) linear8_few_ker
 
 }  // namespace
 
-// Where it is the faster one (the tensor-memory kernel's time in parentheses): 1 x 2048 x 2048 2.5 (4.7) us,
-// 1 x 4096 x 2048 3.4 (5.5), 8 x 6144 x 4096 7.3 (8.9); not where a warp has more than four blocks of K one after
-// the other (1 x 8192 x 8192 20.7 (15.0)) or the CTAs do not fit at once (1 x 16384 x 4096 16.9 (14.0)).
+// Where it is the faster one (the tensor-memory kernel's time in parentheses).  Up to 8 rows while the CTAs fit at once,
+// three an SM, and a warp has four blocks of K at most: 1 x 2048 x 2048 2.4 (4.1) us, 1 x 4096 x 2048 3.2 (4.9),
+// 8 x 7296 x 4096 7.1 (8.2), but 1 x 8192 x 8192 20.7 (14.7) and 1 x 16384 x 4096 16.9 (14.0).  Up to 16 rows with two an SM
+// and two blocks: 16 x 4096 x 2048 3.9 (5.0), but 16 x 7296 x 2048 6.4 (6.1) and 16 x 4096 x 4096 7.6 (6.4).
 bool linear8_few_takes(const Linear8& a, int sms) {
-  return a.T <= 16 && a.K <= 4 * kWarps * kBlockK && (a.N + kRows - 1) / kRows <= 3 * sms;
+  const int ctas = (a.N + kRows - 1) / kRows;
+  return a.T <= 8 ? a.K <= 4 * kWarps * kBlockK && ctas <= 3 * sms : a.T <= 16 && a.K <= 2 * kWarps * kBlockK && ctas <= 2 * sms;
 }
 
-int linear8_few_launch(const Linear8& a, cudaStream_t stream) {
-  const bool once = a.K <= 2 * kWarps * kBlockK;
-  auto kernel = a.T <= 8 ? (once ? linear8_few_kernel<2, 1> : linear8_few_kernel<1, 1>) : (once ? linear8_few_kernel<2, 2> : linear8_few_kernel<1, 2>);
-  return launch_chained(kernel, dim3((a.N + kRows - 1) / kRows), dim3(kThreads), 0, stream, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+int linear8_few_launch(const Linear8& a, int sms, cudaStream_t stream) {
+  const int ctas = (a.N + kRows - 1) / kRows;
+  // two blocks at once where a warp has two and two CTAs fit (1 x 2048 x 2048 2.4 us, one at a time 3.0; 1 x 7296 x
+  // 2048 5.1 and 4.3, 1 x 7296 x 1024 4.0 and 3.1)
+  const bool two = a.K > kWarps * kBlockK && a.K <= 2 * kWarps * kBlockK && ctas <= 2 * sms;
+  auto kernel = a.T > 8 ? linear8_few_kernel<2, 2> : two ? linear8_few_kernel<2, 1> : linear8_few_kernel<1, 1>;
+  return launch_chained(kernel, dim3(ctas), dim3(kThreads), 0, stream, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe
