@@ -385,12 +385,11 @@ MOE_API int moe_kv_evict(const moe_kv_dims* d, const moe_kv_pool* src, const moe
  * over the block's finite values, 2^-126 at least, and code = e4m3(x / scale),
  * to nearest even (one rounding of the fp32 value); an infinity or a NaN
  * becomes the NaN code 0x7f.
- * Supported: K % 16 == 0; codes 16-byte aligned, ld % 16 == 0; scales 4-byte
- * aligned, lds % 4 == 0 (bytes of a row beyond ceil(K / 128) may be read, never
- * used or written: a last row of scales has room up to a multiple of 4).  bf16
+ * Supported: K % 16 == 0; codes 16-byte aligned, ld % 16 == 0; any lds.  bf16
  * rows are 16-byte aligned, strides multiples of 8.  The stride of a matrix of
  * one row is not looked at.  The product reads codes fastest where their rows
- * begin at multiples of 128 bytes. */
+ * begin at multiples of 128 bytes; it reads scales by aligned words of 4 bytes,
+ * each with a byte of the matrix in it, and uses no other byte of them. */
 
 /* RMS norm of rows, with the residual's addition:
  *   h[t] = bf16(x[t] + residual[t])  (residual NULL: h = x, and no h is stored)

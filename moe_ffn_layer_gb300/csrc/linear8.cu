@@ -89,9 +89,14 @@ __global__ void __launch_bounds__(kThreads) linear8_narrow_kernel(const __grid_c
   // a group's scale words: the tokens', and the tile's weight rows', which share one
   uint4 sf_a;
   uint32_t sf_w;
+  const bool words_a = scales_are_words(a.a_scales, a.las, a.T), words_w = scales_are_words(a.w_scales, a.lws, (a.N + 127) >> 7);
   auto scales = [&](int g) {
-    sf_a = scale_words(a.a_scales, a.las, t0, a.T, g);
-    sf_w = *reinterpret_cast<const uint32_t*>(a.w_scales + static_cast<long long>(n0 >> 7) * a.lws + 4 * g);
+    sf_a = scale_words_of_rows(a.a_scales, a.las, t0, a.T, g, blocks, words_a);
+    const uint8_t* row[1] = {a.w_scales + static_cast<long long>(n0 >> 7) * a.lws};
+    const bool in[1] = {true};
+    uint32_t w[1];
+    scale_words(w, row, in, g, blocks, words_w);
+    sf_w = w[0];
   };
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&mw);

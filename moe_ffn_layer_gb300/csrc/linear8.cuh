@@ -99,14 +99,47 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
-// Scale words of rows row0 + lane + 32 c (c < 4) for the blocks 4 g .. 4 g + 3;
-// rows from `rows` on have 1.0 (their codes read as 0).
-__device__ __forceinline__ uint4 scale_words(const uint8_t* scales, long long lds, int row0, int rows, int g) {
-  uint32_t w[4];
-  const int r = row0 + static_cast<int>(threadIdx.x & 31);
+// The scales of the blocks 4 g .. 4 g + 3 of kRows rows as words, from the aligned words that hold them: one each
+// where rows of scales are words, else two, of which a byte at least is of the row (what lies beside it, beyond the last
+// block too, is not used).  All loads are issued together, for the scales' warp has as long as the MMAs of four blocks:
+// 8192 x 4096 x 2176 takes 53 us (17 scales a row; 47.7 us with 16, which are words), and 76 us where each row's
+// second load waits for its first.
+template <int kRows>
+__device__ __forceinline__ void scale_words(uint32_t (&w)[kRows], const uint8_t* const (&row)[kRows], const bool (&in)[kRows], int g,
+                                            int blocks, bool words) {
+  if (words) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    w[c] = r + 32 * c < rows ? *reinterpret_cast<const uint32_t*>(scales + (r + 32 * c) * lds + 4 * g) : 0x7F7F7F7Fu;
+    for (int c = 0; c < kRows; ++c) w[c] = in[c] ? reinterpret_cast<const uint32_t*>(row[c])[g] : 0x7F7F7F7Fu;   // (1.0)
+  } else {
+    uint32_t lo[kRows], hi[kRows];
+#pragma unroll
+    for (int c = 0; c < kRows; ++c) {
+      const uint8_t* p = row[c] + 4 * g;
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(p - off);
+      lo[c] = in[c] ? at[0] : 0u;
+      hi[c] = in[c] ? at[off && 4 * g + 4 - off < blocks ? 1 : 0] : 0u;
+    }
+#pragma unroll
+    for (int c = 0; c < kRows; ++c)
+      w[c] = in[c] ? __funnelshift_r(lo[c], hi[c], 8 * static_cast<int>(reinterpret_cast<uintptr_t>(row[c] + 4 * g) & 3)) : 0x7F7F7F7Fu;
+  }
+}
+__device__ __forceinline__ bool scales_are_words(const uint8_t* scales, long long lds, int rows) {
+  return (reinterpret_cast<uintptr_t>(scales) & 3) == 0 && (rows == 1 || (lds & 3) == 0);
+}
+// Those of rows row0 + lane + 32 c (c < 4) of `rows` (rows beyond have 1.0: their codes read as 0).
+__device__ __forceinline__ uint4 scale_words_of_rows(const uint8_t* scales, long long lds, int row0, int rows, int g, int blocks, bool words) {
+  const int r = row0 + static_cast<int>(threadIdx.x & 31);
+  const uint8_t* row[4];
+  bool in[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    row[c] = scales + (r + 32 * c) * lds;
+    in[c] = r + 32 * c < rows;
+  }
+  uint32_t w[4];
+  scale_words(w, row, in, g, blocks, words);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -19,7 +19,7 @@ int check_rows(const void* p, int64_t stride, int rows, int K) {
 int check_block8(const void* codes, int64_t ld, const void* scales, int64_t lds, int rows, int high, int K) {
   const bool one = rows == 1, one_s = rows <= high;
   if (!codes || !scales || (!one && ld < K) || (!one_s && lds < (static_cast<int64_t>(K) + 127) / 128)) return MOE_ERR_INVALID;
-  return aligned(codes, 16) && (one || ld % 16 == 0) && aligned(scales, 4) && (one_s || lds % 4 == 0) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  return aligned(codes, 16) && (one || ld % 16 == 0) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 int check_sizes(int64_t rows, int K) {

@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     uint32_t phase = 0;
     const int groups = (blocks + 3) >> 2;
     bool ok = true;
+    const bool words_a = scales_are_words(a.a_scales, a.las, a.T), words_w = scales_are_words(a.w_scales, a.lws, (a.N + 127) >> 7);
     chain_wait();
     for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step) {
       int m, n;
@@ -295,17 +296,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       for (int g = 0; g < groups; ++g) {
         uint4 w[C::kCopies];
 #pragma unroll
-        for (int h = 0; h < kAcc; ++h) w[h] = scale_words(a.a_scales, a.las, m * C::kM + h * kRows + rank * (kRows / 2), a.T, g);
+        for (int h = 0; h < kAcc; ++h)
+          w[h] = scale_words_of_rows(a.a_scales, a.las, m * C::kM + h * kRows + rank * (kRows / 2), a.T, g, blocks, words_a);
+        // one scale for 128 weight rows: the same for 32 rows of a tile
+        constexpr int kParts = 4 * (C::kCopies - kAcc);
+        const uint8_t* row[kParts];
+        bool in[kParts];
+        uint32_t v[kParts];
 #pragma unroll
-        for (int i = 0; i < C::kCopies - kAcc; ++i) {
-          uint32_t v[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {   // one scale for 128 weight rows: the same for 32 rows of a tile
-            const int of = 128 * i + 32 * c, row = n * kBN + of;
-            v[c] = of < kBN && row < a.N ? *reinterpret_cast<const uint32_t*>(a.w_scales + (row >> 7) * a.lws + 4 * g) : 0x7F7F7F7Fu;
-          }
-          w[kAcc + i] = make_uint4(v[0], v[1], v[2], v[3]);
+        for (int c = 0; c < kParts; ++c) {
+          row[c] = a.w_scales + ((n * kBN + 32 * c) >> 7) * a.lws;
+          in[c] = 32 * c < kBN && n * kBN + 32 * c < a.N;
         }
+        scale_words(v, row, in, g, blocks, words_w);
+#pragma unroll
+        for (int i = 0; i < C::kCopies - kAcc; ++i) w[kAcc + i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sf_empty[slot], phase ^ 1u, abort_flag, status, wait_ns)))) break;
         const uint32_t at = smem_u32(smem + C::kSf + slot * C::kSlotBytes) + lane * 16;
 #pragma unroll

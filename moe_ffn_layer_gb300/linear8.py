@@ -56,27 +56,22 @@ _BF16, _U8 = torch.bfloat16, torch.uint8
 
 def _empty8(rows, K, high, device):
     # Rows of codes lie a multiple of 128 bytes apart, so that the product's copies of 128 bytes a row read whole
-    # lines (8192 x 4096 x 2000 50 us, with rows of 2000 bytes 68), rows of scales a multiple of 4, which it reads at once.
+    # lines (8192 x 4096 x 2000 50 us, with rows of 2000 bytes 68).
     blocks = -(-K // 128)
-    of, apart = (-(-rows // high), blocks), -(-blocks // 4) * 4
-    if K % 128 == 0 and apart == blocks:
-        return torch.empty((rows, K), dtype=_U8, device=device), torch.empty(of, dtype=_U8, device=device)
-    # (one allocation for both, each with room for whole rows, the last one's too)
-    codes = rows * blocks * 128
-    both = torch.empty(codes + of[0] * apart, dtype=_U8, device=device)
-    return both.as_strided((rows, K), (128 * blocks, 1)), both.as_strided(of, (apart, 1), codes)
+    codes = (torch.empty((rows, K), dtype=_U8, device=device) if K % 128 == 0 else
+             torch.empty_strided((rows, K), (128 * blocks, 1), dtype=_U8, device=device))
+    return codes, torch.empty((-(-rows // high), blocks), dtype=_U8, device=device)
 
 
 def rows8(codes: torch.Tensor, scales: torch.Tensor) -> Block8:
     """Codes and scales from elsewhere (uint8 [R, K]; uint8 [.., ceil(K / 128)]),
     each copied where its rows do not lie as the results here do: codes a multiple
-    of 128 bytes apart (of 16 is enough for the calls), scales of 4."""
-    (R, K), S = codes.shape, scales.shape[0]
+    of 128 bytes apart (of 16 is enough for the calls), scales contiguous in a row."""
+    R, K = codes.shape
     if (codes.stride(1) != 1 and K > 1) or (codes.stride(0) % 128 and R > 1) or codes.data_ptr() % 128:
         codes = torch.empty(R, -(-K // 128) * 128, dtype=codes.dtype, device=codes.device)[:, :K].copy_(codes)
-    if (scales.stride(1) != 1 and scales.shape[1] > 1) or (scales.stride(0) % 4 and S > 1) or scales.data_ptr() % 4:
-        padded = torch.empty(S, -(-scales.shape[1] // 4) * 4, dtype=scales.dtype, device=scales.device)
-        scales = padded[:, :scales.shape[1]].copy_(scales)
+    if scales.stride(1) != 1 and scales.shape[1] > 1:
+        scales = scales.contiguous()
     return Block8(codes, scales)
 
 

@@ -250,18 +250,20 @@ def test_linear_exact(T, N, K):
     assert torch.equal(out.cpu().view(torch.int16), torch.from_numpy(ref).float().bfloat16().view(torch.int16))
 
 
-@pytest.mark.parametrize("T,N,K", [(3, 200, 272), (2, 200, 4112), (20, 200, 272), (70, 136, 400), (600, 300, 272), (1100, 4300, 272)])
-def test_linear_strides_and_rows_behind(T, N, K):
+@pytest.mark.parametrize("T,N,K,pad_s", [(3, 200, 272, 2), (2, 200, 4112, 3), (20, 200, 272, 5), (20, 200, 512, 8), (70, 136, 400, 2),
+                                         (70, 136, 512, 3), (600, 300, 272, 4), (1100, 4300, 272, 1), (1100, 4300, 512, 2),
+                                         (1100, 4300, 1024, 8)])
+def test_linear_strides_and_rows_behind(T, N, K, pad_s):
     """Operands and outputs that lie in larger tensors; what is beyond them stays as it was."""
     big = torch.randint(0, 120, (T + 3, K + 48), dtype=torch.uint8, device="cuda")
     nb = -(-K // 128)
-    apart = -(-nb // 4) * 4 + 4
-    bs = torch.randint(120, 130, (T + 3, apart + 4), dtype=torch.uint8, device="cuda")
-    bs[:, :4] = bs[:, 4 + nb:] = 255   # NaN beside what is used
+    apart, at_s = nb + pad_s, pad_s // 2
+    bs = torch.randint(120, 130, (T + 3, apart), dtype=torch.uint8, device="cuda")
+    bs[:, :at_s] = bs[:, at_s + nb:] = 255   # NaN beside what is used
     wide = torch.randint(0, 120, (N, -(-K // 128) * 128 + 128), dtype=torch.uint8, device="cuda")
     ws = torch.randint(120, 130, (-(-N // 128), apart), dtype=torch.uint8, device="cuda")
     ws[:, nb:] = 255
-    a, w = L8.Block8(big[:T, 16:16 + K], bs[:T, 4:4 + nb]), L8.Block8(wide[:, :K], ws[:, :nb])
+    a, w = L8.Block8(big[:T, 16:16 + K], bs[:T, at_s:at_s + nb]), L8.Block8(wide[:, :K], ws[:, :nb])
     lin = L8.Linear8(*w)
     assert lin.codes.data_ptr() == wide.data_ptr()   # not copied
     for pad, at in ((8, 0), (7, 0), (8, 1), (0, 0)):   # 16-byte rows, odd rows, an odd start, its own rows

@@ -94,8 +94,6 @@ LINEAR = dict(a=P, lda=256, a_scales=P, las=4, w=P, ldw=256, w_scales=P, lws=4, 
     ("moe_rms_norm8", NORM, dict(y=P, y_stride=257), UNSUPPORTED),
     ("moe_rms_norm8", NORM, dict(codes=P + 8), UNSUPPORTED),
     ("moe_rms_norm8", NORM, dict(ld=264), UNSUPPORTED),
-    ("moe_rms_norm8", NORM, dict(lds=6), UNSUPPORTED),
-    ("moe_rms_norm8", NORM, dict(scales=P + 2), UNSUPPORTED),
     ("moe_quantize8", ROWS, dict(K=40, x_stride=256), UNSUPPORTED),
     ("moe_quantize8", ROWS, dict(x=P + 4), UNSUPPORTED),
     ("moe_quantize8", ROWS, dict(T=2 ** 31 - 1), UNSUPPORTED),         # more blocks than are counted
@@ -104,8 +102,6 @@ LINEAR = dict(a=P, lda=256, a_scales=P, las=4, w=P, ldw=256, w_scales=P, lws=4, 
     ("moe_linear8", LINEAR, dict(K=136), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(a=P + 8), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(ldw=264), UNSUPPORTED),
-    ("moe_linear8", LINEAR, dict(las=5), UNSUPPORTED),
-    ("moe_linear8", LINEAR, dict(w_scales=P + 1), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(out=P + 1), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(T=2 ** 31 - 1), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(N=2 ** 31 - 1, out_stride=2 ** 31), UNSUPPORTED),
@@ -142,8 +138,9 @@ def test_rows8_lays_out_what_lies_otherwise():
     scales = torch.arange(6, dtype=torch.uint8).view(3, 2)
     codes = apart(3, 144, 256).copy_(values)
     c, s = L8.rows8(codes, scales)
-    assert c.data_ptr() == codes.data_ptr() and s.stride() == (4, 1) and torch.equal(s, scales)
-    assert L8.rows8(c, s)[1].data_ptr() == s.data_ptr()   # as it is
+    assert c.data_ptr() == codes.data_ptr() and s.data_ptr() == scales.data_ptr()   # as they are
+    s = L8.rows8(codes, torch.zeros(2, 3, dtype=torch.uint8).t().copy_(scales))[1]
+    assert s.is_contiguous() and torch.equal(s, scales)
     wide = torch.zeros(144, 3, dtype=torch.uint8).t().copy_(values)
     for other in (values, wide, apart(3, 144, 160).copy_(values)):   # rows 144 bytes, columns, 160 bytes apart
         c, _ = L8.rows8(other, scales)
