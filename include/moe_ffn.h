@@ -401,7 +401,8 @@ MOE_API int moe_kv_evict(const moe_kv_dims* d, const moe_kv_pool* src, const moe
  *  y       bf16(y), or NULL;  codes, scales: y in 8 bits, or both NULL; one of
  *          the two forms at least
  * A row that holds a NaN gives NaN; one whose sum of squares passes the fp32
- * range gives zeros, and NaN where it holds an infinity.  Supported: H <= 65536. */
+ * range gives zeros, and NaN where it holds an infinity; with eps == 0, squares
+ * under the fp32 range are lost (a row of zeros gives NaN).  Supported: H <= 65536. */
 MOE_API int moe_rms_norm8(const void* x, int64_t x_stride, const void* residual, int64_t r_stride, const void* weight,
                           float eps, int T, int H, void* h, int64_t h_stride, void* y, int64_t y_stride, void* codes,
                           int64_t ld, void* scales, int64_t lds, cudaStream_t stream);

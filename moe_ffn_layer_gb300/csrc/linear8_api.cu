@@ -24,7 +24,7 @@ int check_block8(const void* codes, int64_t ld, const void* scales, int64_t lds,
 
 int check_sizes(int64_t rows, int K) {
   if (rows < 0 || K <= 0) return MOE_ERR_INVALID;
-  return K % 16 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return K % 16 || K > INT_MAX - 1024 ? MOE_ERR_UNSUPPORTED : MOE_OK;   // (K is counted in blocks of 128)
 }
 
 }  // namespace
@@ -91,8 +91,8 @@ int moe_linear8(const void* a, int64_t lda, const void* a_scales, int64_t las, c
   if (!out || (T > 1 && out_stride < N)) return MOE_ERR_INVALID;
   if ((rc = check_block8(a, lda, a_scales, las, T, 1, K)) || (rc = check_block8(w, ldw, w_scales, lws, N, 128, K))) return rc;
   if (!aligned(out, 2)) return MOE_ERR_UNSUPPORTED;
-  // (tiles end past T and N, and still fit an int; K is counted in blocks of 128)
-  if (T > INT_MAX - 1024 || N > INT_MAX - 1024 || K > INT_MAX - 1024) return MOE_ERR_UNSUPPORTED;
+  // (tiles end past T and N, and still fit an int)
+  if (T > INT_MAX - 1024 || N > INT_MAX - 1024) return MOE_ERR_UNSUPPORTED;
   if (!moe::device_local(a) || !moe::device_local(w) || !moe::device_local(out)) return MOE_ERR_UNSUPPORTED;
   int* status = nullptr;
   int sms = 0, n = 0;

@@ -24,7 +24,8 @@ from .kv_cache import _call, _current, _device
 
 # The calls are a few microseconds of kernels at decode sizes, and the host has to
 # keep ahead of them: the checks are a few comparisons a tensor, and results that
-# a call made itself are known by what they were made for when they come back as `into`.
+# a call made itself are known by what they were made for when they come back as `into`
+# (copies, and what is loaded from a file, are checked again: `__reduce__`).
 
 
 class _Block8(NamedTuple):
@@ -34,8 +35,11 @@ class _Block8(NamedTuple):
 
 class Block8(_Block8):
     """A matrix in 8 bits: codes, scales."""
-    _for = None     # what they were made for
-    _args = ()      # and where they lie
+    _for = None         # what they were made for
+    _strides = (0, 0)
+
+    def __reduce__(self):
+        return type(self), tuple(self)
 
 
 class _Norm8(NamedTuple):
@@ -48,10 +52,13 @@ class _Norm8(NamedTuple):
 class Norm8(_Norm8):
     """What ``rms_norm8`` gives: codes, scales, h, y; None for what was not asked for."""
     _for = None
-    _args = ()
+    _strides = (0, 0, 0, 0)
+
+    def __reduce__(self):
+        return type(self), tuple(self)
 
 
-_BF16, _U8 = torch.bfloat16, torch.uint8
+_BF16, _U8, _INT_MAX = torch.bfloat16, torch.uint8, 2 ** 31 - 1
 
 
 def _empty8(rows, K, high, device):
@@ -87,10 +94,12 @@ def _want_rows(name, t, dtype, dev, shape):
 
 
 def _want_input(name, x):
-    """Raises ValueError unless x is a bf16 matrix with contiguous rows on a CUDA device."""
+    """Raises ValueError unless x is a bf16 matrix with contiguous rows on a CUDA device, of sizes that the C calls take."""
     if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or (x.stride(1) != 1 and x.shape[1] > 1):
         raise ValueError(f"{name}: want 2-d {_BF16} with contiguous rows on a CUDA device, got {x.dim()}-d {x.dtype} of "
                          f"strides {tuple(x.stride())} on {x.device}")
+    if x.shape[0] > _INT_MAX or x.shape[1] > _INT_MAX:
+        raise ValueError(f"{name}: want sizes of 31 bits, got {tuple(x.shape)}")
 
 
 def _made(stream, device, make):
@@ -101,19 +110,17 @@ def _made(stream, device, make):
         return make()
 
 
-def _norm_into(into, want, x):
-    """Checks results that are to be written, and finds where they lie."""
+def _norm_into(into, want):
+    """Checks results that are to be written, and gives their rows' strides."""
     shape, dev, outputs, plain = want
     codes, scales, h, y = into
     if (codes is None) != (outputs == "y") or (y is None) != (outputs == "codes") or (h is None) != plain:
         raise ValueError(f"into: not the results of a call with outputs={outputs!r} and {'no' if plain else 'a'} residual")
-    args = [None, 0, None, 0, None, 0, None, 0]
-    for name, t, dtype, at, of in (("h", h, _BF16, 0, shape), ("y", y, _BF16, 2, shape), ("codes", codes, _U8, 4, shape),
-                                   ("scales", scales, _U8, 6, (shape[0], -(-shape[1] // 128)))):
+    for name, t, dtype, of in (("h", h, _BF16, shape), ("y", y, _BF16, shape), ("codes", codes, _U8, shape),
+                               ("scales", scales, _U8, (shape[0], -(-shape[1] // 128)))):
         if t is not None:
             _want_rows("into." + name, t, dtype, dev, of)
-            args[at:at + 2] = t.data_ptr(), t.stride(0)
-    return tuple(args)
+    return tuple(0 if t is None else t.stride(0) for t in into)
 
 
 def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -148,13 +155,17 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
             q = _empty8(T, H, 1, x.device) if outputs != "y" else (None, None)
             return Norm8(*q, None if residual is None else row(), None if outputs == "codes" else row())
         into = _made(stream, x.device, make)
-        into._args = _norm_into(into, want, x)
-        into._for = want
     elif not isinstance(into, Norm8):
         into = Norm8(*into)
-    args = into._args if into._for == want else _norm_into(into, want, x)
+    if into._for != want:
+        into._strides = _norm_into(into, want)
+        into._for = want
+    codes, scales, h, y = into
+    ld, lds, h_stride, y_stride = into._strides
     _call("moe_rms_norm8", B.lib().moe_rms_norm8(
-        x.data_ptr(), x.stride(0), r, r_stride, None if weight is None else weight.data_ptr(), eps, T, H, *args,
+        x.data_ptr(), x.stride(0), r, r_stride, None if weight is None else weight.data_ptr(), eps, T, H,
+        None if h is None else h.data_ptr(), h_stride, None if y is None else y.data_ptr(), y_stride,
+        None if codes is None else codes.data_ptr(), ld, None if scales is None else scales.data_ptr(), lds,
         _current(dev) if stream is None else B.handle(stream)))
     return into
 
@@ -178,14 +189,16 @@ def quantize8(x: torch.Tensor, silu_mul: bool = False, into: Block8 | None = Non
         into = Block8(*_made(stream, x.device, lambda: _empty8(T, K, 1, x.device)))
     elif not isinstance(into, Block8):
         into = Block8(*into)
+    codes, scales = into
     if into._for != want:
-        codes, scales = into
         _want_rows("into.codes", codes, _U8, dev, (T, K))
         _want_rows("into.scales", scales, _U8, dev, (T, -(-K // 128)))
-        into._args = (codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0))
+        into._strides = codes.stride(0), scales.stride(0)
         into._for = want
-    _call("moe_quantize8", B.lib().moe_quantize8(x.data_ptr(), x.stride(0), T, K, 1 if silu_mul else 0, *into._args,
-                                                 _current(dev) if stream is None else B.handle(stream)))
+    ld, lds = into._strides
+    _call("moe_quantize8", B.lib().moe_quantize8(
+        x.data_ptr(), x.stride(0), T, K, 1 if silu_mul else 0, codes.data_ptr(), ld, scales.data_ptr(), lds,
+        _current(dev) if stream is None else B.handle(stream)))
     return into
 
 
@@ -221,8 +234,17 @@ class Linear8:
             raise ValueError(f"codes: want {_U8}, got {codes.dtype}")
         if scales.dtype is not _U8 or scales.shape != of or scales.device != codes.device:
             raise ValueError(f"scales: want {_U8} {of} on {codes.device}, got {scales.dtype} {tuple(scales.shape)} on {scales.device}")
-        self.codes, self.scales = rows8(codes, scales)
-        self._w = (self.codes.data_ptr(), self.codes.stride(0), self.scales.data_ptr(), self.scales.stride(0))
+        if self.N > _INT_MAX or self.K > _INT_MAX:
+            raise ValueError(f"codes: want sizes of 31 bits, got {tuple(codes.shape)}")
+        self._codes, self._scales = rows8(codes, scales)
+        self._ld, self._lds = self._codes.stride(0), self._scales.stride(0)
+
+    # (not to be replaced: the calls know their strides)
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+
+    def __reduce__(self):
+        return type(self), (self._codes, self._scales)
 
     @classmethod
     def from_weight(cls, w: torch.Tensor) -> "Linear8":
@@ -233,9 +255,11 @@ class Linear8:
         """out bf16 [T, N] = A W^T of A in 8 bits (codes uint8 [T, K], scales uint8
         [T, ceil(K / 128)], as ``rms_norm8`` and ``quantize8`` give them)."""
         T, K, N, dev = codes.shape[0], self.K, self.N, self._dev
-        if not (_is_rows(codes, _U8, dev, (T, K)) and _is_rows(scales, _U8, dev, (T, self._blocks))):
+        if T > _INT_MAX or not (_is_rows(codes, _U8, dev, (T, K)) and _is_rows(scales, _U8, dev, (T, self._blocks))):
             _want_rows("codes", codes, _U8, dev, (T, K))
             _want_rows("scales", scales, _U8, dev, (T, self._blocks))
+            if T > _INT_MAX:
+                raise ValueError(f"codes: want sizes of 31 bits, got {tuple(codes.shape)}")
         if _device() != dev:
             with torch.cuda.device(dev):
                 return self.forward(codes, scales, out, stream)
@@ -244,7 +268,8 @@ class Linear8:
         elif not _is_rows(out, _BF16, dev, (T, N)):
             _want_rows("out", out, _BF16, dev, (T, N))
         _call("moe_linear8", B.lib().moe_linear8(
-            codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), *self._w, T, N, K,
+            codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), self._codes.data_ptr(), self._ld,
+            self._scales.data_ptr(), self._lds, T, N, K,
             out.data_ptr(), out.stride(0), _current(dev) if stream is None else B.handle(stream)))
         return out
 

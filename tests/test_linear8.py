@@ -13,6 +13,9 @@ The product's sums are in fp32: K / 32 additions of partial sums and 32 products
 to each, a step at most 2^-22 of the sum of magnitudes (a truncating adder that
 keeps 22 bits beside the largest), then bf16's half step 2^-8 of the result.
 """
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -141,6 +144,18 @@ def test_silu_mul_far_gates():
     got = lo.values(np8(codes), np8(scales))[0]
     assert got[0] == 0 and got[1] == 0 and got[7] == 0
     assert np.isnan(got[4:7]).all() and abs(got[3] / 2e4 - 1) < 2.0 ** -4 + 2.0 ** -8
+
+
+def test_silu_mul_small_products():
+    """Gates whose sigmoid is under the fp32 range, alone in their blocks and with ups that bring the product back into it:
+    exp twice of half the gate, 2 + 1.17 |gate| / 2 ulp each, and six for the quotient and products."""
+    g = torch.Generator("cuda").manual_seed(5)
+    gate = -60 - 60 * torch.rand(40, 640, generator=g, device="cuda")
+    up = torch.randn(40, 640, generator=g, device="cuda") * torch.exp2(torch.arange(40, device="cuda") * 3.0)[:, None]
+    x = torch.cat([gate, up], 1).bfloat16()
+    codes, scales = L8.quantize8(x, silu_mul=True)
+    assert int(codes.count_nonzero()) > 12000
+    assert_near_codes(codes, scales, lo.silu_mul(np64(x)), err=160 * 2.0 ** -23)
 
 
 # ---------------------------------------------------------------- the norm
@@ -378,6 +393,14 @@ def test_wrappers_refuse():
                 lambda: L8.Linear8(q.codes, q.scales), lambda: L8.Linear8(x, q.scales)):
         with pytest.raises(ValueError):
             bad()
+    many = x[:1, :16].expand(2 ** 32 + 1, 16)   # (a 32-bit count of its rows is one)
+    for bad in (lambda: L8.quantize8(many), lambda: L8.rms_norm8(many), lambda: L8.quantize8_weight(many),
+                lambda: lin(q.codes[:1].expand(2 ** 32 + 1, 256), q.scales[:1].expand(2 ** 32 + 1, 2), out=x),
+                lambda: L8.Linear8(q.codes[:1].expand(2 ** 32 + 1, 256), q.scales[:1].expand(2 ** 25 + 1, 2))):
+        with pytest.raises(ValueError, match="31 bits"):
+            bad()
+    with pytest.raises(AttributeError):
+        lin.codes = q.codes
     host = torch.empty(4, 40, dtype=torch.bfloat16)
     for bad in (lambda: L8.quantize8(x[:, :40]), lambda: L8.quantize8(x[:, 4:20]),
                 lambda: B.moe_linear8(q.codes, 256, q.scales, 4, lin.codes, 256, lin.scales, 4, 4, 40, 256, host, 40, None)):
@@ -386,6 +409,24 @@ def test_wrappers_refuse():
         assert e.value.code == -2
     assert L8.quantize8(x[:0]).codes.shape == (0, 256) and lin(*L8.quantize8(x[:0])).shape == (0, 40)
     assert L8.rms_norm8(x[:0], residual=x[:0], outputs="both").y.shape == (0, 256)
+
+
+@pytest.mark.parametrize("again", [copy.deepcopy, lambda o: pickle.loads(pickle.dumps(o))])
+def test_copies_are_matrices_of_their_own(again):
+    """A copy of results, or of a weight, has its own memory: written and read there, the original as it was."""
+    x, y = rows(5, 256, 0, 1), rows(5, 256, 0, 2)
+    lin = L8.Linear8(*L8.quantize8_weight(rows(40, 256, 0, 3)))
+    for make in (lambda x, into=None: L8.quantize8(x, into=into), lambda x, into=None: L8.rms_norm8(x, None, 1e-6, x, "both", into)):
+        q = make(x)
+        kept, other = [t.clone() for t in q], again(q)
+        assert type(other) is type(q) and all(torch.equal(t, u) for t, u in zip(q, other))
+        make(y, other)
+        assert all(torch.equal(t, u) for t, u in zip(q, kept)) and all(torch.equal(t, u) for t, u in zip(other, make(y)))
+    q, twin = L8.quantize8(x), again(lin)
+    want = lin(*q)
+    assert torch.equal(twin(*q), want)
+    lin.codes.zero_()
+    assert torch.equal(twin(*q), want) and not lin(*q).any()
 
 
 @pytest.mark.parametrize("T,N,K", [(3, 128, 4112), (3, 300, 8192), (3, 7400, 272), (20, 300, 2048), (40, 520, 1024), (300, 2048, 512),

@@ -99,6 +99,8 @@ LINEAR = dict(a=P, lda=256, a_scales=P, las=4, w=P, ldw=256, w_scales=P, lws=4, 
     ("moe_quantize8", ROWS, dict(T=2 ** 31 - 1), UNSUPPORTED),         # more blocks than are counted
     ("moe_quantize8_weight", WEIGHT, dict(N=65535 * 128 + 1), UNSUPPORTED),
     ("moe_quantize8_weight", WEIGHT, dict(K=8), UNSUPPORTED),
+    ("moe_quantize8_weight", WEIGHT, dict(K=2 ** 31 - 16, w_stride=2 ** 31, ld=2 ** 31, lds=2 ** 24), UNSUPPORTED),
+    ("moe_quantize8", ROWS, dict(K=2 ** 30, x_stride=2 ** 31, ld=2 ** 30, lds=2 ** 23), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(K=136), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(a=P + 8), UNSUPPORTED),
     ("moe_linear8", LINEAR, dict(ldw=264), UNSUPPORTED),
