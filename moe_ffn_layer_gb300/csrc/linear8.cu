@@ -10,12 +10,13 @@
 //
 // Bound: of 17 to 64 rows the latency of one pass (launch, a round trip to memory, the
 // exchange between CTAs: 4.5 us before any streaming) and then the weights' stream
-// (64 x 6144 x 4096 in 9.9 us, 2.6 TB/s); of more rows the operands' way from L2 and
-// the MMAs, which take 122 clocks each however narrow (777 x 2500 x 2000 in 10.9 us).
+// (64 x 6144 x 4096 in 8.7 us, 3.0 TB/s); of more rows the operands' way from L2 and
+// the MMAs, which take 122 clocks each however narrow (777 x 2500 x 2000 in 10.7 us).
 // What it took: copies started before the tensor memory is allocated and the next
 // launch set up meanwhile (1 x 4096 x 2048, which was computed here then, 6.7 -> 5.4 us); bulk
 // copies between the CTAs instead of single stores (64 x 6144 x 4096 12.2 -> 10.8);
-// MMAs issued by a whole warp that spins on its barriers (10.7 -> 9.9).
+// MMAs issued by a whole warp that spins on its barriers (10.7 -> 9.9); arrivals at the
+// cluster's barrier that order nothing by themselves (9.8 -> 8.6).
 #include <mutex>
 
 #include "linear8.cuh"
@@ -28,7 +29,8 @@ constexpr int kWideM = 128;   // weight rows of a tile
 
 template <int kNT>
 struct Cfg {
-  // accumulators that the MMAs of a block take in turn (16 x 512 x 8192 6.2 us, one 6.5; 64 x 6144 x 4096 10.0 and 9.9)
+  // accumulators that the MMAs of a block take in turn (16 x 512 x 8192 6.2 us, one 6.5; 64 x 6144 x 4096, with waits that
+  // took longer, 10.0 and 9.9)
   static constexpr int kChains = kNT <= 32 ? 4 : 1;
   // stages of the ring: so many that one CTA fills an SM, or two do
   static constexpr int kDeep = kNT == 16 ? 9 : kNT == 32 ? 8 : kNT == 64 ? 6 : 4;
@@ -412,7 +414,8 @@ bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows) {
 int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches) {
   // Tiles of 64 tokens while an SM each is enough for them, or, up to 24 blocks of K, half an SM (777 x 2500 x 2048
   // 10.0 us, of 128 tokens 10.9; 256 x 6144 x 4096 15.9 and 15.1); then of 128, then the pairs' tiles (512 x 6144 x
-  // 4096 26.5, 27.8 and 17.7; 1024 x 4096 x 2048 18.9, 19.7 and 11.8; 512 x 4096 x 2048 9.7, 10.3 and 11.1).
+  // 4096 26.5, 27.8 and 17.7; 1024 x 4096 x 2048 18.9, 19.7 and 11.8; 512 x 4096 x 2048 9.7, 10.3 and 11.1; 777 x 2500 x
+  // 2000 10.7 of 64 tokens and 12.4).
   const long long wide = (a.N + kWideM - 1) / kWideM, most = a.K <= 24 * kBlockK ? 2 * sms : sms;
   int rc;
   if (linear8_few_takes(a, sms)) rc = linear8_few_launch(a, sms, stream);
