@@ -82,24 +82,26 @@ def rows8(codes: torch.Tensor, scales: torch.Tensor) -> Block8:
     return Block8(codes, scales)
 
 
-def _is_rows(t, dtype, dev, shape):
-    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and (t.stride(1) == 1 or shape[1] == 1)
+def _rows(name, t, dtype, dev, shape):
+    """The stride of t's rows.  Raises ValueError unless t has that type, device and shape, its rows contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        apart, step = t.stride()
+        if step == 1 or shape[1] == 1:
+            return apart
+    raise ValueError(f"{name}: want {dtype} {tuple(shape)} with contiguous rows on device {dev}, got {t.dtype} "
+                     f"{tuple(t.shape)} of strides {tuple(t.stride())} on {t.device}")
 
 
-def _want_rows(name, t, dtype, dev, shape):
-    """Raises ValueError unless t has that type, device and shape, its rows contiguous."""
-    if t.dim() != 2 or not _is_rows(t, dtype, dev, shape):
-        raise ValueError(f"{name}: want {dtype} {tuple(shape)} with contiguous rows on device {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} of strides {tuple(t.stride())} on {t.device}")
-
-
-def _want_input(name, x):
-    """Raises ValueError unless x is a bf16 matrix with contiguous rows on a CUDA device, of sizes that the C calls take."""
-    if x.dtype is not _BF16 or x.dim() != 2 or not x.is_cuda or (x.stride(1) != 1 and x.shape[1] > 1):
+def _input(name, x):
+    """Shape, device and stride of the rows of x.  Raises ValueError unless x is a bf16 matrix with contiguous rows on a
+    CUDA device, of sizes that the C calls take."""
+    shape, dev, strides = x.shape, x.get_device(), x.stride()
+    if x.dtype is not _BF16 or len(shape) != 2 or dev < 0 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}: want 2-d {_BF16} with contiguous rows on a CUDA device, got {x.dim()}-d {x.dtype} of "
-                         f"strides {tuple(x.stride())} on {x.device}")
-    if x.shape[0] > _INT_MAX or x.shape[1] > _INT_MAX:
-        raise ValueError(f"{name}: want sizes of 31 bits, got {tuple(x.shape)}")
+                         f"strides {tuple(strides)} on {x.device}")
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:
+        raise ValueError(f"{name}: want sizes of 31 bits, got {tuple(shape)}")
+    return shape, dev, strides[0]
 
 
 def _made(stream, device, make):
@@ -116,11 +118,9 @@ def _norm_into(into, want):
     codes, scales, h, y = into
     if (codes is None) != (outputs == "y") or (y is None) != (outputs == "codes") or (h is None) != plain:
         raise ValueError(f"into: not the results of a call with outputs={outputs!r} and {'no' if plain else 'a'} residual")
-    for name, t, dtype, of in (("h", h, _BF16, shape), ("y", y, _BF16, shape), ("codes", codes, _U8, shape),
-                               ("scales", scales, _U8, (shape[0], -(-shape[1] // 128)))):
-        if t is not None:
-            _want_rows("into." + name, t, dtype, dev, of)
-    return tuple(0 if t is None else t.stride(0) for t in into)
+    return tuple(0 if t is None else _rows("into." + name, t, dtype, dev, of) for name, t, dtype, of in (
+        ("codes", codes, _U8, shape), ("scales", scales, _U8, (shape[0], -(-shape[1] // 128))), ("h", h, _BF16, shape),
+        ("y", y, _BF16, shape)))
 
 
 def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -131,8 +131,7 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
     `into` takes the results of an earlier call of the same sizes, or a Norm8 of
     other tensors; its h may be x or residual themselves.  Without a residual, h is
     None (it would be x)."""
-    _want_input("x", x)
-    shape, dev = x.shape, x.get_device()
+    shape, dev, stride = _input("x", x)
     if _device() != dev:   # (the library works on the current device)
         with torch.cuda.device(dev):
             return rms_norm8(x, weight, eps, residual, outputs, into, stream)
@@ -140,9 +139,8 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
     if residual is None:
         r, r_stride = None, 0
     else:
-        if not _is_rows(residual, _BF16, dev, shape):
-            _want_rows("residual", residual, _BF16, dev, shape)
-        r, r_stride = residual.data_ptr(), residual.stride(0)
+        r_stride = _rows("residual", residual, _BF16, dev, shape)
+        r = residual.data_ptr()
     if weight is not None and (weight.dtype is not _BF16 or weight.shape != shape[1:] or weight.get_device() != dev or
                                not weight.is_contiguous()):
         raise ValueError(f"weight: want contiguous {_BF16} ({H},) on {x.device}, got {weight.dtype} {tuple(weight.shape)} on {weight.device}")
@@ -163,7 +161,7 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
     codes, scales, h, y = into
     ld, lds, h_stride, y_stride = into._strides
     _call("moe_rms_norm8", B.lib().moe_rms_norm8(
-        x.data_ptr(), x.stride(0), r, r_stride, None if weight is None else weight.data_ptr(), eps, T, H,
+        x.data_ptr(), stride, r, r_stride, None if weight is None else weight.data_ptr(), eps, T, H,
         None if h is None else h.data_ptr(), h_stride, None if y is None else y.data_ptr(), y_stride,
         None if codes is None else codes.data_ptr(), ld, None if scales is None else scales.data_ptr(), lds,
         _current(dev) if stream is None else B.handle(stream)))
@@ -174,12 +172,10 @@ def quantize8(x: torch.Tensor, silu_mul: bool = False, into: Block8 | None = Non
     """The rows of x (bf16 [T, K], any multiple of 8 elements apart) in 8 bits;
     silu_mul: of SiLU(x[:, :K]) * x[:, K:], x bf16 [T, 2K].  `into` takes the
     results of an earlier call of the same sizes, or a Block8 of other tensors."""
-    _want_input("x", x)
-    dev = x.get_device()
+    (T, K), dev, stride = _input("x", x)
     if _device() != dev:
         with torch.cuda.device(dev):
             return quantize8(x, silu_mul, into, stream)
-    T, K = x.shape
     if silu_mul:
         if K % 2:
             raise ValueError(f"x: want an even number of columns (gate, up), got {K}")
@@ -191,13 +187,12 @@ def quantize8(x: torch.Tensor, silu_mul: bool = False, into: Block8 | None = Non
         into = Block8(*into)
     codes, scales = into
     if into._for != want:
-        _want_rows("into.codes", codes, _U8, dev, (T, K))
-        _want_rows("into.scales", scales, _U8, dev, (T, -(-K // 128)))
-        into._strides = codes.stride(0), scales.stride(0)
+        into._strides = (_rows("into.codes", codes, _U8, dev, (T, K)),
+                         _rows("into.scales", scales, _U8, dev, (T, -(-K // 128))))
         into._for = want
     ld, lds = into._strides
     _call("moe_quantize8", B.lib().moe_quantize8(
-        x.data_ptr(), x.stride(0), T, K, 1 if silu_mul else 0, codes.data_ptr(), ld, scales.data_ptr(), lds,
+        x.data_ptr(), stride, T, K, 1 if silu_mul else 0, codes.data_ptr(), ld, scales.data_ptr(), lds,
         _current(dev) if stream is None else B.handle(stream)))
     return into
 
@@ -205,16 +200,14 @@ def quantize8(x: torch.Tensor, silu_mul: bool = False, into: Block8 | None = Non
 def quantize8_weight(w: torch.Tensor, stream=None) -> Block8:
     """A weight bf16 [N, K] (rows any multiple of 8 elements apart) in 8 bits, with
     a scale per block of 128 x 128."""
-    _want_input("w", w)
-    N, K = w.shape
-    dev = w.get_device()
+    (N, K), dev, stride = _input("w", w)
     if _device() != dev:
         with torch.cuda.device(dev):
             return quantize8_weight(w, stream)
     device = w.device
     codes, scales = _empty8(N, K, 128, device) if stream is None else _made(stream, device, lambda: _empty8(N, K, 128, device))
     _call("moe_quantize8_weight", B.lib().moe_quantize8_weight(
-        w.data_ptr(), w.stride(0), N, K, codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0),
+        w.data_ptr(), stride, N, K, codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0),
         _current(dev) if stream is None else B.handle(stream)))
     return Block8(codes, scales)
 
@@ -255,22 +248,20 @@ class Linear8:
         """out bf16 [T, N] = A W^T of A in 8 bits (codes uint8 [T, K], scales uint8
         [T, ceil(K / 128)], as ``rms_norm8`` and ``quantize8`` give them)."""
         T, K, N, dev = codes.shape[0], self.K, self.N, self._dev
-        if T > _INT_MAX or not (_is_rows(codes, _U8, dev, (T, K)) and _is_rows(scales, _U8, dev, (T, self._blocks))):
-            _want_rows("codes", codes, _U8, dev, (T, K))
-            _want_rows("scales", scales, _U8, dev, (T, self._blocks))
-            if T > _INT_MAX:
-                raise ValueError(f"codes: want sizes of 31 bits, got {tuple(codes.shape)}")
+        if T > _INT_MAX:
+            raise ValueError(f"codes: want sizes of 31 bits, got {tuple(codes.shape)}")
+        ld, lds = _rows("codes", codes, _U8, dev, (T, K)), _rows("scales", scales, _U8, dev, (T, self._blocks))
         if _device() != dev:
             with torch.cuda.device(dev):
                 return self.forward(codes, scales, out, stream)
         if out is None:
-            out = _made(stream, self.device, lambda: torch.empty((T, N), dtype=_BF16, device=self.device))
-        elif not _is_rows(out, _BF16, dev, (T, N)):
-            _want_rows("out", out, _BF16, dev, (T, N))
+            out, out_stride = _made(stream, self.device, lambda: torch.empty((T, N), dtype=_BF16, device=self.device)), N
+        else:
+            out_stride = _rows("out", out, _BF16, dev, (T, N))
         _call("moe_linear8", B.lib().moe_linear8(
-            codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), self._codes.data_ptr(), self._ld,
+            codes.data_ptr(), ld, scales.data_ptr(), lds, self._codes.data_ptr(), self._ld,
             self._scales.data_ptr(), self._lds, T, N, K,
-            out.data_ptr(), out.stride(0), _current(dev) if stream is None else B.handle(stream)))
+            out.data_ptr(), out_stride, _current(dev) if stream is None else B.handle(stream)))
         return out
 
     __call__ = forward
