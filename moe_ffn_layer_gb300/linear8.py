@@ -23,39 +23,23 @@ from .kv_cache import _call, _current, _device
 
 
 # The calls are a few microseconds of kernels at decode sizes, and the host has to
-# keep ahead of them: the checks are a few comparisons a tensor, and results that
-# a call made itself are known by what they were made for when they come back as `into`
-# (copies, and what is loaded from a file, are checked again: `__reduce__`).
+# keep ahead of them: the checks are a few comparisons a tensor.  They are made of every
+# tensor of every call, of results given back and of weights too, since any tensor may
+# have been changed in place (set_, resize_, .data) since the last one.
 
 
-class _Block8(NamedTuple):
+class Block8(NamedTuple):
+    """A matrix in 8 bits: codes, scales."""
     codes: torch.Tensor
     scales: torch.Tensor
 
 
-class Block8(_Block8):
-    """A matrix in 8 bits: codes, scales."""
-    _for = None         # what they were made for
-    _strides = (0, 0)
-
-    def __reduce__(self):
-        return type(self), tuple(self)
-
-
-class _Norm8(NamedTuple):
+class Norm8(NamedTuple):
+    """What ``rms_norm8`` gives: codes, scales, h, y; None for what was not asked for."""
     codes: torch.Tensor | None
     scales: torch.Tensor | None
     h: torch.Tensor | None
     y: torch.Tensor | None
-
-
-class Norm8(_Norm8):
-    """What ``rms_norm8`` gives: codes, scales, h, y; None for what was not asked for."""
-    _for = None
-    _strides = (0, 0, 0, 0)
-
-    def __reduce__(self):
-        return type(self), tuple(self)
 
 
 _BF16, _U8, _INT_MAX = torch.bfloat16, torch.uint8, 2 ** 31 - 1
@@ -112,17 +96,6 @@ def _made(stream, device, make):
         return make()
 
 
-def _norm_into(into, want):
-    """Checks results that are to be written, and gives their rows' strides."""
-    shape, dev, outputs, plain = want
-    codes, scales, h, y = into
-    if (codes is None) != (outputs == "y") or (y is None) != (outputs == "codes") or (h is None) != plain:
-        raise ValueError(f"into: not the results of a call with outputs={outputs!r} and {'no' if plain else 'a'} residual")
-    return tuple(0 if t is None else _rows("into." + name, t, dtype, dev, of) for name, t, dtype, of in (
-        ("codes", codes, _U8, shape), ("scales", scales, _U8, (shape[0], -(-shape[1] // 128))), ("h", h, _BF16, shape),
-        ("y", y, _BF16, shape)))
-
-
 def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6, residual: torch.Tensor | None = None,
               outputs: str = "codes", into: Norm8 | None = None, stream=None) -> Norm8:
     """h = x + residual (bf16), y = RMS norm of h's rows times weight.  x and
@@ -146,7 +119,6 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
         raise ValueError(f"weight: want contiguous {_BF16} ({H},) on {x.device}, got {weight.dtype} {tuple(weight.shape)} on {weight.device}")
     if outputs not in ("codes", "y", "both"):
         raise ValueError(f"outputs: want 'codes', 'y' or 'both', got {outputs!r}")
-    want = (shape, dev, outputs, r is None)
     if into is None:
         def make():
             row = lambda: torch.empty(shape, dtype=_BF16, device=x.device)  # noqa: E731
@@ -155,11 +127,14 @@ def rms_norm8(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 
         into = _made(stream, x.device, make)
     elif not isinstance(into, Norm8):
         into = Norm8(*into)
-    if into._for != want:
-        into._strides = _norm_into(into, want)
-        into._for = want
     codes, scales, h, y = into
-    ld, lds, h_stride, y_stride = into._strides
+    no8 = outputs == "y"
+    if (codes is None) != no8 or (scales is None) != no8 or (y is None) != (outputs == "codes") or (h is None) != (r is None):
+        raise ValueError(f"into: not the results of a call with outputs={outputs!r} and {'no' if r is None else 'a'} residual")
+    ld = 0 if no8 else _rows("into.codes", codes, _U8, dev, shape)
+    lds = 0 if no8 else _rows("into.scales", scales, _U8, dev, (T, -(-H // 128)))
+    h_stride = 0 if h is None else _rows("into.h", h, _BF16, dev, shape)
+    y_stride = 0 if y is None else _rows("into.y", y, _BF16, dev, shape)
     _call("moe_rms_norm8", B.lib().moe_rms_norm8(
         x.data_ptr(), stride, r, r_stride, None if weight is None else weight.data_ptr(), eps, T, H,
         None if h is None else h.data_ptr(), h_stride, None if y is None else y.data_ptr(), y_stride,
@@ -180,17 +155,13 @@ def quantize8(x: torch.Tensor, silu_mul: bool = False, into: Block8 | None = Non
         if K % 2:
             raise ValueError(f"x: want an even number of columns (gate, up), got {K}")
         K //= 2
-    want = (T, K, dev)
     if into is None:
         into = Block8(*_made(stream, x.device, lambda: _empty8(T, K, 1, x.device)))
     elif not isinstance(into, Block8):
         into = Block8(*into)
     codes, scales = into
-    if into._for != want:
-        into._strides = (_rows("into.codes", codes, _U8, dev, (T, K)),
-                         _rows("into.scales", scales, _U8, dev, (T, -(-K // 128))))
-        into._for = want
-    ld, lds = into._strides
+    ld = _rows("into.codes", codes, _U8, dev, (T, K))
+    lds = _rows("into.scales", scales, _U8, dev, (T, -(-K // 128)))
     _call("moe_quantize8", B.lib().moe_quantize8(
         x.data_ptr(), stride, T, K, 1 if silu_mul else 0, codes.data_ptr(), ld, scales.data_ptr(), lds,
         _current(dev) if stream is None else B.handle(stream)))
@@ -221,8 +192,7 @@ class Linear8:
             raise ValueError(f"codes: want 2-d on a CUDA device, got {codes.dim()}-d on {codes.device}")
         self.N, self.K = codes.shape
         self.device, self._dev = codes.device, codes.get_device()
-        self._blocks = -(-self.K // 128)
-        of = (-(-self.N // 128), self._blocks)
+        self._of = of = (-(-self.N // 128), -(-self.K // 128))
         if codes.dtype is not _U8:
             raise ValueError(f"codes: want {_U8}, got {codes.dtype}")
         if scales.dtype is not _U8 or scales.shape != of or scales.device != codes.device:
@@ -230,9 +200,7 @@ class Linear8:
         if self.N > _INT_MAX or self.K > _INT_MAX:
             raise ValueError(f"codes: want sizes of 31 bits, got {tuple(codes.shape)}")
         self._codes, self._scales = rows8(codes, scales)
-        self._ld, self._lds = self._codes.stride(0), self._scales.stride(0)
 
-    # (not to be replaced: the calls know their strides)
     codes = property(lambda self: self._codes)
     scales = property(lambda self: self._scales)
 
@@ -250,7 +218,9 @@ class Linear8:
         T, K, N, dev = codes.shape[0], self.K, self.N, self._dev
         if T > _INT_MAX:
             raise ValueError(f"codes: want sizes of 31 bits, got {tuple(codes.shape)}")
-        ld, lds = _rows("codes", codes, _U8, dev, (T, K)), _rows("scales", scales, _U8, dev, (T, self._blocks))
+        ld, lds = _rows("codes", codes, _U8, dev, (T, K)), _rows("scales", scales, _U8, dev, (T, self._of[1]))
+        w, ws = self._codes, self._scales
+        ldw, lws = _rows("weight's codes", w, _U8, dev, (N, K)), _rows("weight's scales", ws, _U8, dev, self._of)
         if _device() != dev:
             with torch.cuda.device(dev):
                 return self.forward(codes, scales, out, stream)
@@ -259,8 +229,7 @@ class Linear8:
         else:
             out_stride = _rows("out", out, _BF16, dev, (T, N))
         _call("moe_linear8", B.lib().moe_linear8(
-            codes.data_ptr(), ld, scales.data_ptr(), lds, self._codes.data_ptr(), self._ld,
-            self._scales.data_ptr(), self._lds, T, N, K,
+            codes.data_ptr(), ld, scales.data_ptr(), lds, w.data_ptr(), ldw, ws.data_ptr(), lws, T, N, K,
             out.data_ptr(), out_stride, _current(dev) if stream is None else B.handle(stream)))
         return out
 
