@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
     int stage = 0, slot = 0, tile_no = 0;
     uint32_t phase = 0, sf_phase = 0;
     bool ok = true;
+    chain_wait();   // (it touches no memory of the launch before, but its waits are not to count, or spin through, that one's time)
     for (int tile = blockIdx.x >> 1; tile < tiles && ok; tile += step, ++tile_no) {
       for (int kb = 0; kb < blocks; ++kb) {
         const uint32_t sfa = tmem + C::kSfBase + slot * C::kSlotCols, sfb = sfa + kAcc * kSfCols;
