@@ -147,7 +147,7 @@ __device__ __forceinline__ uint4 scale_words_of_rows(const uint8_t* scales, long
 // box_rows in the 128-byte swizzle; what lies outside reads as 0.
 bool linear8_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
 
-// The output in boxes of 32 columns x box_rows (64-byte swizzle); what lies outside is not written.
+// The output in boxes of 32 columns x box_rows (64-byte swizzle), N a multiple of 8; what lies outside is not written.
 bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows);
 
 // Up to 16 rows, of the sizes that it takes: a stream of the weights.

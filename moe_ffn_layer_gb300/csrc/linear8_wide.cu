@@ -442,8 +442,9 @@ int launch_wide(const Linear8& a, int* status, cudaStream_t stream) {
   if (tiles > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   CUtensorMap ma, mw, mo = {};
   if (!linear8_map(&ma, a.a, a.T, a.K, a.lda, kRows / 2) || !linear8_map(&mw, a.w, a.N, a.K, a.ldw, kBN / 2)) return MOE_ERR_CUDA;
-  // by TMA where the rows lie as it takes them
-  const bool tma_out = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && (a.T == 1 || a.ldo % 8 == 0);
+  // by TMA where the rows lie as it takes them, and are whole vectors of 16 bytes: it writes such a vector whole where
+  // a row ends inside it
+  const bool tma_out = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && a.N % 8 == 0 && (a.T == 1 || a.ldo % 8 == 0);
   if (tma_out && !linear8_out_map(&mo, a, 32)) return MOE_ERR_CUDA;
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
   return launch_chained_cluster(linear8_wide_kernel<kBN, kAcc>, dim3(grid), dim3(kThreads), C::kSmem, stream, 2, ma, mw, mo, a,
