@@ -369,7 +369,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear8_wide_kernel(const __grid_
       uint32_t v[kCols / 2];
 #pragma unroll
       for (int c = 0; c < kCols; c += 32) {
-        if (c >= cols) break;
+        if (c >= cols) {   // (the second group's part is smaller; store_rows moves all of v)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[c / 2 + i] = 0u;
+          continue;
+        }
         uint32_t r[32];
         tmem_ld_32cols(acc + c, r);
         tmem_ld_wait();
