@@ -409,7 +409,7 @@ MOE_API int moe_rms_norm8(const void* x, int64_t x_stride, const void* residual,
 
 /* Rows in 8 bits.
  *   act == 0: of x[t][0..K-1]
- *   act == 1: of SiLU(x[t][0..K-1]) * x[t][K..2K-1], computed in fp32
+ *   act == 1: of SiLU(x[t][0..K-1]) * x[t][K..2K-1], computed in fp32 to within 20 * 2^-24 of its value
  *  x bf16 [T], rows x_stride elements apart; must not overlap codes or scales */
 MOE_API int moe_quantize8(const void* x, int64_t x_stride, int T, int K, int act, void* codes, int64_t ld, void* scales,
                           int64_t lds, cudaStream_t stream);
