@@ -228,6 +228,8 @@ class Linear8:
             out, out_stride = _made(stream, self.device, lambda: torch.empty((T, N), dtype=_BF16, device=self.device)), N
         else:
             out_stride = _rows("out", out, _BF16, dev, (T, N))
+        if N == 0:   # (a weight of no rows: the C call wants one)
+            return out
         _call("moe_linear8", B.lib().moe_linear8(
             codes.data_ptr(), ld, scales.data_ptr(), lds, w.data_ptr(), ldw, ws.data_ptr(), lws, T, N, K,
             out.data_ptr(), out_stride, _current(dev) if stream is None else B.handle(stream)))
