@@ -68,6 +68,8 @@ class DecoderLayer:
     def __init__(self, w_qkv, w_o, ffn: MoEFFN, cache: KVCache8, heads: int):
         self.w_qkv, self.w_o, self.ffn, self.cache, self.heads = w_qkv, w_o, ffn, cache, heads
 
+    hidden = property(lambda self: self.w_o.shape[0])
+
     def linear(self, x, w):
         out = torch.empty(x.shape[0], w.shape[0], dtype=torch.bfloat16, device=x.device)
         B.moe_grouped_gemm(x, w, None, 1, x.shape[0], w.shape[0], w.shape[1], 0, out, None, 0,
@@ -87,8 +89,10 @@ class DecoderLayer8(DecoderLayer):
     """The layer with its projections in 8 bits."""
 
     def __init__(self, w_qkv, w_o, ffn: MoEFFN, cache: KVCache8, heads: int):
-        super().__init__(w_qkv, w_o, ffn, cache, heads)
+        super().__init__(None, None, ffn, cache, heads)   # (the bf16 weights are not kept)
         self.qkv, self.o = Linear8.from_weight(w_qkv), Linear8.from_weight(w_o)
+
+    hidden = property(lambda self: self.o.N)
 
     def __call__(self, x, table, lens, cu, max_new, max_len, weights=None):
         Hq, Hkv, D = self.heads, self.cache.kv_heads, self.cache.head_dim
@@ -113,7 +117,7 @@ def serve(layer, prompts, steps, limit, budget, sink=4, recent=16, seed=1):
     """Runs the prompts (lengths), then `steps` single tokens of each sequence.
     Returns (last outputs [B, H], lengths, evictions)."""
     n, page, dev = len(prompts), layer.cache.page, layer.cache.device
-    H = layer.w_o.shape[0]
+    H = layer.hidden
     g = torch.Generator(dev).manual_seed(seed)
     # room for every sequence at its limit, and for the pages an eviction writes beside it
     pages = Pages(n, -(-limit // page), layer.cache.num_pages, dev)
