@@ -423,9 +423,12 @@ MOE_API int moe_quantize8_weight(const void* w, int64_t w_stride, int N, int K, 
  *  a [T][K] with a scale per row and 128 values (las bytes between its rows)
  *  w [N][K] with a scale per 128 x 128 (lws bytes between its rows)
  *  out bf16, rows out_stride elements apart; any N
- * Products are exact and summed in fp32; a NaN code or scale makes what it
- * reaches NaN.  a, w and out must be device memory of the current device.
- * Results do not depend on scheduling. */
+ * Products are exact and summed in fp32 accumulators, in which an addition of the
+ * tensor cores may drop what lies under 2^-22 of the larger part: before its
+ * rounding to bf16 a result is within (K / 32 + 32) 2^-22 of the sum of its
+ * products' magnitudes.  A NaN code or scale makes what it reaches NaN.  a, w and
+ * out must be device memory of the current device.  Results do not depend on
+ * scheduling. */
 MOE_API int moe_linear8(const void* a, int64_t lda, const void* a_scales, int64_t las, const void* w, int64_t ldw,
                         const void* w_scales, int64_t lws, int T, int N, int K, void* out, int64_t out_stride,
                         cudaStream_t stream);

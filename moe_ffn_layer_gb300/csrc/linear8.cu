@@ -10,8 +10,10 @@
 //
 // Bound: of 17 to 64 rows the latency of one pass (launch, a round trip to memory, the
 // exchange between CTAs: 4.5 us before any streaming) and then the weights' stream
-// (64 x 6144 x 4096 in 8.7 us, 3.0 TB/s); of more rows the operands' way from L2 and
-// the MMAs, which take 122 clocks each however narrow (777 x 2500 x 2000 in 10.7 us).
+// (64 x 6144 x 4096 in 8.5 us, 3.1 TB/s); of more rows the operands' way from L2 and
+// the MMAs, which take 122 clocks each however narrow (777 x 2500 x 2000 in 10.8 us).
+// Times are of replayed graphs over several sets of operands, together more than L2 holds; over one set, which L2
+// holds, 64 x 6144 x 4096 takes 7.9 us and 777 x 2500 x 2000 9.9.
 // What it took: copies started before the tensor memory is allocated and the next
 // launch set up meanwhile (1 x 4096 x 2048, which was computed here then, 6.7 -> 5.4 us); bulk
 // copies between the CTAs instead of single stores (64 x 6144 x 4096 12.2 -> 10.8);
@@ -412,10 +414,12 @@ bool linear8_out_map(CUtensorMap* m, const Linear8& a, uint32_t box_rows) {
 }
 
 int linear8_launch(const Linear8& a, int* status, int sms, cudaStream_t stream, int* launches) {
-  // Tiles of 64 tokens while an SM each is enough for them, or, up to 24 blocks of K, half an SM (777 x 2500 x 2048
-  // 10.0 us, of 128 tokens 10.9; 256 x 6144 x 4096 15.9 and 15.1); then of 128, then the pairs' tiles (512 x 6144 x
-  // 4096 26.5, 27.8 and 17.7; 1024 x 4096 x 2048 18.9, 19.7 and 11.8; 512 x 4096 x 2048 9.7, 10.3 and 11.1; 777 x 2500 x
-  // 2000 10.7 of 64 tokens and 12.4).
+  // Tiles of 64 tokens while an SM each is enough for them, or, up to 24 blocks of K, half an SM.  By blocks of K (16, 22,
+  // 24, 26, 32), tiles of 64 tokens and of 128: 256 x 6144 10.3, 12.8, 13.3, 14.3, 16.0 and 10.7, 12.9, 13.1, 14.2, 15.4 us;
+  // 512 x 4096 10.0, 12.6, 13.0, 13.8, 15.4 and 10.5, 12.8, 12.9, 13.9, 15.1; 300 x 6144 10.2, 12.8, 13.1, 14.2, 15.9 and
+  // 10.7, 12.9, 13.2, 14.1, 15.5; 777 x 2500, whose last tiles are less full, 10.3, 12.7, 13.1, 14.0, 15.5 and 11.3, 13.5,
+  // 13.6, 14.6, 15.9.  Then of 128, then the pairs' tiles (512 x 6144 x 4096 26.5, 27.8 and 17.7; 1024 x 4096 x 2048 18.9,
+  // 19.7 and 11.8; of the sizes above the pairs' take 1.2 to 4.5 us longer than the better of the others).
   const long long wide = (a.N + kWideM - 1) / kWideM, most = a.K <= 24 * kBlockK ? 2 * sms : sms;
   int rc;
   if (linear8_few_takes(a, sms)) rc = linear8_few_launch(a, sms, stream);

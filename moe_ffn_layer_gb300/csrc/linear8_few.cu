@@ -133,10 +133,12 @@ __global__ void __launch_bounds__(kThreads, kBatch == 1 ? 3 : 2) linear8_few_ker
 
 }  // namespace
 
-// Where it is the faster one (the tensor-memory kernel's time in parentheses).  Up to 8 rows while the CTAs fit at once,
-// three an SM, and a warp has four blocks of K at most: 1 x 2048 x 2048 2.4 (4.1) us, 1 x 4096 x 2048 3.2 (4.9),
-// 8 x 7296 x 4096 7.1 (8.2), but 1 x 8192 x 8192 20.7 (14.7) and 1 x 16384 x 4096 16.9 (14.0).  Up to 16 rows with two an SM
-// and two blocks: 16 x 4096 x 2048 3.9 (5.0), but 16 x 7296 x 2048 6.4 (6.1) and 16 x 4096 x 4096 7.6 (6.4).
+// Where it is the faster one (the tensor-memory kernel's time in parentheses; replays over several sets of operands, more
+// than L2 holds).  Up to 8 rows while the CTAs fit at once, three an SM, and a warp has four blocks of K at most:
+// 1 x 2048 x 2048 2.3 (4.0) us, 1 x 4096 x 2048 3.2 (4.9), 8 x 7296 x 4096 6.9 (8.0), but 1 x 8192 x 8192 17.2 (12.7),
+// 1 x 16384 x 4096 14.8 (12.8) and 1 x 8192 x 4096 9.7 (8.2).  Up to 16 rows with two an SM and two blocks: 16 x 4096 x 2048
+// 3.9 (5.1), 16 x 4864 x 2048 4.0 (5.3), but 16 x 7296 x 2048 6.4 (6.0).  (With more blocks it would still be the faster one at
+// 16 x 4096 x 4096, 6.0 (6.4).)
 bool linear8_few_takes(const Linear8& a, int sms) {
   const int ctas = (a.N + kRows - 1) / kRows;
   return a.T <= 8 ? a.K <= 4 * kWarps * kBlockK && ctas <= 3 * sms : a.T <= 16 && a.K <= 2 * kWarps * kBlockK && ctas <= 2 * sms;

@@ -11,7 +11,8 @@
 // it, the MMAs without copies 264), and then the power cap: run back to back the
 // clock settles at 1.45 GHz and a call at 368 us.  A tile has 512 tokens where that
 // many fill the pairs, since it then moves (512 + 224) rows a block of K instead of
-// 2 (256 + 224) for the same products.
+// 2 (256 + 224) for the same products.  (Its kernel spills 28 bytes: an epilogue thread
+// holds 112 packed pairs beside the 32 columns that it reads.)
 // What it took (16384 x 8192 x 4096): pairs instead of single CTAs 997 -> 408 us; the
 // MMA warp run whole, descriptors in uniform registers -> 356; two accumulators of a
 // 512-token tile -> 327; copies issued by a whole warp, the accumulators in turn

@@ -73,10 +73,14 @@ constexpr int kMaxNormWarps = 32;
 // h = bf16(x + r); y = h rsqrt(mean h^2 + eps) w.  A CTA per row; thread i has
 // the row's vectors i, i + blockDim, ... in registers, so that x and r are read
 // once.  The sum of squares is held in fp32; y is rounded once, to e4m3 or bf16.
-// Bound: memory (7 bytes a value with a residual and codes): 8192 x 4096 in 35.3 us,
-// 6.65 TB/s; one row of 2048 is latency, 1.8 us.  About two vectors a thread and
+// Bound: memory (7 bytes a value with a residual and codes): 8192 x 4096 in 34.8 us,
+// 6.75 TB/s; one row of 2048 is latency, 1.4 us.  About two vectors a thread and
 // 256 threads: with one vector and 512 threads 8192 x 4096 takes 40 us, with four
 // and 128 threads 36 and 4096 x 8192 63 instead of 36 (too few loads in flight).
+// Rows of more than 8192 values (many rows) or 16384 have eight vectors a thread, of which 84
+// bytes are spilled at the 64 registers that 1024 threads leave: 2048 x 16384 takes 48 us.
+// Of short rows the CTAs' launches are the bound, 1.0 ns a row: 65536 x 512 takes 66 us,
+// 262144 x 128 262.
 template <int kVecs>
 __global__ void __launch_bounds__(1024) rms_norm8_kernel(Norm8 a) {
   chain_wait();
@@ -184,8 +188,8 @@ constexpr uint32_t kQuantizeMany = 1u << 16;   // blocks of 128: from here on se
 
 // 16 lanes a block of 128; blocks are numbered along the rows.  A thread has
 // kPer blocks' vectors in flight at once.  Bound: memory (3 bytes a value, 5 with
-// SiLU): 16384 x 4096 in 31.5 us, 6.4 TB/s (one block a thread 39.6, two 33.0, eight
-// 40.3: registers), with SiLU in 57.6 us, 5.8 TB/s (two 59.8).
+// SiLU): 16384 x 4096 in 31.1 us, 6.5 TB/s (one block a thread 39.6, two 33.0, eight
+// 40.3: registers), with SiLU in 59.8 us, 5.6 TB/s (before its exponent came in two parts 57.6, with two blocks 59.8).
 template <int kAct, int kPer>
 __global__ void __launch_bounds__(kQuantizeThreads) quantize8_kernel(Quantize8 a, uint32_t blocks_per_row, uint32_t blocks) {
   chain_wait();
@@ -224,7 +228,8 @@ __global__ void __launch_bounds__(kQuantizeThreads) quantize8_kernel(Quantize8 a
 
 // ---------------------------------------------------------------- weights
 // A CTA per block of 128 x 128: 16 lanes a row, eight rows a thread, kept packed between the maximum and the
-// rounding so that four CTAs fit an SM (8192 x 4096 in 16.9 us, 6.0 TB/s; three CTAs 19.7).
+// rounding so that four CTAs fit an SM (8192 x 4096 in 16.9 us, 5.9 TB/s; three CTAs 19.7), though 52 bytes a
+// thread are spilled at the 64 registers that this leaves.
 __global__ void __launch_bounds__(256, 4) quantize8_weight_kernel(Quantize8 a, int N) {
   chain_wait();
   chain_release();
